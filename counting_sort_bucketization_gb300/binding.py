@@ -53,6 +53,20 @@ class _CDesc(ctypes.Structure):
                 ("num_ranks", ctypes.c_int32), ("alignment", ctypes.c_int32)]
 
 
+@dataclasses.dataclass(frozen=True)
+class GateConfig:
+    """Settings of the top-k gate (moe_gate_desc; the logits' type comes from the tensor)."""
+    score: str = "softmax"         # "softmax" over the experts or "sigmoid"
+    normalize: bool = True         # a token's weights sum to ``scale``
+    scale: float = 1.0
+    balance_coef: float = 0.0      # factor of the balance loss
+
+
+class _CGateDesc(ctypes.Structure):
+    _fields_ = [("logits_bf16", ctypes.c_int32), ("sigmoid", ctypes.c_int32), ("normalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("balance_coef", ctypes.c_float)]
+
+
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
 
@@ -88,6 +102,16 @@ def load_library() -> ctypes.CDLL:
         lib.moe_dispatch_permute_ranks.argtypes = [dp, p, i64, p, i64, p, p, p, p, i64, p, sz, p]
         lib.moe_combine_unpermute.argtypes = [dp, p, i64, i64, p, p, p, p, sz, p]
         lib.moe_dispatch_sf_col_major.argtypes = [dp, p, i64, p, p, p, i64, i64, ctypes.c_int, p, sz, p]
+        gp, ci = ctypes.POINTER(_CGateDesc), ctypes.c_int
+        lib.moe_gate_workspace_bytes.argtypes = [dp, ctypes.POINTER(ctypes.c_size_t)]
+        lib.moe_gate_forward.argtypes = [dp, gp, p, i64, p, p, p, p, p, p, p, p, sz, p]
+        lib.moe_gate_backward.argtypes = [dp, gp, p, i64, p, p, p, p, p, p, i64, p, sz, p]
+        lib.moe_quantize_rows.argtypes = [p, i64, i64, p, p, p, i64, p]
+        lib.moe_swiglu_quantize.argtypes = [p, i64, i64, p, p, p, i64, p]
+        lib.moe_swiglu_backward.argtypes = [p, p, i64, i64, p, p, p]
+        lib.moe_quantize_cols.argtypes = [dp, p, i64, i64, p, p, p, i64, p, p, sz, p]
+        lib.moe_expert_gemm_fp8.argtypes = [dp, p, p, i64, i64, i64, p, p, i64, p, p, p, p, sz, p]
+        lib.moe_expert_wgrad_fp8.argtypes = [dp, p, p, p, p, i64, i64, i64, i64, p, p, p, ci, ci, p, sz, p]
         lib.moe_layout_get_error.argtypes = [p, ctypes.POINTER(i32), p]
         lib.moe_strerror.argtypes = [ctypes.c_int]
         lib.moe_strerror.restype = ctypes.c_char_p
@@ -102,7 +126,9 @@ def load_library() -> ctypes.CDLL:
                      "moe_layout_rank_rows", "moe_dispatch_permute_ranks", "moe_dispatch_from_host",
                      "moe_combine_to_host", "moe_layout_accumulate_stats",
                      "moe_dispatch_permute", "moe_combine_unpermute", "moe_layout_get_error",
-                     "moe_dispatch_sf_col_major"):
+                     "moe_dispatch_sf_col_major", "moe_gate_workspace_bytes", "moe_gate_forward",
+                     "moe_gate_backward", "moe_quantize_rows", "moe_swiglu_quantize", "moe_swiglu_backward",
+                     "moe_quantize_cols", "moe_expert_gemm_fp8", "moe_expert_wgrad_fp8"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -391,6 +417,195 @@ def combine_to_host(lay: "Layout", expert_out, weights, out, out_host, chunk_tok
     _check(st, "moe_combine_to_host")
 
 
+# ---------------------------------------------------------------- gate
+def gate_workspace_bytes(desc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_gate_workspace_bytes(ctypes.byref(_desc(desc)), ctypes.byref(n)),
+           "moe_gate_workspace_bytes")
+    return int(n.value)
+
+
+def new_gate_workspace(desc, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace of the gate for ``desc``; its error word is read with ``get_error``."""
+    return torch.zeros(gate_workspace_bytes(desc), dtype=torch.uint8, device=device)
+
+
+def _gate_desc(cfg, logits) -> _CGateDesc:
+    if cfg.score not in ("softmax", "sigmoid"):
+        raise ValueError(f"unknown score {cfg.score!r}")
+    return _CGateDesc(int(logits.dtype == torch.bfloat16), int(cfg.score == "sigmoid"), int(bool(cfg.normalize)),
+                      float(cfg.scale), float(cfg.balance_coef))
+
+
+def _matrix(t, name, rows, cols, dtypes):
+    """A [rows, cols] device matrix with contiguous columns; returns (pointer, row stride in elements)."""
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap")
+    return ctypes.c_void_p(t.data_ptr()), int(ld)
+
+
+_LOGITS = (torch.float32, torch.bfloat16)
+
+
+def gate_forward(desc, cfg, logits, topk_idx, weights, expert_count, prob_mean, routed_tokens, balance_loss,
+                 workspace, bias=None, stream=None) -> None:
+    """Top-k ids and weights, per-expert counts and the balance loss of ``logits`` [N, E] (moe_gate_forward)."""
+    N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
+    lp, ld = _matrix(logits, "logits", N, E, _LOGITS)
+    st = load_library().moe_gate_forward(
+        ctypes.byref(_desc(desc)), ctypes.byref(_gate_desc(cfg, logits)), lp, ld,
+        _dev(bias, "bias", torch.float32, E, allow_none=True), _dev(topk_idx, "topk_idx", torch.int64, N * K),
+        _dev(weights, "weights", torch.float32, N * K), _dev(expert_count, "expert_count", torch.int32, E),
+        _dev(prob_mean, "prob_mean", torch.float32, E), _dev(routed_tokens, "routed_tokens", torch.int32, 1),
+        _dev(balance_loss, "balance_loss", torch.float32, 1), _dev(workspace, "workspace", torch.uint8),
+        workspace.numel(), _stream(stream))
+    _check(st, "moe_gate_forward")
+
+
+def gate_backward(desc, cfg, logits, topk_idx, expert_count, routed_tokens, dlogits, workspace, dweights=None,
+                  dloss=None, stream=None) -> None:
+    """Gradient of the weights and the balance loss with respect to the logits (moe_gate_backward)."""
+    N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
+    lp, ld = _matrix(logits, "logits", N, E, _LOGITS)
+    gp, gld = _matrix(dlogits, "dlogits", N, E, (logits.dtype,))
+    st = load_library().moe_gate_backward(
+        ctypes.byref(_desc(desc)), ctypes.byref(_gate_desc(cfg, logits)), lp, ld,
+        _dev(topk_idx, "topk_idx", torch.int64, N * K), _dev(expert_count, "expert_count", torch.int32, E),
+        _dev(routed_tokens, "routed_tokens", torch.int32, 1),
+        _dev(dweights, "dweights", torch.float32, N * K, allow_none=True),
+        _dev(dloss, "dloss", torch.float32, 1, allow_none=True), gp, gld, _dev(workspace, "workspace", torch.uint8),
+        workspace.numel(), _stream(stream))
+    _check(st, "moe_gate_backward")
+
+
+# ---------------------------------------------------------------- 8-bit rows
+def _blocks(n: int) -> int:
+    return (int(n) + 127) // 128
+
+
+def _sf_ld(sf, rows: int, blocks: int) -> int:
+    """Column-major scales [blocks, ld]: the leading dimension."""
+    if sf.dim() != 2 or sf.shape[0] != blocks or sf.shape[1] < rows:
+        raise ValueError(f"column-major scales must be [{blocks}, ld >= {rows}], got {tuple(sf.shape)}")
+    return int(sf.shape[1])
+
+
+def quantize_rows(x, q, sf, total_rows=None, col_major=False, stream=None) -> None:
+    """bf16 rows to e4m3 with a scale for each 1x128 block: ``sf`` [rows, blocks], or [blocks, ld] when
+    ``col_major`` (see ``new_sf_col_major``).  Rows from ``total_rows`` (device int32) on are left alone."""
+    if x.dim() != 2 or q.shape != x.shape:
+        raise ValueError("x and q must be matrices of the same shape")
+    rows, cols = x.shape
+    if col_major:
+        ld = _sf_ld(sf, rows, _blocks(cols))
+    else:
+        ld = 0
+        if tuple(sf.shape) != (rows, _blocks(cols)):
+            raise ValueError(f"sf must be [{rows}, {_blocks(cols)}], got {tuple(sf.shape)}")
+    st = load_library().moe_quantize_rows(
+        _dev(x, "x", torch.bfloat16), rows, cols, _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True),
+        _dev(q, "q", torch.float8_e4m3fn), _dev(sf, "sf", torch.float32), ld, _stream(stream))
+    _check(st, "moe_quantize_rows")
+
+
+def swiglu_quantize(gate_up, q, sf, total_rows=None, stream=None) -> None:
+    """silu(gate) * up of ``gate_up`` [rows, 2 * width] = [gate | up], quantised into ``q`` [rows, width] with
+    column-major scales ``sf`` [ceil(width / 128), ld]."""
+    if gate_up.dim() != 2 or q.dim() != 2 or gate_up.shape != (q.shape[0], 2 * q.shape[1]):
+        raise ValueError("gate_up must be [rows, 2 * width] and q [rows, width]")
+    rows, width = q.shape
+    st = load_library().moe_swiglu_quantize(
+        _dev(gate_up, "gate_up", torch.bfloat16), rows, width,
+        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True), _dev(q, "q", torch.float8_e4m3fn),
+        _dev(sf, "sf", torch.float32), _sf_ld(sf, rows, _blocks(width)), _stream(stream))
+    _check(st, "moe_swiglu_quantize")
+
+
+def swiglu_backward(gate_up, dh, dgate_up, total_rows=None, stream=None) -> None:
+    """Gradient of silu(gate) * up with respect to ``gate_up``, all bf16."""
+    if dh.dim() != 2 or gate_up.shape != (dh.shape[0], 2 * dh.shape[1]) or dgate_up.shape != gate_up.shape:
+        raise ValueError("gate_up and dgate_up must be [rows, 2 * width] and dh [rows, width]")
+    rows, width = dh.shape
+    st = load_library().moe_swiglu_backward(
+        _dev(gate_up, "gate_up", torch.bfloat16), _dev(dh, "dh", torch.bfloat16), rows, width,
+        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True),
+        _dev(dgate_up, "dgate_up", torch.bfloat16), _stream(stream))
+    _check(st, "moe_swiglu_backward")
+
+
+def quantize_cols(desc, x, expert_offset, expert_count, q, sf, workspace, stream=None) -> None:
+    """Receive rows ``x`` [capacity, cols] (bf16) to transposed e4m3 ``q`` [cols, ld] with a scale for each block
+    of 128 rows, ``sf`` [ceil(capacity / 128), cols]; gap rows count as zeros."""
+    E = int(desc.num_experts)
+    if x.dim() != 2 or q.dim() != 2 or q.shape[0] != x.shape[1]:
+        raise ValueError("x must be [capacity, cols] and q [cols, ld]")
+    cap, cols = x.shape
+    if tuple(sf.shape) != (_blocks(cap), cols):
+        raise ValueError(f"sf must be [{_blocks(cap)}, {cols}], got {tuple(sf.shape)}")
+    st = load_library().moe_quantize_cols(
+        ctypes.byref(_desc(desc)), _dev(x, "x", torch.bfloat16), cap, cols,
+        _dev(expert_offset, "expert_offset", torch.int32, E + 1), _dev(expert_count, "expert_count", torch.int32, E),
+        _dev(q, "q", torch.float8_e4m3fn), q.shape[1], _dev(sf, "sf", torch.float32),
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check(st, "moe_quantize_cols")
+
+
+# ---------------------------------------------------------------- expert products
+def expert_gemm(desc, x, x_sf, w, w_sf, expert_offset, expert_count, out, workspace, stream=None) -> None:
+    """out[r] = w[e] x[r] for the receive rows of every expert: e4m3 operands with block scales, bf16 out.
+
+    ``x`` [capacity, in], ``x_sf`` [ceil(in / 128), ld] (column-major), ``w`` [E, out, in], ``w_sf``
+    [E, ceil(out / 128), ceil(in / 128)], ``out`` [capacity, out].  With the weights transposed it is the input
+    gradient; with E = 1 a dense product."""
+    E = int(desc.num_experts)
+    if x.dim() != 2 or w.dim() != 3 or w.shape[0] != E or w.shape[2] != x.shape[1]:
+        raise ValueError(f"x must be [capacity, in] and w [{E}, out, in]")
+    cap, wi = x.shape
+    wo = w.shape[1]
+    if tuple(w_sf.shape) != (E, _blocks(wo), _blocks(wi)):
+        raise ValueError(f"w_sf must be [{E}, {_blocks(wo)}, {_blocks(wi)}], got {tuple(w_sf.shape)}")
+    if tuple(out.shape) != (cap, wo):
+        raise ValueError(f"out must be [{cap}, {wo}], got {tuple(out.shape)}")
+    st = load_library().moe_expert_gemm_fp8(
+        ctypes.byref(_desc(desc)), _dev(x, "x", torch.float8_e4m3fn), _dev(x_sf, "x_sf", torch.float32),
+        _sf_ld(x_sf, cap, _blocks(wi)), cap, wi, _dev(w, "w", torch.float8_e4m3fn),
+        _dev(w_sf, "w_sf", torch.float32), wo, _dev(expert_offset, "expert_offset", torch.int32, E + 1),
+        _dev(expert_count, "expert_count", torch.int32, E), _dev(out, "out", torch.bfloat16),
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check(st, "moe_expert_gemm_fp8")
+
+
+def expert_wgrad(desc, dy, dy_sf, x, x_sf, expert_offset, expert_count, dw, workspace, accumulate=False,
+                 stream=None) -> None:
+    """dw[e] = dy_e^T x_e from operands as ``quantize_cols`` writes them: ``dy`` [out, ld], ``x`` [in, ld] with the
+    same ld; ``dw`` [E, out, in] in bf16 or fp32 (``accumulate`` adds to an fp32 dw)."""
+    E = int(desc.num_experts)
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[1] != x.shape[1]:
+        raise ValueError("dy must be [out, ld] and x [in, ld]")
+    wo, wi, ld = dy.shape[0], x.shape[0], x.shape[1]
+    if dy_sf.dim() != 2 or dy_sf.shape[1] != wo or tuple(x_sf.shape) != (dy_sf.shape[0], wi):
+        raise ValueError("dy_sf must be [row blocks, out] and x_sf [row blocks, in]")
+    if tuple(dw.shape) != (E, wo, wi) or dw.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"dw must be [{E}, {wo}, {wi}] in bfloat16 or float32")
+    cap = min(ld, dy_sf.shape[0] * 128)
+    st = load_library().moe_expert_wgrad_fp8(
+        ctypes.byref(_desc(desc)), _dev(dy, "dy", torch.float8_e4m3fn), _dev(dy_sf, "dy_sf", torch.float32),
+        _dev(x, "x", torch.float8_e4m3fn), _dev(x_sf, "x_sf", torch.float32), ld, cap, wo, wi,
+        _dev(expert_offset, "expert_offset", torch.int32, E + 1), _dev(expert_count, "expert_count", torch.int32, E),
+        _dev(dw, "dw"), int(dw.dtype == torch.float32), int(bool(accumulate)),
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check(st, "moe_expert_wgrad_fp8")
+
+
 def get_error(workspace, stream=None) -> int:
     """Synchronise, read and clear the workspace's sticky device error (0 = none)."""
     v = ctypes.c_int32(0)
@@ -466,6 +681,51 @@ class Layout:
 
     def combine(self, expert_out, weights, out, stream=None):
         combine_unpermute(self.desc, expert_out, self.dst_slot, weights, out, self.workspace, stream)
+
+    def expert_gemm(self, x, x_sf, w, w_sf, out, stream=None):
+        """Expert product of 8-bit receive rows (column-major scales ``x_sf``) with weights [E, out, in]."""
+        expert_gemm(self.desc, x, x_sf, w, w_sf, self.expert_offset, self.expert_count, out, self.workspace, stream)
+
+    def quantize_cols(self, x, q, sf, stream=None):
+        """Receive rows transposed and quantised down the columns, for ``expert_wgrad``."""
+        quantize_cols(self.desc, x, self.expert_offset, self.expert_count, q, sf, self.workspace, stream)
+
+    def expert_wgrad(self, dy, dy_sf, x, x_sf, dw, accumulate=False, stream=None):
+        """Weight gradient of the expert product from transposed operands."""
+        expert_wgrad(self.desc, dy, dy_sf, x, x_sf, self.expert_offset, self.expert_count, dw, self.workspace,
+                     accumulate, stream)
+
+    def error(self, stream=None) -> int:
+        return get_error(self.workspace, stream)
+
+
+class Gate:
+    """Output buffers and workspace of the top-k gate for one batch shape.
+
+    ``forward(logits)`` fills ``topk_idx`` [N, K] (int64, ready for ``Layout.build``), ``weights`` [N, K] (for
+    ``Layout.combine``), ``expert_count`` [E], ``prob_mean`` [E], ``routed_tokens`` [1] and ``loss`` [1];
+    ``backward`` reads them and the same logits."""
+
+    def __init__(self, desc, cfg: GateConfig = GateConfig(), device="cuda"):
+        N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
+        self.desc, self.cfg = desc, cfg
+        self.workspace = new_gate_workspace(desc, device)
+        self.topk_idx = torch.empty((N, K), dtype=torch.int64, device=device)
+        self.weights = torch.empty((N, K), dtype=torch.float32, device=device)
+        self.expert_count = torch.empty(E, dtype=torch.int32, device=device)
+        self.prob_mean = torch.empty(E, dtype=torch.float32, device=device)
+        self.routed_tokens = torch.empty(1, dtype=torch.int32, device=device)
+        self.loss = torch.empty(1, dtype=torch.float32, device=device)
+
+    def forward(self, logits, bias=None, stream=None) -> "Gate":
+        gate_forward(self.desc, self.cfg, logits, self.topk_idx, self.weights, self.expert_count, self.prob_mean,
+                     self.routed_tokens, self.loss, self.workspace, bias, stream)
+        return self
+
+    def backward(self, logits, dlogits, dweights=None, dloss=None, stream=None):
+        gate_backward(self.desc, self.cfg, logits, self.topk_idx, self.expert_count, self.routed_tokens, dlogits,
+                      self.workspace, dweights, dloss, stream)
+        return dlogits
 
     def error(self, stream=None) -> int:
         return get_error(self.workspace, stream)

@@ -1,0 +1,365 @@
+// gate_kernels.cu -- the top-k gate of a mixture-of-experts layer with its
+// balance loss, and the gradient of both with respect to the logits.
+//
+// One warp owns a token; lane j holds the columns j, j+32, ... in registers,
+// so a row is read once and every reduction over experts is a warp reduction.
+//
+//   key_e = l_e + bias_e (one fp32 addition); the K largest keys are taken one
+//   after the other as integers that sort like the floats: redux.max gives the
+//   key and redux.min the lowest id that has it.  A key of -inf is not taken.
+//   s = softmax(l) or sigmoid(l), q = s / sum(s); w_k = scale * s_k / D.
+//   Balance loss: coef * E * sum_e f_e P_e with P_e the mean of q over the
+//   routed tokens and f_e = count_e / (K * routed tokens).
+//
+// A row without a key above -inf routes nowhere: ids -1, weights 0, not counted
+// as routed.  A row with a NaN or +inf key is treated the same and recorded in
+// the error word.
+//
+// The sums over tokens are kept in fp32 a lane and column while a warp walks
+// its tokens, then summed over warps, CTAs and last over the CTAs' partials in
+// a fixed order, so results do not change from run to run.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kGateThreads = 512;
+constexpr int kGateWarps = kGateThreads / 32;
+constexpr float kTiny = 1e-30f;              // floor of a sum of scores that divides
+constexpr unsigned kKeyNegInf = 0x007fffffu; // sortable key of -inf
+
+template <typename T>
+__device__ __forceinline__ float load_logit(const T* p);
+template <>
+__device__ __forceinline__ float load_logit<float>(const float* p) { return __ldg(p); }
+template <>
+__device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) {
+  return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+}
+
+__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_logit(uint16_t* p, float v) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(v);
+  *p = *reinterpret_cast<const uint16_t*>(&b);
+}
+
+// Unsigned integers in the order of the floats (no NaN); never 0.
+__device__ __forceinline__ unsigned sortable(float f) {
+  const unsigned b = __float_as_uint(f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float unsortable(unsigned u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float sigmoid_acc(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
+
+// One row's logits in registers: columns lane, lane + 32, ...; -inf past E.
+template <int VPL, typename T>
+__device__ __forceinline__ void load_row(const T* row, bool live, int lane, int E, float* l) {
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int col = lane + 32 * i;
+    l[i] = live && col < E ? load_logit(row + col) : -INFINITY;
+  }
+}
+
+// Scores of a row in place of its logits; returns their sum (floored).  `m` is
+// the row's largest logit (finite).
+template <int VPL, bool SIGMOID>
+__device__ __forceinline__ float scores(float* l, float m) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    // expf(-inf) = 0, and sigmoid(-inf) = 1 / (1 + inf) = 0: closed experts score nothing
+    l[i] = SIGMOID ? sigmoid_acc(l[i]) : expf(l[i] - m);
+    s += l[i];
+  }
+  return fmaxf(warp_sum(s), kTiny);
+}
+
+template <int VPL>
+__device__ __forceinline__ float row_max(const float* l) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+  return unsortable(__reduce_max_sync(kFull, sortable(m)));
+}
+
+template <int VPL, typename T, bool SIGMOID>
+__global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) {
+  extern __shared__ uint8_t smem[];
+  const int E = a.num_experts, K = a.topk;
+  float* sum_s = reinterpret_cast<float*>(smem);       // [E]
+  int* cnt_s = reinterpret_cast<int*>(smem) + E;       // [E + 1]: picks of each expert, routed tokens
+  __shared__ bool last_s;
+  __shared__ float red_s[kGateWarps];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  for (int e = threadIdx.x; e < E; e += kGateThreads) sum_s[e] = 0.0f;
+  for (int e = threadIdx.x; e <= E; e += kGateThreads) cnt_s[e] = 0;
+  __syncthreads();
+  ptx::grid_dependency_wait();
+
+  float bias[VPL], acc[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int col = lane + 32 * i;
+    bias[i] = a.bias != nullptr && col < E ? a.bias[col] : 0.0f;
+    acc[i] = 0.0f;
+  }
+  const T* logits = static_cast<const T*>(a.logits);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+  int routed = 0;
+  float next[VPL];
+  load_row<VPL, T>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
+  for (; t < a.num_tokens; t += stride) {
+    const T* row = logits + t * a.logits_stride;
+    float l[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = next[i];
+    load_row<VPL, T>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
+
+    unsigned u[VPL];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float key = l[i] + bias[i];   // also turns -0 into +0: they tie
+      const bool in = lane + 32 * i < E;
+      bad |= in && !(key < INFINITY);
+      u[i] = in ? sortable(key) : 0u;
+    }
+    bad = __any_sync(kFull, bad);
+    if (bad && lane == 0) set_error(a.err, MOE_ERR_INVALID_ARG);
+    unsigned best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (u[i] > best) best = u[i], at = i;
+    unsigned top = __reduce_max_sync(kFull, best);
+    const bool route = !bad && top > kKeyNegInf;
+    int mine = -1;
+    float w = 0.0f;
+    if (route) {
+      // without a bias the largest key is the largest logit
+      const float m = SIGMOID ? 0.0f : a.bias == nullptr ? unsortable(top) : row_max<VPL>(l);
+      const float total = scores<VPL, SIGMOID>(l, m);
+      const float inv = 1.0f / total;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) acc[i] += l[i] * inv;
+      ++routed;
+
+      for (int k = 0; k < K && top > kKeyNegInf; ++k) {
+        const unsigned id = __reduce_min_sync(kFull, best == top ? static_cast<unsigned>(lane + 32 * at) : kFull);
+        if (lane == k) mine = static_cast<int>(id);
+        if (static_cast<int>(id % 32) == lane) {
+          const int gone = static_cast<int>(id / 32);
+          best = 0;
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) {
+            if (i == gone) u[i] = 0;
+            if (u[i] > best) best = u[i], at = i;
+          }
+        }
+        top = __reduce_max_sync(kFull, best);
+      }
+      float s = 0.0f;
+      if (mine >= 0) {
+        const float lk = load_logit(row + mine);
+        s = SIGMOID ? sigmoid_acc(lk) : expf(lk - m) * inv;
+        atomicAdd(&cnt_s[mine], 1);
+      }
+      const float den = a.normalize ? fmaxf(warp_sum(s), kTiny) : 1.0f;
+      w = a.scale * s / den;
+    }
+    if (lane < K) {
+      a.topk_idx[t * K + lane] = mine;
+      a.weights[t * K + lane] = w;
+    }
+  }
+
+  // The CTA's sums: warps one after the other, so the order is fixed.
+  if (lane == 0 && routed > 0) atomicAdd(&cnt_s[E], routed);
+  for (int w = 0; w < kGateWarps; ++w) {
+    if (w == warp) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int col = lane + 32 * i;
+        if (col < E) sum_s[col] += acc[i];
+      }
+    }
+    __syncthreads();
+  }
+  float* part_sum = a.part_sum + static_cast<int64_t>(blockIdx.x) * E;
+  int* part_cnt = a.part_cnt + static_cast<int64_t>(blockIdx.x) * (E + 1);
+  for (int e = threadIdx.x; e < E; e += kGateThreads) part_sum[e] = sum_s[e];
+  for (int e = threadIdx.x; e <= E; e += kGateThreads) part_cnt[e] = cnt_s[e];
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last_s = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last_s) return;
+  __threadfence();
+
+  // The last CTA to finish: the other CTAs' partials in CTA order.
+  for (int e = threadIdx.x; e <= E; e += kGateThreads) {
+    float s = 0.0f;
+    int c = 0;
+    for (unsigned b = 0; b < gridDim.x; ++b) {
+      if (e < E) s += __ldcg(a.part_sum + static_cast<int64_t>(b) * E + e);
+      c += __ldcg(a.part_cnt + static_cast<int64_t>(b) * (E + 1) + e);
+    }
+    if (e < E) sum_s[e] = s;
+    cnt_s[e] = c;
+  }
+  __syncthreads();
+  const float inv_tokens = 1.0f / static_cast<float>(max(cnt_s[E], 1));
+  float part = 0.0f;
+  for (int e = threadIdx.x; e < E; e += kGateThreads) {
+    const float mean = sum_s[e] * inv_tokens;
+    part += mean * static_cast<float>(cnt_s[e]);
+    a.expert_count[e] = cnt_s[e];
+    a.prob_mean[e] = mean;
+  }
+  part = warp_sum(part);
+  if (lane == 0) red_s[warp] = part;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.0f;
+    for (int w = 0; w < kGateWarps; ++w) s += red_s[w];
+    *a.routed_tokens = cnt_s[E];
+    *a.balance_loss = a.balance_coef * static_cast<float>(E) * s * inv_tokens / static_cast<float>(K);
+    *a.ticket = 0;
+  }
+}
+
+// Gradient.  With g_e = dloss * coef * E * f_e / routed and A = sum_e q_e g_e,
+// the score's gradient is (g_e - A) / sum(s) plus, for a picked expert,
+// scale / D * (dw_k - sum_j dw_j s_j / D) (without the inner sum if weights are
+// not normalised).  softmax: dl = p (ds - c) with c = sum p ds, of which the
+// balance part is zero; sigmoid: dl = s (1 - s) ds.  The picked columns are
+// written by lane k after the row, over the value the row store left there.
+template <int VPL, typename T, bool SIGMOID>
+__global__ void __launch_bounds__(kGateThreads) gate_backward_kernel(GateArgs a) {
+  const int E = a.num_experts, K = a.topk;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  ptx::grid_dependency_wait();
+  float g[VPL];
+  const float routed = static_cast<float>(max(*a.routed_tokens, 1));
+  const float coef = a.dloss != nullptr ? *a.dloss * a.balance_coef * static_cast<float>(E) /
+                                              (static_cast<float>(K) * routed * routed) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int col = lane + 32 * i;
+    g[i] = col < E ? coef * static_cast<float>(a.expert_count[col]) : 0.0f;
+  }
+  const T* logits = static_cast<const T*>(a.logits);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+  float next[VPL];
+  load_row<VPL, T>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
+  for (; t < a.num_tokens; t += stride) {
+    const T* row = logits + t * a.logits_stride;
+    T* out = static_cast<T*>(a.dlogits) + t * a.dlogits_stride;
+    float l[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = next[i];
+    load_row<VPL, T>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
+    int64_t mine = lane < K ? a.topk_idx[t * K + lane] : -1;
+    if (mine >= E) {
+      mine = -1;
+      set_error(a.err, MOE_ERR_BAD_EXPERT_ID);
+    }
+    if (!__any_sync(kFull, mine >= 0)) {   // routed nowhere: no gradient
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (lane + 32 * i < E) store_logit(out + lane + 32 * i, 0.0f);
+      continue;
+    }
+    const float m = SIGMOID ? 0.0f : row_max<VPL>(l);
+    const float total = scores<VPL, SIGMOID>(l, m);
+    const float inv = 1.0f / total;
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) dot += l[i] * g[i];
+    const float A = warp_sum(dot) * inv;
+
+    float s = 0.0f, dw = 0.0f;
+    if (mine >= 0) {
+      const float lk = load_logit(row + mine);
+      s = SIGMOID ? sigmoid_acc(lk) : expf(lk - m) * inv;
+      if (a.dweights != nullptr) dw = a.dweights[t * K + lane];
+    }
+    float ds = a.scale * dw;
+    if (a.normalize) {
+      const float den = fmaxf(warp_sum(s), kTiny);
+      const float mean = warp_sum(s * dw) / den;
+      ds = a.scale / den * (dw - mean);
+    }
+    const float c = SIGMOID ? 0.0f : warp_sum(mine >= 0 ? s * ds : 0.0f);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int col = lane + 32 * i;
+      // softmax: sum(s) is 1, so (g - A) is the balance part of ds
+      const float d = SIGMOID ? l[i] * (1.0f - l[i]) * ((g[i] - A) * inv) : l[i] * inv * ((g[i] - A) - c);
+      if (col < E) store_logit(out + col, d);
+    }
+    __syncwarp();
+    if (mine >= 0) {
+      const float gk = coef * static_cast<float>(a.expert_count[mine]);
+      const float d = SIGMOID ? s * (1.0f - s) * ((gk - A) * inv + ds) : s * ((gk - A) - c + ds);
+      store_logit(out + mine, d);
+    }
+  }
+}
+
+template <typename T, bool SIGMOID>
+cudaError_t launch_gate(const GateArgs& a, bool backward, cudaStream_t stream) {
+  const int vpl = (a.num_experts + 31) / 32;
+  const int64_t want = ceil_div64(a.num_tokens, kGateWarps);
+  const int64_t most = backward ? 4 * static_cast<int64_t>(device_sm_count()) : kGateMaxCtas;
+  const unsigned grid = static_cast<unsigned>(max64(1, min64(want, most)));
+  const size_t smem = backward ? 0 : 4 * static_cast<size_t>(2 * a.num_experts + 1);
+  count_launch();
+#define MOE_GATE_CASE(V)                                                                                     \
+  if (vpl <= V)                                                                                              \
+    return backward ? launch_pdl(gate_backward_kernel<V, T, SIGMOID>, grid, kGateThreads, smem, stream, a)   \
+                    : launch_pdl(gate_forward_kernel<V, T, SIGMOID>, grid, kGateThreads, smem, stream, a);
+  MOE_GATE_CASE(1)
+  MOE_GATE_CASE(2)
+  MOE_GATE_CASE(4)
+  MOE_GATE_CASE(8)
+  MOE_GATE_CASE(12)
+  MOE_GATE_CASE(16)
+  MOE_GATE_CASE(32)
+#undef MOE_GATE_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+// The gate writes topk_idx, which the layout kernels may read before their
+// griddepcontrol.wait, so it never releases its dependents early.
+cudaError_t launch_gate(const GateArgs& a, bool backward, cudaStream_t stream) {
+  if (backward && a.num_tokens == 0) return cudaSuccess;
+  if (a.logits_bf16)
+    return a.sigmoid ? launch_gate<uint16_t, true>(a, backward, stream) : launch_gate<uint16_t, false>(a, backward, stream);
+  return a.sigmoid ? launch_gate<float, true>(a, backward, stream) : launch_gate<float, false>(a, backward, stream);
+}
+
+}  // namespace moe

@@ -99,6 +99,135 @@ struct SfColMajorArgs {
 
 cudaError_t launch_sf_col_major(const SfColMajorArgs& a, cudaStream_t stream);
 
+// Argument checks shared by the C entry points (moe_layout_api.cu).
+int check_desc(const moe_layout_desc* d);
+int check_workspace(const moe_layout_desc* d, const void* ws, size_t ws_bytes, WorkspaceLayout* out);
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
+}
+
+// ------------------------------------------------ gate (gate_kernels.cu)
+// CTAs of the forward kernel at most: each leaves one partial of the sums over
+// tokens in the gate's workspace, [error word | ticket | pad to 256 B]
+// [fp32 kGateMaxCtas x E][int32 kGateMaxCtas x (E + 1)].
+constexpr int kGateMaxCtas = 304;
+
+struct GateArgs {
+  const void* logits;
+  const float* bias;             // may be null
+  int64_t logits_stride;         // elements
+  int64_t num_tokens;
+  int num_experts;
+  int topk;
+  bool logits_bf16;
+  bool sigmoid;
+  bool normalize;
+  float scale;
+  float balance_coef;
+  int64_t* topk_idx;             // written forward, read backward
+  float* weights;
+  int32_t* expert_count;         // written forward, read backward
+  float* prob_mean;
+  int32_t* routed_tokens;        // written forward, read backward
+  float* balance_loss;
+  float* part_sum;
+  int32_t* part_cnt;
+  unsigned* ticket;              // zero between launches
+  int* err;
+  const float* dweights;         // backward; may be null
+  const float* dloss;            // backward; may be null
+  void* dlogits;
+  int64_t dlogits_stride;
+};
+
+cudaError_t launch_gate(const GateArgs& a, bool backward, cudaStream_t stream);
+
+// ------------------------------------------------ 8-bit rows (quantize_kernels.cu)
+struct QuantRowsArgs {
+  const uint16_t* x;             // bf16 bits [rows, cols], or [rows, 2 * cols] with swiglu
+  int64_t rows;
+  int64_t cols;
+  const int32_t* total_rows;     // rows in use, or null: all
+  uint8_t* q;                    // e4m3 [rows, cols]
+  float* sf;                     // scale of (row, block) at row * sf_row_stride + block * sf_block_stride
+  int64_t sf_row_stride;
+  int64_t sf_block_stride;
+  bool swiglu;
+};
+
+cudaError_t launch_quantize_rows(const QuantRowsArgs& a, cudaStream_t stream);
+
+struct QuantColsArgs {
+  const uint16_t* x;             // bf16 bits [capacity, cols]
+  int64_t capacity;
+  int64_t cols;
+  const int32_t* expert_offset;
+  const int32_t* expert_count;
+  int num_experts;
+  uint8_t* q;                    // e4m3 [cols, ld]
+  int64_t ld;
+  float* sf;                     // [capacity / 128, cols]
+  int* err;
+};
+
+cudaError_t launch_quantize_cols(const QuantColsArgs& a, cudaStream_t stream);
+
+struct SwigluBackwardArgs {
+  const uint16_t* gate_up;       // bf16 bits [rows, 2 * width]
+  const uint16_t* dh;            // bf16 bits [rows, width]
+  int64_t rows;
+  int64_t width;
+  const int32_t* total_rows;     // rows in use, or null: all
+  uint16_t* dgate_up;
+};
+
+cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, cudaStream_t stream);
+
+// ------------------------------------------------ expert products (expert_gemm_kernel.cu)
+struct ExpertGemmArgs {
+  const void* x;                 // e4m3: receive rows [capacity, width_in]; gradient: [width_in, sf_ld]
+  const float* x_sf;
+  int64_t sf_ld;                 // pitch of x_sf; gradient: pitch of both operands
+  int64_t capacity;
+  int64_t width_in;
+  const void* w;                 // e4m3: weights [E, width_out, width_in]; gradient: dy [width_out, sf_ld]
+  const float* w_sf;
+  int64_t width_out;
+  const int32_t* expert_offset;
+  const int32_t* expert_count;
+  void* out;
+  bool out_fp32;
+  bool accumulate;
+  int num_experts;
+  int64_t pairs;                 // (token, slot) pairs the layout was built for
+  int* err;
+};
+
+// The kernel's view: D[p, q] = sum over k-blocks of scales times <P_p, Q_q>.
+struct GemmParams {
+  const float* p_sf;
+  const float* q_sf;             // scale of (k-block, row of Q) at k-block * q_sf_pitch + row
+  int64_t q_sf_pitch;
+  int p_rows;                    // rows of P of an expert = columns (and pitch) of out
+  int q_rows;                    // gradient: rows of Q
+  int kblocks;                   // forward: k-blocks of a row
+  int num_experts;
+  const int32_t* expert_offset;
+  const int32_t* expert_count;
+  int64_t capacity;
+  void* out;
+  bool out_fp32;
+  bool accumulate;
+  int* err;
+  uint64_t wait_ns;              // bound on each mbarrier wait
+  unsigned extra_tx;             // test hook: bytes no copy delivers, on each CTA's (pair's) first stage
+};
+
+cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream);
+cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream);
+
 // Limit of every in-kernel wait and the test hooks that make a wait run out
 // (moe_debug_set_waits); the launchers copy them into the kernels' arguments.
 struct WaitConfig {

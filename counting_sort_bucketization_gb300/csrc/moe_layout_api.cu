@@ -153,10 +153,6 @@ WaitConfig wait_config() {
                     g_extra_tx.load(std::memory_order_relaxed)};
 }
 
-namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 int check_desc(const moe_layout_desc* d) {
   if (d == nullptr) return MOE_ERR_INVALID_ARG;
   if (d->num_tokens < 0 || d->topk < 1 || d->num_experts < 1 || d->num_ranks < 1 || d->alignment < 1)
@@ -178,12 +174,6 @@ int check_workspace(const moe_layout_desc* d, const void* ws, size_t ws_bytes, W
   return MOE_OK;
 }
 
-template <typename T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
-}
-
-}  // namespace
 }  // namespace moe
 
 using namespace moe;

@@ -68,7 +68,8 @@ extern "C" {
 enum moe_status {
   MOE_OK = 0,
   MOE_ERR_INVALID_ARG = 1,   /* host check failed: null pointer, bad size or alignment;
-                                device (moe_dispatch_sf_col_major): map entry out of range */
+                                device (moe_dispatch_sf_col_major): map entry out of range;
+                                device (moe_gate_forward): a NaN or +inf logit       */
   MOE_ERR_CUDA = 2,          /* a CUDA launch or copy failed                           */
   MOE_ERR_BAD_EXPERT_ID = 3, /* device: some topk_idx entry was >= E                   */
   MOE_ERR_CAPACITY = 4,      /* device: the layout needs more rows than capacity_rows  */
@@ -353,6 +354,148 @@ MOE_API int moe_combine_to_host(const moe_layout_desc* desc, const void* expert_
                                 void* out_host, void* workspace, size_t workspace_bytes,
                                 int64_t chunk_tokens, void* stream, void* copy_stream);
 
+/* ------------------------------------------------------------------------
+ * Around the layout: the gate that makes topk_idx and the weights, the 8-bit
+ * rows the dispatch moves, and the expert products on the receive buffer.
+ * The pages leave all of these to the caller; the formulas below are plain
+ * definitions.  None of these kernels releases its dependents early, so their
+ * outputs may be passed to the layout and dispatch calls directly.
+ */
+
+/* Gate settings.  Plain values, copied by every call. */
+typedef struct moe_gate_desc {
+  int32_t logits_bf16;   /* 0: fp32 logits (and gradient), 1: bf16                    */
+  int32_t sigmoid;       /* scores: 0 softmax over the experts, 1 sigmoid             */
+  int32_t normalize;     /* 1: a token's weights sum to scale                         */
+  float scale;           /* factor of the weights                                     */
+  float balance_coef;    /* factor of the balance loss                                */
+} moe_gate_desc;
+
+/* Bytes of the gate's workspace: its error word (read with
+ * moe_layout_get_error) and the partial sums of the forward call.  Zero-fill
+ * once; one stream at a time. */
+MOE_API int moe_gate_workspace_bytes(const moe_layout_desc* desc, size_t* bytes);
+
+/*
+ * Top-k gate with per-expert counts and balance loss.  For token t with logits
+ * l (row t at logits + t * logits_stride elements; columns contiguous):
+ *   key_e = l_e + bias_e in fp32 (bias may be NULL: 0); the K largest keys, in
+ *     descending order, equal keys by ascending id; a key of -inf is never
+ *     taken, so l_e = -inf closes expert e for the token;
+ *   s = softmax(l) or sigmoid(l) (without the bias), q = s / sum_e s;
+ *   topk_idx[t*K+k] = id (int64), weights[t*K+k] = scale * s_id / D with
+ *     D = the sum of the token's picked s if normalize, else 1; slots without
+ *     an expert get id -1 and weight 0.
+ * Tokens without a key above -inf are not routed (ids -1, weights 0).  Tokens
+ * with a NaN or +inf key are treated the same and record MOE_ERR_INVALID_ARG
+ * in the workspace.  Over the T routed tokens:
+ *   expert_count[E], routed_tokens[1] = T,
+ *   prob_mean[E] = (1/T) sum_t q, balance_loss[1] =
+ *     balance_coef * E * sum_e (expert_count[e] / (K*T)) * prob_mean[e]
+ * (zeros if T = 0).  Everything is fp32 and does not change from run to run.
+ * alignment and num_ranks of desc are not used.
+ */
+MOE_API int moe_gate_forward(const moe_layout_desc* desc, const moe_gate_desc* gate, const void* logits,
+                             int64_t logits_stride, const float* bias, int64_t* topk_idx, float* weights,
+                             int32_t* expert_count, float* prob_mean, int32_t* routed_tokens,
+                             float* balance_loss, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of weights and balance_loss with respect to the logits, from the
+ * forward call's logits, topk_idx, expert_count and routed_tokens.
+ * dweights [N*K] and dloss [1] are fp32 and may each be NULL (zero).  The counts
+ * and the choice of experts carry no gradient; the bias gets none.  dlogits
+ * [N, dlogits_stride] has the logits' type; tokens that were not routed get 0.
+ */
+MOE_API int moe_gate_backward(const moe_layout_desc* desc, const moe_gate_desc* gate, const void* logits,
+                              int64_t logits_stride, const int64_t* topk_idx, const int32_t* expert_count,
+                              const int32_t* routed_tokens, const float* dweights, const float* dloss,
+                              void* dlogits, int64_t dlogits_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * bf16 rows to e4m3 with one fp32 scale for each 1x128 block (the last block of
+ * a row may be shorter):
+ *   sf = max(max|x|, 1e-30) / 448, q = e4m3(x * (1 / sf)), nearest even.
+ *   x bf16 [rows, cols], q [rows, cols]: cols a positive multiple of 16, bases
+ *   16-byte aligned; B = ceil(cols / 128) scales a row:
+ *   sf_ld == 0: row-major [rows, B], as moe_dispatch_permute takes them;
+ *   sf_ld > 0:  column-major [B, sf_ld], sf_ld >= rows and a multiple of 4, as
+ *               moe_dispatch_sf_col_major writes them and moe_expert_gemm_fp8
+ *               reads them.
+ * total_rows (device int32, may be NULL): rows in use; later rows are neither
+ * read nor written.
+ */
+MOE_API int moe_quantize_rows(const void* x, int64_t rows, int64_t cols, const int32_t* total_rows, void* q,
+                              float* sf, int64_t sf_ld, void* stream);
+
+/*
+ * silu(gate) * up of rows [gate | up] (bf16 [rows, 2 * width]), quantised as by
+ * moe_quantize_rows with column-major scales [ceil(width / 128), sf_ld].
+ */
+MOE_API int moe_swiglu_quantize(const void* gate_up, int64_t rows, int64_t width, const int32_t* total_rows,
+                                void* q, float* sf, int64_t sf_ld, void* stream);
+
+/*
+ * Gradient of silu(gate) * up: gate_up bf16 [rows, 2 * width], dh bf16
+ * [rows, width], dgate_up bf16 [rows, 2 * width]; width a multiple of 8.
+ */
+MOE_API int moe_swiglu_backward(const void* gate_up, const void* dh, int64_t rows, int64_t width,
+                                const int32_t* total_rows, void* dgate_up, void* stream);
+
+/*
+ * Receive rows to transposed e4m3 with one scale for each block of 128 rows of a
+ * column: the operands of moe_expert_wgrad_fp8.
+ *   x bf16 [capacity_rows, cols], cols a multiple of 8; q [cols, ld] with
+ *   ld >= capacity_rows rounded up to 128, a multiple of 128; sf
+ *   [ceil(capacity_rows / 128), cols].  Rows in the alignment gaps count as
+ *   zeros whatever they hold.  Row blocks past the last segment are not written.
+ * desc->alignment must be a multiple of 128 (MOE_ERR_UNSUPPORTED otherwise).
+ */
+MOE_API int moe_quantize_cols(const moe_layout_desc* desc, const void* x, int64_t capacity_rows, int64_t cols,
+                              const int32_t* expert_offset, const int32_t* expert_count, void* q, int64_t ld,
+                              float* sf, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Expert product on the receive buffer.  For every row r of expert e
+ * (expert_offset[e] <= r < expert_offset[e] + expert_count[e]) and output o:
+ *   out[r, o] = bf16( sum_b x_sf[b, r] * w_sf[e, o / 128, b] *
+ *                           sum_{i in block b} x[r, i] * w[e, o, i] )
+ * over the 128-wide blocks b of width_in; products and sums in fp32, rounded
+ * once.  Rows in the alignment gaps of out are set to zero; later rows are not
+ * written.  Rows of x outside the segments' real rows are never used, whatever
+ * they hold.
+ *   x e4m3 [capacity_rows, width_in], x_sf fp32 [ceil(width_in / 128), sf_ld]
+ *   (column-major), w e4m3 [E, width_out, width_in], w_sf fp32
+ *   [E, ceil(width_out / 128), ceil(width_in / 128)], out bf16
+ *   [capacity_rows, width_out]; width_in a multiple of 16, width_out of 8;
+ *   x, w and out 16-byte aligned.
+ * The input gradient is the same call with the weights (and their scales)
+ * transposed.  A single dense product is E = 1.  desc->num_tokens * topk is the
+ * number of pairs the layout was built for: it chooses the tiling, not the result's
+ * meaning.
+ */
+MOE_API int moe_expert_gemm_fp8(const moe_layout_desc* desc, const void* x, const float* x_sf, int64_t sf_ld,
+                                int64_t capacity_rows, int64_t width_in, const void* w, const float* w_sf,
+                                int64_t width_out, const int32_t* expert_offset, const int32_t* expert_count,
+                                void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Weight gradient of the expert product.  For every expert e, with b over the
+ * 128-row blocks of its segment:
+ *   dw[e, o, i] = sum_b dy_sf[b, o] * x_sf[b, i] * sum_{r in block b} dy[o, r] * x[i, r]
+ * (0 for an expert without rows), from operands as moe_quantize_cols writes
+ * them: dy [width_out, ld], dy_sf [ceil(capacity_rows/128), width_out],
+ * x [width_in, ld], x_sf [ceil(capacity_rows/128), width_in].
+ * dw is [E, width_out, width_in], bf16 (dw_fp32 == 0) or fp32; accumulate != 0
+ * adds to what an fp32 dw holds.  width_in a multiple of 8.  desc->alignment
+ * must be a multiple of 128.
+ */
+MOE_API int moe_expert_wgrad_fp8(const moe_layout_desc* desc, const void* dy, const float* dy_sf, const void* x,
+                                 const float* x_sf, int64_t ld, int64_t capacity_rows, int64_t width_out,
+                                 int64_t width_in, const int32_t* expert_offset, const int32_t* expert_count,
+                                 void* dw, int dw_fp32, int accumulate, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
 /*
  * Synchronise `stream`, copy the workspace's sticky error word (the first
  * device-side error since the last read; MOE_OK if none) into
@@ -374,7 +517,8 @@ MOE_API uint64_t moe_kernel_launches(void);
  * raises the cooperative layout kernel's grid-barrier targets past the number
  * of CTAs, so its first barrier can only run out; extra_tx (a multiple of 16)
  * adds transaction bytes that no copy delivers to each CTA's first stage of
- * the dynamic permute, so that stage can only run out.  A layout that timed
+ * the dynamic permute and of the expert products, so that stage can only run
+ * out.  A layout that timed
  * out leaves its workspace's barrier counter set: zero the workspace before
  * reusing it.  Call with (0, 0, 0) to restore normal operation.
  */
