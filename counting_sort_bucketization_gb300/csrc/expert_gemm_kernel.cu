@@ -19,8 +19,11 @@
 //
 //   warp 0      TMA loads of P and Q tiles (128-byte rows, one k-block wide)
 //   warp 1      tcgen05.mma, 4 per k-block, into one of NBUF tensor-memory buffers
-//   warps 2-3   the k-block's scales to shared memory (cp.async)
-//   warps 4-11  tensor memory -> fp32 sums; at the tile's end bf16 (fp32) rows out
+//   warps 2-3   the k-block's scales to shared memory
+//   warps 4-19  tensor memory -> fp32 sums; at the tile's end bf16 (fp32) rows out
+//
+// More than 128 columns are two accumulators, each with its own barriers and 8
+// of the 16 epilogue warps: the tensor core fills one while the other is read.
 //
 // One persistent CTA (or pair: CTAS == 2, one 256-row MMA over two SMs, each
 // loading half of Q) per SM walks the tiles of all experts.  All sums are fp32;
@@ -40,9 +43,11 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kEpilogueWarps = 8;
-constexpr int kScaleThreads = 64;
+constexpr int kThreads = 640;
+constexpr int kEpilogueWarps = 16;
+constexpr int kHalfCols = 128;                     // columns of an accumulator
+constexpr int kBatchCols = 32;                     // columns a warp loads at a time
+constexpr int kBatches = 2;                        // of a warp: 8 warps, 4 of them side by side in rows
 constexpr int kKBlock = 128;                       // values (and bytes) of K in a scale block
 constexpr int kPRows = 128;                        // accumulator rows of a CTA
 constexpr int kPBytes = kPRows * kKBlock;
@@ -52,10 +57,12 @@ constexpr int kStages = 6;
 constexpr int kScaleSlots = 6;
 constexpr int kSlotWords = 256 + kPRows;           // Q scales, then P scales (forward: one word)
 constexpr int kOutPitch = 80;                      // bytes; 64 of data, conflict-free for stmatrix
-constexpr int kOutBytes = 16 * kOutPitch;          // a warp's 16 rows x 32 columns of bf16
+constexpr int kOutBytes = 8 * kOutPitch;           // a warp's 8 rows x 32 columns of bf16
 constexpr int kTmemCols = 512;
-constexpr int kEpilogueRegs = 208, kOtherRegs = 88;
-static_assert(256 * kEpilogueRegs + 128 * kOtherRegs <= kThreads * 168, "register split above the launch's total");
+constexpr int kScaleThreads = 64;
+// Registers a thread: each SM quarter holds 4 epilogue warps and one other.
+constexpr int kLaunchRegs = 96, kEpilogueRegs = 104, kOtherRegs = 64;
+static_assert(512 * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split above the launch's total");
 
 struct Smem {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
@@ -66,7 +73,7 @@ struct Smem {
   int seg_count[MOE_MAX_EXPERTS];
   uint64_t full[kStages], empty[kStages];
   uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
-  uint64_t acc_full[8], acc_empty[8];
+  uint64_t acc_full[2][4], acc_empty[2][4];        // [half][buffer]
   uint32_t tmem;
   int warp_sum[kThreads / 32];
 };
@@ -79,7 +86,7 @@ struct Tile {
   int p0;          // first row of P for this CTA
   int q0;          // first row of Q
   int q_valid;     // rows of Q that exist
-  int n;           // accumulator columns: q_valid rounded up
+  int n[2];        // columns of the two accumulators; the second may have none
   int k0;          // first k (forward 0, gradient: the segment's first row)
   int kblocks;
   bool last_q;     // the expert's last tile along Q
@@ -111,7 +118,9 @@ struct Tiling {
     r.p0 = (pt * CTAS + static_cast<int>(rank)) * kPRows;
     r.q_valid = max(0, min(per, q_rows - q * per));
     r.q0 = (WGRAD ? 0 : s.seg_start[lo]) + q * per;
-    r.n = max(kUnit, ceil_div(r.q_valid, kUnit) * kUnit);
+    const int n = max(kUnit, ceil_div(r.q_valid, kUnit) * kUnit);
+    r.n[0] = n <= kHalfCols ? n : ceil_div(n / 2, 32) * 32;
+    r.n[1] = n - r.n[0];
     r.k0 = WGRAD ? s.seg_start[lo] : 0;
     r.kblocks = WGRAD ? ceil_div(count, kKBlock) : p.kblocks;
     r.last_q = q == nq - 1;
@@ -126,15 +135,15 @@ __device__ __forceinline__ int scale_place(int j) {
 
 // The whole warp waits, and leaves together (tcgen05.ld needs all lanes).
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, ptx::mbar_wait_parity_bounded(bar, parity, limit_ns));
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, limit_ns));
 }
 
 template <int CTAS, int MAXN, bool WGRAD>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q64,
                    const __grid_constant__ CUtensorMap map_q16, const GemmParams p) {
-  constexpr int NBUF = kTmemCols / MAXN < 8 ? kTmemCols / MAXN : 8;
-  constexpr int kChunks = MAXN / 32;        // 16-column chunks of an epilogue warp
+  constexpr int NBUF = kTmemCols / MAXN;
+  static_assert(NBUF <= 4 && (MAXN <= kHalfCols || CTAS == 2), "tensor memory and shared memory of Q");
   using T = Tiling<CTAS, MAXN, WGRAD>;
   extern __shared__ uint8_t smem_raw[];
   // The same offset in both CTAs of a pair: the bases are equal.
@@ -155,10 +164,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       ptx::mbar_init(&s.scale_full[i], kScaleThreads);
       ptx::mbar_init(&s.scale_empty[i], kEpilogueWarps);
     }
-    for (int i = 0; i < NBUF; ++i) {
-      ptx::mbar_init(&s.acc_full[i], 1);
-      ptx::mbar_init(&s.acc_empty[i], kEpilogueWarps * CTAS);
-    }
+    for (int i = 0; i < NBUF; ++i)
+      for (int h = 0; h < 2; ++h) {
+        ptx::mbar_init(&s.acc_full[h][i], 1);
+        ptx::mbar_init(&s.acc_empty[h][i], kEpilogueWarps / 2 * CTAS);
+      }
     ptx::fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc<CTAS>(&s.tmem, kTmemCols);
@@ -217,206 +227,230 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       uint32_t it = 0;
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = T::get(p, s, t, rank);
-        const int rows = tile.n / CTAS;                                 // rows of Q this CTA loads
-        const int q = tile.q0 + static_cast<int>(rank) * rows;
-        const uint32_t bytes = CTAS * (kPBytes + rows * kKBlock);
+        const uint32_t bytes = CTAS * kPBytes + (tile.n[0] + tile.n[1]) * kKBlock;
         for (int kb = 0; kb < tile.kblocks; ++kb, ++it) {
-          const uint32_t st = it % kStages, use = it / kStages;
-          if (!(ok = ptx::mbar_wait_parity_bounded(&s.empty[st], (use & 1) ^ 1, p.wait_ns))) break;
+          const uint32_t st = it % kStages;
+          if (!(ok = tc::mbar_wait(&s.empty[st], (it / kStages & 1) ^ 1, p.wait_ns))) break;
           if (leader) ptx::mbar_arrive_expect_tx(&s.full[st], bytes + (it == 0 ? p.extra_tx : 0));
           uint32_t bar = ptx::smem_addr(&s.full[st]);
           if (CTAS == 2) bar = tc::map_to_rank(bar, 0);
           const uint32_t dst = ptx::smem_addr(s.stage[st]);
           const int x = tile.k0 + kb * kKBlock;
           tc::load_box<CTAS>(dst, &map_p, x, tile.p0, WGRAD ? 0 : tile.expert, bar);
-          int r = 0;
-          for (; r + 64 <= rows; r += 64) tc::load_box<CTAS>(dst + kPBytes + r * kKBlock, &map_q64, x, q + r, 0, bar);
-          for (; r < rows; r += 16) tc::load_box<CTAS>(dst + kPBytes + r * kKBlock, &map_q16, x, q + r, 0, bar);
+          // the columns of each accumulator, half of them by each CTA of a pair
+#pragma unroll
+          for (int h = 0; h < CTAS; ++h) {
+            const int rows = tile.n[h] / CTAS;
+            const int q = tile.q0 + (h == 0 ? 0 : tile.n[0]) + static_cast<int>(rank) * rows;
+            const uint32_t to = dst + kPBytes + h * (kHalfCols / CTAS) * kKBlock;
+            int r = 0;
+            for (; r + 64 <= rows; r += 64) tc::load_box<CTAS>(to + r * kKBlock, &map_q64, x, q + r, 0, bar);
+            for (; r < rows; r += 16) tc::load_box<CTAS>(to + r * kKBlock, &map_q16, x, q + r, 0, bar);
+          }
         }
       }
       // Every stage handed back: no copy or remote arrival is left in flight.
       for (uint32_t i = 0; i < kStages; ++i, ++it)
-        if (it >= kStages) ok &= ptx::mbar_wait_parity_bounded(&s.empty[it % kStages], (it / kStages & 1) ^ 1, p.wait_ns);
+        if (it >= kStages) ok &= tc::mbar_wait(&s.empty[it % kStages], (it / kStages & 1) ^ 1, p.wait_ns);
     } else if (warp == 1 && lane == 0 && leader) {
       // ---- MMA -----------------------------------------------------------
-      uint32_t it = 0;
+      uint32_t it = 0, used[2] = {0, 0};
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = T::get(p, s, t, rank);
-        const uint32_t idesc = tc::instr_desc(kPRows * CTAS, tile.n);
-        for (int kb = 0; kb < tile.kblocks; ++kb, ++it) {
-          const uint32_t st = it % kStages, b = it % NBUF;
-          if (!(ok = ptx::mbar_wait_parity_bounded(&s.acc_empty[b], (it / NBUF & 1) ^ 1, p.wait_ns))) break;
-          if (!(ok = ptx::mbar_wait_parity_bounded(&s.full[st], it / kStages & 1, p.wait_ns))) break;
-          tc::fence_after();
+        for (int kb = 0; kb < tile.kblocks && ok; ++kb, ++it) {
+          const uint32_t st = it % kStages;
+          if (!(ok = tc::mbar_wait(&s.full[st], it / kStages & 1, p.wait_ns))) break;
           const uint64_t a = tc::operand_desc(ptx::smem_addr(s.stage[st]));
-          const uint64_t q = tc::operand_desc(ptx::smem_addr(s.stage[st]) + kPBytes);
 #pragma unroll
-          for (int k = 0; k < kKBlock / 32; ++k)
-            tc::mma_e4m3<CTAS>(tmem + b * MAXN, a + 2 * k, q + 2 * k, idesc, k > 0);
-          tc::commit<CTAS>(&s.empty[st]);
-          tc::commit<CTAS>(&s.acc_full[b]);
+          for (int h = 0; h < CTAS; ++h) {
+            if (tile.n[h] == 0) continue;
+            const uint32_t b = used[h] % NBUF;
+            if (!(ok = tc::mbar_wait(&s.acc_empty[h][b], (used[h] / NBUF & 1) ^ 1, p.wait_ns))) break;
+            ++used[h];
+            tc::fence_after();
+            const uint64_t q =
+                tc::operand_desc(ptx::smem_addr(s.stage[st]) + kPBytes + h * (kHalfCols / CTAS) * kKBlock);
+            const uint32_t idesc = tc::instr_desc(kPRows * CTAS, tile.n[h]);
+#pragma unroll
+            for (int k = 0; k < kKBlock / 32; ++k)
+              tc::mma_e4m3<CTAS>(tmem + b * MAXN + h * kHalfCols, a + 2 * k, q + 2 * k, idesc, k > 0);
+            tc::commit<CTAS>(&s.acc_full[h][b]);
+          }
+          if (ok) tc::commit<CTAS>(&s.empty[st]);
         }
       }
-      for (uint32_t i = 0; i < NBUF; ++i, ++it)   // the epilogues' last (remote) arrivals
-        if (it >= NBUF) ok &= ptx::mbar_wait_parity_bounded(&s.acc_empty[it % NBUF], (it / NBUF & 1) ^ 1, p.wait_ns);
+      for (int h = 0; h < 2; ++h)   // the epilogues' last (remote) arrivals
+        for (uint32_t i = 0; i < NBUF; ++i, ++used[h])
+          if (used[h] >= NBUF)
+            ok &= tc::mbar_wait(&s.acc_empty[h][used[h] % NBUF], (used[h] / NBUF & 1) ^ 1, p.wait_ns);
     } else if (warp >= 2) {
       // ---- scales --------------------------------------------------------
+      // Through registers, kAhead k-blocks ahead; the forward product's P scale is
+      // one number a k-block and goes into the Q scales here.
+      constexpr int kAhead = 3, kQ = MAXN / kScaleThreads, kP = WGRAD ? kPRows / kScaleThreads : 1;
       const int j0 = static_cast<int>(threadIdx.x) - 64;
       uint32_t it = 0;
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = T::get(p, s, t, rank);
         const int64_t kb0 = tile.k0 / kKBlock;
-        const float* qs = p.q_sf + kb0 * p.q_sf_pitch + tile.q0;
-        const int mblk = tile.p0 / kKBlock;
-        const float* ps = WGRAD ? p.p_sf + kb0 * p.p_rows + tile.p0
-                                : p.p_sf + (static_cast<int64_t>(tile.expert) * ceil_div(p.p_rows, kKBlock) + mblk) * p.kblocks;
-        for (int kb = 0; kb < tile.kblocks; ++kb, ++it) {
-          const uint32_t sl = it % kScaleSlots;
-          if (!(ok = ptx::mbar_wait_parity_bounded(&s.scale_empty[sl], (it / kScaleSlots & 1) ^ 1, p.wait_ns))) break;
-          const uint32_t dst = ptx::smem_addr(s.scale[sl]);
-          for (int j = j0; j < tile.n; j += kScaleThreads) {
-            const bool in = j < tile.q_valid;
-            tc::cp_async4(dst + 4 * scale_place(j), in ? qs + j : p.q_sf, in);
-          }
-          if (WGRAD) {
-            for (int j = j0; j < kPRows; j += kScaleThreads) {
-              const bool in = tile.p0 + j < p.p_rows;
-              tc::cp_async4(dst + 4 * (256 + j), in ? ps + j : p.p_sf, in);
+        const float* qs = p.q_sf + kb0 * p.q_sf_pitch + tile.q0 + j0;
+        const float* ps = WGRAD ? p.p_sf + kb0 * p.p_rows + tile.p0 + j0
+                                : p.p_sf + (static_cast<int64_t>(tile.expert) * ceil_div(p.p_rows, kKBlock) +
+                                            tile.p0 / kKBlock) * p.kblocks;
+        float q[kAhead][kQ], w[kAhead][kP];
+        const auto fetch = [&](int kb, float* qv, float* wv) {
+          const bool in = kb < tile.kblocks;
+#pragma unroll
+          for (int i = 0; i < kQ; ++i)
+            qv[i] = in && j0 + i * kScaleThreads < tile.q_valid ? __ldg(qs + kb * p.q_sf_pitch + i * kScaleThreads) : 0.0f;
+#pragma unroll
+          for (int i = 0; i < kP; ++i)
+            wv[i] = !in || tile.p0 + (WGRAD ? j0 + i * kScaleThreads : 0) >= p.p_rows ? 0.0f
+                    : WGRAD ? __ldg(ps + static_cast<int64_t>(kb) * p.p_rows + i * kScaleThreads) : __ldg(ps + kb);
+        };
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) fetch(d, q[d], w[d]);
+        for (int kb = 0; kb < tile.kblocks && ok; kb += kAhead) {
+#pragma unroll
+          for (int d = 0; d < kAhead; ++d) {
+            if (kb + d >= tile.kblocks) break;
+            const uint32_t sl = it % kScaleSlots;
+            if (!(ok = tc::mbar_wait(&s.scale_empty[sl], (it / kScaleSlots & 1) ^ 1, p.wait_ns))) break;
+            ++it;
+#pragma unroll
+            for (int i = 0; i < kQ; ++i)
+              s.scale[sl][scale_place(j0 + i * kScaleThreads)] = WGRAD ? q[d][i] : q[d][i] * w[d][0];
+            if (WGRAD) {
+#pragma unroll
+              for (int i = 0; i < kP; ++i) s.scale[sl][256 + j0 + i * kScaleThreads] = w[d][i];
             }
-            ps += p.p_rows;
-          } else if (j0 == 0) {
-            const bool in = tile.p0 < p.p_rows;
-            tc::cp_async4(dst + 4 * 256, in ? ps + kb : p.p_sf, in);
+            ptx::mbar_arrive(&s.scale_full[sl]);
+            fetch(kb + d + kAhead, q[d], w[d]);
           }
-          qs += p.q_sf_pitch;
-          tc::cp_async_arrive(&s.scale_full[sl]);
         }
       }
     }
   } else {
     // ---- epilogue --------------------------------------------------------
-    // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 and every second
-    // 16-column chunk.
+    // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of one accumulator:
+    // 32 columns, and the 32 columns 64 further on.
     tc::reg_inc<kEpilogueRegs>();
-    const int quarter = warp % 4, group = (warp - 4) / 4;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint8_t* stage = s.out[warp - 4];
-    uint32_t it = 0;
+    const int ew = warp - 4, quarter = warp % 4, half = ew / 8, sub = ew / 4 % 2;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalfCols + sub * kBatchCols;
+    uint8_t* stage = s.out[ew];
+    uint32_t it = 0, used = 0;
     for (int t = first_tile; t < tiles && ok; t += step) {
-      const Tile tile = T::get(p, s, t, rank);
-      const int chunks = tile.n / 16;
-      uint64_t acc[kChunks][8];
+      // Only these three values stay in registers over the k-blocks.
+      int n, first, kblocks;
+      {
+        const Tile tile = T::get(p, s, t, rank);
+        n = half == 0 ? tile.n[0] : tile.n[1];
+        first = half == 0 ? 0 : tile.n[0];                  // column of the tile the accumulator starts at
+        kblocks = tile.kblocks;
+      }
+      uint64_t acc[kBatches][16];
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
+      for (int c = 0; c < kBatches; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[c][i] = 0;
-      for (int kb = 0; kb < tile.kblocks; ++kb, ++it) {
-        const uint32_t b = it % NBUF, sl = it % kScaleSlots;
+        for (int i = 0; i < 16; ++i) acc[c][i] = 0;
+      for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        const uint32_t b = used % NBUF, sl = it % kScaleSlots;
         if (!(ok = wait_warp(&s.scale_full[sl], it / kScaleSlots & 1, p.wait_ns))) break;
-        if (!(ok = wait_warp(&s.acc_full[b], it / NBUF & 1, p.wait_ns))) break;
-        tc::fence_after();
-        const float* sc = s.scale[sl];
-        uint64_t pw[4];
-        if (WGRAD) {
+        if (n > 0) {
+          if (!(ok = wait_warp(&s.acc_full[half][b], used / NBUF & 1, p.wait_ns))) break;
+          ++used;
+          tc::fence_after();
+          const float* sc = s.scale[sl];
+          uint64_t pw[4];
+          if (WGRAD) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = sc[256 + quarter * 32 + 8 * i + lane / 4];
-            pw[i] = tc::pack2(v, v);
-          }
-        } else {
-          pw[0] = tc::pack2(sc[256], sc[256]);
-        }
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int chunk = 2 * c + group;
-          if (chunk < chunks) {
-            uint32_t v[16];
-            tc::ld_16x16(lane_base + b * MAXN + chunk * 16, v);
-            tc::ld_16x16(lane_base + b * MAXN + chunk * 16 + (16u << 16), v + 8);
-            const float4 q4 = *reinterpret_cast<const float4*>(sc + chunk * 16 + (lane % 4) * 4);
-            uint64_t qs[2] = {tc::pack2(q4.x, q4.y), tc::pack2(q4.z, q4.w)};
-            if (!WGRAD) {
-              qs[0] = tc::mul2(qs[0], pw[0]);
-              qs[1] = tc::mul2(qs[1], pw[0]);
-            }
-            tc::wait_ld();
-            // acc[c][4 * half + 2 * h + r]: rows 16 * half + 8 * r + lane / 4, columns 8 * h + 2 * (lane % 4), +1
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int half = i / 4, h = i / 2 % 2, r = i % 2;
-              uint64_t v2 = tc::pack2(v[8 * half + 4 * h + 2 * r], v[8 * half + 4 * h + 2 * r + 1]);
-              if (WGRAD) v2 = tc::mul2(v2, pw[2 * half + r]);
-              acc[c][i] = tc::fma2(v2, qs[h], acc[c][i]);
+            for (int i = 0; i < 4; ++i) {
+              const float v = sc[256 + quarter * 32 + 8 * i + lane / 4];
+              pw[i] = tc::pack2(v, v);
             }
           }
+          sc += first + sub * kBatchCols + (lane % 4) * 4;
+#pragma unroll
+          for (int c = 0; c < kBatches; ++c) {
+            if (c * 2 * kBatchCols + sub * kBatchCols < n) {
+              uint32_t v[32];
+              tc::ld_16x32(lane_base + b * MAXN + c * 2 * kBatchCols, v);
+              tc::ld_16x32(lane_base + b * MAXN + c * 2 * kBatchCols + (16u << 16), v + 16);
+              const float4 q4[2] = {*reinterpret_cast<const float4*>(sc + c * 2 * kBatchCols),
+                                    *reinterpret_cast<const float4*>(sc + c * 2 * kBatchCols + 16)};
+              tc::wait_ld();
+              // acc[c][8 * up + 2 * h + r]: rows 16 * up + 8 * r + lane / 4, columns 8 * h + 2 * (lane % 4), +1
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const uint64_t qs = h % 2 == 0 ? tc::pack2(q4[h / 2].x, q4[h / 2].y) : tc::pack2(q4[h / 2].z, q4[h / 2].w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int up = i / 2, r = i % 2;
+                  uint64_t v2 = tc::pack2(v[16 * up + 4 * h + 2 * r], v[16 * up + 4 * h + 2 * r + 1]);
+                  if (WGRAD) v2 = tc::mul2(v2, pw[i]);
+                  acc[c][8 * up + 2 * h + r] = tc::fma2(v2, qs, acc[c][8 * up + 2 * h + r]);
+                }
+              }
+            }
+          }
+          tc::fence_before();
         }
-        tc::fence_before();
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(&s.scale_empty[sl]);
-          const uint32_t bar = ptx::smem_addr(&s.acc_empty[b]);
-          if (CTAS == 2) tc::mbar_arrive_cluster(tc::map_to_rank(bar, 0));
-          else ptx::mbar_arrive(&s.acc_empty[b]);
+          if (n > 0) {
+            if (CTAS == 2) tc::mbar_arrive_cluster_relaxed(tc::map_to_rank(ptx::smem_addr(&s.acc_empty[half][b]), 0));
+            else ptx::mbar_arrive(&s.acc_empty[half][b]);
+          }
         }
       }
       if (!ok) break;
 
-      const int col0 = tile.p0 + quarter * 32;             // the warp's first column of out
-      if (WGRAD && p.out_fp32) {
-        float* out = static_cast<float*>(p.out) + (static_cast<int64_t>(tile.expert) * p.q_rows + tile.q0) * p.p_rows;
+      const Tile tile = T::get(p, s, t, rank);
+      const int col0 = tile.p0 + quarter * 32;              // the warp's first column of out
+      const int64_t row0 = (WGRAD ? static_cast<int64_t>(tile.expert) * p.q_rows : 0) + tile.q0;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int chunk = 2 * c + group;
-          if (chunk >= chunks) break;
+      for (int c = 0; c < kBatches; ++c) {
+        const int col = c * 2 * kBatchCols + sub * kBatchCols;
+        if (col >= n) break;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int half = i / 4, h = i / 2 % 2, r = i % 2;
-            const int col = col0 + 16 * half + 8 * r + lane / 4;
-            const int row = chunk * 16 + 8 * h + 2 * (lane % 4);
-            const float2 v = tc::unpack2(acc[c][i]);
-            if (col < p.p_rows) {
-              float* o = out + static_cast<int64_t>(row) * p.p_rows + col;
-              if (row < tile.q_valid) *o = p.accumulate ? *o + v.x : v.x;
-              if (row + 1 < tile.q_valid) o[p.p_rows] = p.accumulate ? o[p.p_rows] + v.y : v.y;
+        for (int h = 0; h < 4; ++h) {
+          const int row = first + col + 8 * h;              // of the tile; 8 of them
+          if (WGRAD && p.out_fp32) {
+            float* out = static_cast<float*>(p.out) + row0 * p.p_rows;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 v = tc::unpack2(acc[c][8 * (i / 2) + 2 * h + i % 2]);
+              const int oc = col0 + 8 * i + lane / 4, r = row + 2 * (lane % 4);
+              float* o = out + static_cast<int64_t>(r) * p.p_rows + oc;
+              if (oc < p.p_rows && r < tile.q_valid) *o = p.accumulate ? *o + v.x : v.x;
+              if (oc < p.p_rows && r + 1 < tile.q_valid) o[p.p_rows] = p.accumulate ? o[p.p_rows] + v.y : v.y;
             }
+            continue;
           }
-        }
-        continue;
-      }
-      uint16_t* out = static_cast<uint16_t*>(p.out) +
-                      ((WGRAD ? static_cast<int64_t>(tile.expert) * p.q_rows : 0) + tile.q0) * p.p_rows;
+          uint32_t v[4];
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int chunk = 2 * c + group;
-        if (chunk >= chunks) break;
-        uint32_t v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = tc::unpack2(acc[c][i]);
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(f.x, f.y);
-          v[i] = *reinterpret_cast<const uint32_t*>(&h2);
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = tc::unpack2(acc[c][8 * (i / 2) + 2 * h + i % 2]);
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(f.x, f.y);
+            v[i] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          // four matrices of 8 columns of out, transposed to 8 rows of 64 bytes
+          tc::stmatrix_x4_trans(ptx::smem_addr(stage) + (lane % 8) * kOutPitch + (lane / 8) * 16, v[0], v[1], v[2], v[3]);
+          __syncwarp();
+          const int r = row + lane / 4, oc = col0 + (lane % 4) * 8;
+          const uint4 w = ptx::ld_shared_v4(stage + lane / 4 * kOutPitch + (lane % 4) * 16);
+          if (r < tile.q_valid && oc < p.p_rows) ptx::st_v4(static_cast<uint16_t*>(p.out) + (row0 + r) * p.p_rows + oc, w);
+          __syncwarp();
         }
-        // matrices: 8 columns of out each, for the 8 rows of one h
-        const uint32_t addr = ptx::smem_addr(stage) + (lane % 8) * kOutPitch + (lane / 8) * 16;
-        tc::stmatrix_x4_trans(addr, v[0], v[1], v[4], v[5]);
-        tc::stmatrix_x4_trans(addr + 8 * kOutPitch, v[2], v[3], v[6], v[7]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = i * 8 + lane / 4, col = col0 + (lane % 4) * 8;
-          const uint4 w = ptx::ld_shared_v4(stage + row * kOutPitch + (lane % 4) * 16);
-          if (chunk * 16 + row < tile.q_valid && col < p.p_rows)
-            ptx::st_v4(out + static_cast<int64_t>(chunk * 16 + row) * p.p_rows + col, w);
-        }
-        __syncwarp();
       }
       if (!WGRAD && tile.last_q) {
-        // gap rows of the segment: zeros, the two groups in turn
+        // gap rows of the segment: zeros, the four warps of the same columns in turn
         const int64_t end = min64(p.expert_offset[tile.expert + 1], p.capacity);
-        const int col = col0 + (lane % 4) * 8;
-        if (col < p.p_rows)
-          for (int64_t r = static_cast<int64_t>(tile.q0) + tile.q_valid + group * 8 + lane / 4; r < end; r += 16)
-            ptx::st_v4(static_cast<uint16_t*>(p.out) + r * p.p_rows + col, make_uint4(0, 0, 0, 0));
+        const int oc = col0 + (lane % 4) * 8;
+        if (oc < p.p_rows)
+          for (int64_t r = static_cast<int64_t>(tile.q0) + tile.q_valid + ew / 4 * 8 + lane / 4; r < end; r += 32)
+            ptx::st_v4(static_cast<uint16_t*>(p.out) + r * p.p_rows + oc, make_uint4(0, 0, 0, 0));
       }
     }
   }

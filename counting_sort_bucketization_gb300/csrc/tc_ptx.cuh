@@ -27,8 +27,11 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+// Arrive on a mbarrier of the cluster without release semantics: the thread only
+// signals that its tensor-memory loads are done (tcgen05.wait::ld has returned).
+// A release at cluster scope would first wait for all its outstanding stores.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // ------------------------------------------------------------- registers
@@ -39,6 +42,28 @@ __device__ __forceinline__ void reg_inc() {
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ------------------------------------------------------------- waits
+// Like ptx::mbar_wait_parity_bounded, but each try may sleep for up to 20 us: few
+// instructions are issued (and the timer is seldom read) while nothing happens.
+__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(ptx::smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait_sleep(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!mbar_try_wait_sleep(bar, parity))
+    if (ptx::globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
 }
 
 // ------------------------------------------------------------- TMA loads
@@ -64,15 +89,6 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, int
   }
 }
 
-// 4-byte copy to shared memory; zero when !in.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
-}
-// Arrive on `bar` once this thread's cp.async so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
-}
-
 // ------------------------------------------------------------- tensor memory
 template <int CTAS>
 __device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t cols) {
@@ -95,13 +111,16 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// 16 lanes x 16 fp32 columns.  Lane j of the warp gets, for h = 0, 1 (8-column
-// halves): v[4h], v[4h+1] = row j/4, columns 8h + 2(j%4), +1; v[4h+2], v[4h+3]
+// 16 lanes x 32 fp32 columns.  Lane j of the warp gets, for each group h of 8
+// columns: v[4h], v[4h+1] = row j/4, columns 8h + 2(j%4), +1; v[4h+2], v[4h+3]
 // the same columns of row j/4 + 8.
-__device__ __forceinline__ void ld_16x16(uint32_t addr, uint32_t* v) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "r"(addr));
+__device__ __forceinline__ void ld_16x32(uint32_t addr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr));
 }
 
 // ------------------------------------------------------------- MMA
