@@ -20,10 +20,10 @@
 //   warp 0      TMA loads of P and Q tiles (128-byte rows, one k-block wide)
 //   warp 1      tcgen05.mma, 4 per k-block, into one of NBUF tensor-memory buffers
 //   warps 2-3   the k-block's scales to shared memory
-//   warps 4-19  tensor memory -> fp32 sums; at the tile's end bf16 (fp32) rows out
+//   warps 4-11  tensor memory -> fp32 sums; at the tile's end bf16 (fp32) rows out
 //
-// More than 128 columns are two accumulators, each with its own barriers and 8
-// of the 16 epilogue warps: the tensor core fills one while the other is read.
+// More than 128 columns are two accumulators, each with its own barriers and 4
+// of the 8 epilogue warps: the tensor core fills one while the other is read.
 //
 // One persistent CTA (or pair: CTAS == 2, one 256-row MMA over two SMs, each
 // loading half of Q) per SM walks the tiles of all experts.  All sums are fp32;
@@ -43,37 +43,35 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kEpilogueWarps = 16;
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
 constexpr int kHalfCols = 128;                     // columns of an accumulator
 constexpr int kBatchCols = 32;                     // columns a warp loads at a time
-constexpr int kBatches = 2;                        // of a warp: 8 warps, 4 of them side by side in rows
+constexpr int kBatches = kHalfCols / kBatchCols;
 constexpr int kKBlock = 128;                       // values (and bytes) of K in a scale block
 constexpr int kPRows = 128;                        // accumulator rows of a CTA
 constexpr int kPBytes = kPRows * kKBlock;
 constexpr int kQBytes = 128 * kKBlock;             // Q rows a CTA holds at most: 128
 constexpr int kStageBytes = kPBytes + kQBytes;
 constexpr int kStages = 6;
-constexpr int kScaleSlots = 6;
-constexpr int kSlotWords = 256 + kPRows;           // Q scales, then P scales (forward: one word)
-constexpr int kOutPitch = 80;                      // bytes; 64 of data, conflict-free for stmatrix
+constexpr int kSlotWords = kHalfCols + kPRows;     // scales of an accumulator's columns, then (gradient) of its rows
+constexpr int kOutPitch = 96;                      // bytes; 64 of data, 4 rows' 32-byte pieces in different banks
 constexpr int kOutBytes = 8 * kOutPitch;           // a warp's 8 rows x 32 columns of bf16
 constexpr int kTmemCols = 512;
-constexpr int kScaleThreads = 64;
-// Registers a thread: each SM quarter holds 4 epilogue warps and one other.
-constexpr int kLaunchRegs = 96, kEpilogueRegs = 104, kOtherRegs = 64;
-static_assert(512 * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split above the launch's total");
+// Registers a thread: 128 sums, two batches of tensor memory in flight.
+constexpr int kLaunchRegs = 168, kEpilogueRegs = 224, kOtherRegs = 56;
+static_assert(256 * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split above the launch's total");
 
 struct Smem {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
-  alignas(16) float scale[kScaleSlots][kSlotWords];
+  alignas(16) float scale[2][4][kSlotWords];       // [half][buffer]
   alignas(16) uint8_t out[kEpilogueWarps][kOutBytes];
   int tile_end[MOE_MAX_EXPERTS];                   // tiles of experts 0..e
   int seg_start[MOE_MAX_EXPERTS];
   int seg_count[MOE_MAX_EXPERTS];
   uint64_t full[kStages], empty[kStages];
-  uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
-  uint64_t acc_full[2][4], acc_empty[2][4];        // [half][buffer]
+  uint64_t acc_full[2][4], acc_empty[2][4];        // [half][buffer]; full: product and scales are there
+  uint64_t scale_empty[2][4];
   uint32_t tmem;
   int warp_sum[kThreads / 32];
 };
@@ -128,10 +126,20 @@ struct Tiling {
   }
 };
 
-// Place of column j's scale: a lane reads the four it needs of 16 columns as one vector.
+// Place of column j's scale: a lane reads the eight it needs of 32 columns (j % 4
+// is the same) as two vectors.
 __device__ __forceinline__ int scale_place(int j) {
-  return (j & ~15) + ((j & 7) >> 1) * 4 + ((j & 8) >> 3) * 2 + (j & 1);
+  return (j & ~31) + ((j & 16) >> 4) * 16 + (j & 3) * 4 + ((j & 15) >> 2);
 }
+
+// Position in a ring of N buffers, and the parity of the phase it is in.
+template <int N>
+struct Ring {
+  uint32_t i = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) i = 0, phase ^= 1;
+  }
+};
 
 // The whole warp waits, and leaves together (tcgen05.ld needs all lanes).
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
@@ -140,8 +148,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64
 
 template <int CTAS, int MAXN, bool WGRAD>
 __global__ void __launch_bounds__(kThreads, 1)
-expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q64,
-                   const __grid_constant__ CUtensorMap map_q16, const GemmParams p) {
+expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                   const GemmParams p) {
   constexpr int NBUF = kTmemCols / MAXN;
   static_assert(NBUF <= 4 && (MAXN <= kHalfCols || CTAS == 2), "tensor memory and shared memory of Q");
   using T = Tiling<CTAS, MAXN, WGRAD>;
@@ -154,20 +162,16 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 
   if (threadIdx.x == 0) {
     tc::prefetch_map(&map_p);
-    tc::prefetch_map(&map_q64);
-    tc::prefetch_map(&map_q16);
+    tc::prefetch_map(&map_q);
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
       ptx::mbar_init(&s.empty[i], 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      ptx::mbar_init(&s.scale_full[i], kScaleThreads);
-      ptx::mbar_init(&s.scale_empty[i], kEpilogueWarps);
-    }
     for (int i = 0; i < NBUF; ++i)
       for (int h = 0; h < 2; ++h) {
-        ptx::mbar_init(&s.acc_full[h][i], 1);
+        ptx::mbar_init(&s.acc_full[h][i], 2);      // the commit, and the scales' warp
         ptx::mbar_init(&s.acc_empty[h][i], kEpilogueWarps / 2 * CTAS);
+        ptx::mbar_init(&s.scale_empty[h][i], kEpilogueWarps / 2);
       }
     ptx::fence_mbar_init();
   }
@@ -222,79 +226,99 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 
   if (warp < 4) {
     tc::reg_dec<kOtherRegs>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---- loads ---------------------------------------------------------
-      uint32_t it = 0;
+      // The warp stays together so that addresses live in uniform registers; one
+      // lane issues.
+      Ring<kStages> ring;
+      uint32_t loads = 0;
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = T::get(p, s, t, rank);
-        const uint32_t bytes = CTAS * kPBytes + (tile.n[0] + tile.n[1]) * kKBlock;
-        for (int kb = 0; kb < tile.kblocks; ++kb, ++it) {
-          const uint32_t st = it % kStages;
-          if (!(ok = tc::mbar_wait(&s.empty[st], (it / kStages & 1) ^ 1, p.wait_ns))) break;
-          if (leader) ptx::mbar_arrive_expect_tx(&s.full[st], bytes + (it == 0 ? p.extra_tx : 0));
-          uint32_t bar = ptx::smem_addr(&s.full[st]);
-          if (CTAS == 2) bar = tc::map_to_rank(bar, 0);
-          const uint32_t dst = ptx::smem_addr(s.stage[st]);
-          const int x = tile.k0 + kb * kKBlock;
-          tc::load_box<CTAS>(dst, &map_p, x, tile.p0, WGRAD ? 0 : tile.expert, bar);
-          // the columns of each accumulator, half of them by each CTA of a pair
+        // Q rows of each accumulator, an equal share by each CTA of a pair, in whole boxes
+        int q[CTAS], boxes[CTAS], all = 0;
 #pragma unroll
-          for (int h = 0; h < CTAS; ++h) {
-            const int rows = tile.n[h] / CTAS;
-            const int q = tile.q0 + (h == 0 ? 0 : tile.n[0]) + static_cast<int>(rank) * rows;
-            const uint32_t to = dst + kPBytes + h * (kHalfCols / CTAS) * kKBlock;
-            int r = 0;
-            for (; r + 64 <= rows; r += 64) tc::load_box<CTAS>(to + r * kKBlock, &map_q64, x, q + r, 0, bar);
-            for (; r < rows; r += 16) tc::load_box<CTAS>(to + r * kKBlock, &map_q16, x, q + r, 0, bar);
+        for (int h = 0; h < CTAS; ++h) {
+          const int rows = tile.n[h] / CTAS;
+          q[h] = tile.q0 + (h == 0 ? 0 : tile.n[0]) + static_cast<int>(rank) * rows;
+          boxes[h] = ceil_div(rows, p.q_box);
+          all += boxes[h];
+        }
+        const uint32_t bytes = CTAS * (kPBytes + all * p.q_box * kKBlock);
+        for (int kb = 0; kb < tile.kblocks; ++kb) {
+          if (!(ok = wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns))) break;
+          if (tc::elect_one()) {
+            if (leader) ptx::mbar_arrive_expect_tx(&s.full[ring.i], bytes + (loads == 0 ? p.extra_tx : 0));
+            uint32_t bar = ptx::smem_addr(&s.full[ring.i]);
+            if (CTAS == 2) bar = tc::map_to_rank(bar, 0);
+            const uint32_t dst = ptx::smem_addr(s.stage[ring.i]);
+            const int x = tile.k0 + kb * kKBlock;
+            tc::load_box<CTAS>(dst, &map_p, x, tile.p0, WGRAD ? 0 : tile.expert, bar);
+#pragma unroll
+            for (int h = 0; h < CTAS; ++h)
+              for (int i = 0; i < boxes[h]; ++i)
+                tc::load_box<CTAS>(dst + kPBytes + (h * (kHalfCols / CTAS) + i * p.q_box) * kKBlock, &map_q, x,
+                                   q[h] + i * p.q_box, 0, bar);
           }
+          __syncwarp();
+          ring.next();
+          ++loads;
         }
       }
       // Every stage handed back: no copy or remote arrival is left in flight.
-      for (uint32_t i = 0; i < kStages; ++i, ++it)
-        if (it >= kStages) ok &= tc::mbar_wait(&s.empty[it % kStages], (it / kStages & 1) ^ 1, p.wait_ns);
-    } else if (warp == 1 && lane == 0 && leader) {
+      for (uint32_t i = 0; i < kStages; ++i, ++loads, ring.next())
+        if (loads >= kStages) ok &= wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns);
+    } else if (warp == 1 && leader) {
       // ---- MMA -----------------------------------------------------------
-      uint32_t it = 0, used[2] = {0, 0};
+      Ring<kStages> ring;
+      Ring<NBUF> buf[2];
+      uint32_t used[2] = {0, 0};
+      const uint64_t p_desc = tc::operand_desc(ptx::smem_addr(s.stage[0]));
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = T::get(p, s, t, rank);
-        for (int kb = 0; kb < tile.kblocks && ok; ++kb, ++it) {
-          const uint32_t st = it % kStages;
-          if (!(ok = tc::mbar_wait(&s.full[st], it / kStages & 1, p.wait_ns))) break;
-          const uint64_t a = tc::operand_desc(ptx::smem_addr(s.stage[st]));
+        const uint32_t idesc[2] = {tc::instr_desc(kPRows * CTAS, tile.n[0]), tc::instr_desc(kPRows * CTAS, tile.n[1])};
+        for (int kb = 0; kb < tile.kblocks && ok; ++kb) {
+          if (!(ok = wait_warp(&s.full[ring.i], ring.phase, p.wait_ns))) break;
+          const uint64_t a = p_desc + ring.i * (kStageBytes >> 4);
 #pragma unroll
           for (int h = 0; h < CTAS; ++h) {
-            if (tile.n[h] == 0) continue;
-            const uint32_t b = used[h] % NBUF;
-            if (!(ok = tc::mbar_wait(&s.acc_empty[h][b], (used[h] / NBUF & 1) ^ 1, p.wait_ns))) break;
-            ++used[h];
+            if (h == 1 && tile.n[1] == 0) continue;
+            if (!(ok = wait_warp(&s.acc_empty[h][buf[h].i], buf[h].phase ^ 1, p.wait_ns))) break;
             tc::fence_after();
-            const uint64_t q =
-                tc::operand_desc(ptx::smem_addr(s.stage[st]) + kPBytes + h * (kHalfCols / CTAS) * kKBlock);
-            const uint32_t idesc = tc::instr_desc(kPRows * CTAS, tile.n[h]);
+            if (tc::elect_one()) {
+              const uint64_t q = a + ((kPBytes + h * (kHalfCols / CTAS) * kKBlock) >> 4);
+              const uint32_t d = tmem + buf[h].i * MAXN + h * kHalfCols;
 #pragma unroll
-            for (int k = 0; k < kKBlock / 32; ++k)
-              tc::mma_e4m3<CTAS>(tmem + b * MAXN + h * kHalfCols, a + 2 * k, q + 2 * k, idesc, k > 0);
-            tc::commit<CTAS>(&s.acc_full[h][b]);
+              for (int k = 0; k < kKBlock / 32; ++k) tc::mma_e4m3<CTAS>(d, a + 2 * k, q + 2 * k, idesc[h], k > 0);
+              tc::commit<CTAS>(&s.acc_full[h][buf[h].i]);
+            }
+            __syncwarp();
+            buf[h].next();
+            ++used[h];
           }
-          if (ok) tc::commit<CTAS>(&s.empty[st]);
+          if (ok && tc::elect_one()) tc::commit<CTAS>(&s.empty[ring.i]);
+          __syncwarp();
+          ring.next();
         }
       }
+#pragma unroll
       for (int h = 0; h < 2; ++h)   // the epilogues' last (remote) arrivals
-        for (uint32_t i = 0; i < NBUF; ++i, ++used[h])
-          if (used[h] >= NBUF)
-            ok &= tc::mbar_wait(&s.acc_empty[h][used[h] % NBUF], (used[h] / NBUF & 1) ^ 1, p.wait_ns);
+        for (uint32_t i = 0; i < NBUF; ++i, ++used[h], buf[h].next())
+          if (used[h] >= NBUF) ok &= wait_warp(&s.acc_empty[h][buf[h].i], buf[h].phase ^ 1, p.wait_ns);
     } else if (warp >= 2) {
       // ---- scales --------------------------------------------------------
-      // Through registers, kAhead k-blocks ahead; the forward product's P scale is
-      // one number a k-block and goes into the Q scales here.
-      constexpr int kAhead = 3, kQ = MAXN / kScaleThreads, kP = WGRAD ? kPRows / kScaleThreads : 1;
-      const int j0 = static_cast<int>(threadIdx.x) - 64;
-      uint32_t it = 0;
+      // Warp 2 + h brings those of accumulator h, through registers and kAhead
+      // k-blocks ahead; the forward product's P scale is one number a k-block and
+      // goes into the Q scales here.
+      constexpr int kAhead = 3, kQ = kHalfCols / 32, kP = WGRAD ? kPRows / 32 : 1;
+      const int half = warp - 2;
+      Ring<NBUF> ring;
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = T::get(p, s, t, rank);
+        if ((half == 0 ? tile.n[0] : tile.n[1]) == 0) continue;
         const int64_t kb0 = tile.k0 / kKBlock;
+        const int j0 = (half == 0 ? 0 : tile.n[0]) + lane;
         const float* qs = p.q_sf + kb0 * p.q_sf_pitch + tile.q0 + j0;
-        const float* ps = WGRAD ? p.p_sf + kb0 * p.p_rows + tile.p0 + j0
+        const float* ps = WGRAD ? p.p_sf + kb0 * p.p_rows + tile.p0 + lane
                                 : p.p_sf + (static_cast<int64_t>(tile.expert) * ceil_div(p.p_rows, kKBlock) +
                                             tile.p0 / kKBlock) * p.kblocks;
         float q[kAhead][kQ], w[kAhead][kP];
@@ -302,11 +326,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
           const bool in = kb < tile.kblocks;
 #pragma unroll
           for (int i = 0; i < kQ; ++i)
-            qv[i] = in && j0 + i * kScaleThreads < tile.q_valid ? __ldg(qs + kb * p.q_sf_pitch + i * kScaleThreads) : 0.0f;
+            qv[i] = in && j0 + i * 32 < tile.q_valid ? __ldg(qs + kb * p.q_sf_pitch + i * 32) : 0.0f;
 #pragma unroll
           for (int i = 0; i < kP; ++i)
-            wv[i] = !in || tile.p0 + (WGRAD ? j0 + i * kScaleThreads : 0) >= p.p_rows ? 0.0f
-                    : WGRAD ? __ldg(ps + static_cast<int64_t>(kb) * p.p_rows + i * kScaleThreads) : __ldg(ps + kb);
+            wv[i] = !in || tile.p0 + (WGRAD ? lane + i * 32 : 0) >= p.p_rows ? 0.0f
+                    : WGRAD ? __ldg(ps + static_cast<int64_t>(kb) * p.p_rows + i * 32) : __ldg(ps + kb);
         };
 #pragma unroll
         for (int d = 0; d < kAhead; ++d) fetch(d, q[d], w[d]);
@@ -314,17 +338,17 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 #pragma unroll
           for (int d = 0; d < kAhead; ++d) {
             if (kb + d >= tile.kblocks) break;
-            const uint32_t sl = it % kScaleSlots;
-            if (!(ok = tc::mbar_wait(&s.scale_empty[sl], (it / kScaleSlots & 1) ^ 1, p.wait_ns))) break;
-            ++it;
+            if (!(ok = wait_warp(&s.scale_empty[half][ring.i], ring.phase ^ 1, p.wait_ns))) break;
+            float* to = s.scale[half][ring.i];
 #pragma unroll
-            for (int i = 0; i < kQ; ++i)
-              s.scale[sl][scale_place(j0 + i * kScaleThreads)] = WGRAD ? q[d][i] : q[d][i] * w[d][0];
+            for (int i = 0; i < kQ; ++i) to[scale_place(lane + i * 32)] = WGRAD ? q[d][i] : q[d][i] * w[d][0];
             if (WGRAD) {
 #pragma unroll
-              for (int i = 0; i < kP; ++i) s.scale[sl][256 + j0 + i * kScaleThreads] = w[d][i];
+              for (int i = 0; i < kP; ++i) to[kHalfCols + lane + i * 32] = w[d][i];
             }
-            ptx::mbar_arrive(&s.scale_full[sl]);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.acc_full[half][ring.i]);
+            ring.next();
             fetch(kb + d + kAhead, q[d], w[d]);
           }
         }
@@ -332,13 +356,15 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     }
   } else {
     // ---- epilogue --------------------------------------------------------
-    // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of one accumulator:
-    // 32 columns, and the 32 columns 64 further on.
+    // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of one accumulator, 32
+    // columns at a time; the next batch is on its way while one is added.
     tc::reg_inc<kEpilogueRegs>();
-    const int ew = warp - 4, quarter = warp % 4, half = ew / 8, sub = ew / 4 % 2;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalfCols + sub * kBatchCols;
+    const int ew = warp - 4, quarter = warp % 4, half = ew / 4;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalfCols;
     uint8_t* stage = s.out[ew];
-    uint32_t it = 0, used = 0;
+    uint32_t freed = ptx::smem_addr(&s.acc_empty[half][0]);   // the leader's barriers
+    if (CTAS == 2) freed = tc::map_to_rank(freed, 0);
+    Ring<NBUF> buf;
     for (int t = first_tile; t < tiles && ok; t += step) {
       // Only these three values stay in registers over the k-blocks.
       int n, first, kblocks;
@@ -346,63 +372,58 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         const Tile tile = T::get(p, s, t, rank);
         n = half == 0 ? tile.n[0] : tile.n[1];
         first = half == 0 ? 0 : tile.n[0];                  // column of the tile the accumulator starts at
-        kblocks = tile.kblocks;
+        kblocks = n > 0 ? tile.kblocks : 0;
       }
-      uint64_t acc[kBatches][16];
+      // acc[c][16 * up + 2 * i + r]: row 16 * up + 8 * r + lane / 4, column 32 * c + 4 * i + lane % 4
+      float acc[kBatches][32];
 #pragma unroll
       for (int c = 0; c < kBatches; ++c)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[c][i] = 0;
-      for (int kb = 0; kb < kblocks; ++kb, ++it) {
-        const uint32_t b = used % NBUF, sl = it % kScaleSlots;
-        if (!(ok = wait_warp(&s.scale_full[sl], it / kScaleSlots & 1, p.wait_ns))) break;
-        if (n > 0) {
-          if (!(ok = wait_warp(&s.acc_full[half][b], used / NBUF & 1, p.wait_ns))) break;
-          ++used;
-          tc::fence_after();
-          const float* sc = s.scale[sl];
-          uint64_t pw[4];
-          if (WGRAD) {
+        for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (!(ok = wait_warp(&s.acc_full[half][buf.i], buf.phase, p.wait_ns))) break;
+        tc::fence_after();
+        const float* sc = s.scale[half][buf.i];
+        float pw[4];
+        if (WGRAD) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float v = sc[256 + quarter * 32 + 8 * i + lane / 4];
-              pw[i] = tc::pack2(v, v);
+          for (int i = 0; i < 4; ++i) pw[i] = sc[kHalfCols + quarter * 32 + 8 * i + lane / 4];
+        }
+        sc += (lane % 4) * 4;
+        const uint32_t from = lane_base + buf.i * MAXN;
+        float v[2][32];
+        tc::ld_16x32(from, v[0]);
+        tc::ld_16x32(from + (16u << 16), v[0] + 16);
+#pragma unroll
+        for (int c = 0; c < kBatches; ++c) {
+          if (c * kBatchCols < n) {
+            const float4 lo = *reinterpret_cast<const float4*>(sc + c * kBatchCols);
+            const float4 hi = *reinterpret_cast<const float4*>(sc + c * kBatchCols + 16);
+            tc::wait_ld();
+            if (c + 1 < kBatches && (c + 1) * kBatchCols < n) {
+              tc::ld_16x32(from + (c + 1) * kBatchCols, v[(c + 1) % 2]);
+              tc::ld_16x32(from + (c + 1) * kBatchCols + (16u << 16), v[(c + 1) % 2] + 16);
+            } else {   // everything is in registers: the tensor core may have the buffer back
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
             }
-          }
-          sc += first + sub * kBatchCols + (lane % 4) * 4;
+            const float q[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int c = 0; c < kBatches; ++c) {
-            if (c * 2 * kBatchCols + sub * kBatchCols < n) {
-              uint32_t v[32];
-              tc::ld_16x32(lane_base + b * MAXN + c * 2 * kBatchCols, v);
-              tc::ld_16x32(lane_base + b * MAXN + c * 2 * kBatchCols + (16u << 16), v + 16);
-              const float4 q4[2] = {*reinterpret_cast<const float4*>(sc + c * 2 * kBatchCols),
-                                    *reinterpret_cast<const float4*>(sc + c * 2 * kBatchCols + 16)};
-              tc::wait_ld();
-              // acc[c][8 * up + 2 * h + r]: rows 16 * up + 8 * r + lane / 4, columns 8 * h + 2 * (lane % 4), +1
+            for (int up = 0; up < 2; ++up)
 #pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                const uint64_t qs = h % 2 == 0 ? tc::pack2(q4[h / 2].x, q4[h / 2].y) : tc::pack2(q4[h / 2].z, q4[h / 2].w);
+              for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int up = i / 2, r = i % 2;
-                  uint64_t v2 = tc::pack2(v[16 * up + 4 * h + 2 * r], v[16 * up + 4 * h + 2 * r + 1]);
-                  if (WGRAD) v2 = tc::mul2(v2, pw[i]);
-                  acc[c][8 * up + 2 * h + r] = tc::fma2(v2, qs, acc[c][8 * up + 2 * h + r]);
+                for (int r = 0; r < 2; ++r) {
+                  float x = v[c % 2][16 * up + 2 * i + r];
+                  if (WGRAD) x *= pw[2 * up + r];
+                  acc[c][16 * up + 2 * i + r] = fmaf(x, q[i], acc[c][16 * up + 2 * i + r]);
                 }
-              }
-            }
           }
-          tc::fence_before();
         }
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&s.scale_empty[sl]);
-          if (n > 0) {
-            if (CTAS == 2) tc::mbar_arrive_cluster_relaxed(tc::map_to_rank(ptx::smem_addr(&s.acc_empty[half][b]), 0));
-            else ptx::mbar_arrive(&s.acc_empty[half][b]);
-          }
-        }
+        if (lane == 0) ptx::mbar_arrive(&s.scale_empty[half][buf.i]);
+        buf.next();
       }
       if (!ok) break;
 
@@ -411,32 +432,36 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       const int64_t row0 = (WGRAD ? static_cast<int64_t>(tile.expert) * p.q_rows : 0) + tile.q0;
 #pragma unroll
       for (int c = 0; c < kBatches; ++c) {
-        const int col = c * 2 * kBatchCols + sub * kBatchCols;
+        const int col = c * kBatchCols;
         if (col >= n) break;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int row = first + col + 8 * h;              // of the tile; 8 of them
+        for (int h = 0; h < 4; ++h) {                       // 8 columns of the accumulator: rows of out
+          const int row = first + col + 8 * h;
           if (WGRAD && p.out_fp32) {
             float* out = static_cast<float*>(p.out) + row0 * p.p_rows;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 v = tc::unpack2(acc[c][8 * (i / 2) + 2 * h + i % 2]);
-              const int oc = col0 + 8 * i + lane / 4, r = row + 2 * (lane % 4);
-              float* o = out + static_cast<int64_t>(r) * p.p_rows + oc;
-              if (oc < p.p_rows && r < tile.q_valid) *o = p.accumulate ? *o + v.x : v.x;
-              if (oc < p.p_rows && r + 1 < tile.q_valid) o[p.p_rows] = p.accumulate ? o[p.p_rows] + v.y : v.y;
+            for (int i = 0; i < 8; ++i) {
+              const int up = i / 4, r = i % 2, at = row + 4 * (i / 2 % 2) + lane % 4;
+              const int oc = col0 + 16 * up + 8 * r + lane / 4;
+              if (at < tile.q_valid && oc < p.p_rows) {
+                float* o = out + static_cast<int64_t>(at) * p.p_rows + oc;
+                const float v = acc[c][16 * up + 4 * h + i % 4];
+                *o = p.accumulate ? *o + v : v;
+              }
             }
             continue;
           }
-          uint32_t v[4];
+          // Lanes j and j ^ 4 hold rows k and k + 1 (k = j/4 even) and the rows 8 further
+          // on; they trade so that each has two neighbours: one 32-bit word of out.
+          const bool odd = (lane & 4) != 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = tc::unpack2(acc[c][8 * (i / 2) + 2 * h + i % 2]);
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(f.x, f.y);
-            v[i] = *reinterpret_cast<const uint32_t*>(&h2);
+          for (int i = 0; i < 4; ++i) {                     // up = i / 2, column 4 * (i % 2) + lane % 4
+            const float lo = acc[c][16 * (i / 2) + 4 * h + 2 * (i % 2)], hi = acc[c][16 * (i / 2) + 4 * h + 2 * (i % 2) + 1];
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 4);
+            const __nv_bfloat162 h2 = odd ? __floats2bfloat162_rn(other, hi) : __floats2bfloat162_rn(lo, other);
+            *reinterpret_cast<__nv_bfloat162*>(stage + (4 * (i % 2) + lane % 4) * kOutPitch + 32 * (i / 2) +
+                                               (odd ? 16 : 0) + lane / 8 * 4) = h2;
           }
-          // four matrices of 8 columns of out, transposed to 8 rows of 64 bytes
-          tc::stmatrix_x4_trans(ptx::smem_addr(stage) + (lane % 8) * kOutPitch + (lane / 8) * 16, v[0], v[1], v[2], v[3]);
           __syncwarp();
           const int r = row + lane / 4, oc = col0 + (lane % 4) * 8;
           const uint4 w = ptx::ld_shared_v4(stage + lane / 4 * kOutPitch + (lane % 4) * 16);
@@ -445,11 +470,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
       }
       if (!WGRAD && tile.last_q) {
-        // gap rows of the segment: zeros, the four warps of the same columns in turn
+        // gap rows of the segment: zeros, the two warps of the same columns in turn
         const int64_t end = min64(p.expert_offset[tile.expert + 1], p.capacity);
         const int oc = col0 + (lane % 4) * 8;
         if (oc < p.p_rows)
-          for (int64_t r = static_cast<int64_t>(tile.q0) + tile.q_valid + ew / 4 * 8 + lane / 4; r < end; r += 32)
+          for (int64_t r = static_cast<int64_t>(tile.q0) + tile.q_valid + half * 8 + lane / 4; r < end; r += 16)
             ptx::st_v4(static_cast<uint16_t*>(p.out) + r * p.p_rows + oc, make_uint4(0, 0, 0, 0));
       }
     }
@@ -518,7 +543,7 @@ cudaError_t launch(const CUtensorMap* maps, const GemmParams& p, cudaStream_t st
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], p);
+  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], p);
 }
 
 }  // namespace
@@ -538,13 +563,15 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream) {
   p.err = a.err;
   p.wait_ns = wait_config().limit_ns;
   p.extra_tx = wait_config().extra_tx;
-  CUtensorMap maps[3];
+  CUtensorMap maps[2];
   cudaError_t e = encode(&maps[0], a.w, a.width_in, a.width_out, a.num_experts, kPRows);
-  if (e == cudaSuccess) e = encode(&maps[1], a.x, a.width_in, a.capacity, 1, 64);
-  if (e == cudaSuccess) e = encode(&maps[2], a.x, a.width_in, a.capacity, 1, 16);
-  if (e != cudaSuccess) return e;
   // Rows an expert has in the mean: many fill the 256 columns of a pair's tile.
-  if (a.pairs / a.num_experts >= 192) return launch<2, 256, false>(maps, p, stream);
+  const int64_t mean = a.pairs / a.num_experts;
+  const bool pair = mean >= 192;
+  p.q_box = pair || mean >= 32 ? 64 : 16;
+  if (e == cudaSuccess) e = encode(&maps[1], a.x, a.width_in, a.capacity, 1, p.q_box);
+  if (e != cudaSuccess) return e;
+  if (pair) return launch<2, 256, false>(maps, p, stream);
   return launch<1, 128, false>(maps, p, stream);
 }
 
@@ -565,10 +592,10 @@ cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
   p.err = a.err;
   p.wait_ns = wait_config().limit_ns;
   p.extra_tx = wait_config().extra_tx;
-  CUtensorMap maps[3];
+  CUtensorMap maps[2];
   cudaError_t e = encode(&maps[0], a.x, a.sf_ld, a.width_in, 1, kPRows);
-  if (e == cudaSuccess) e = encode(&maps[1], a.w, a.sf_ld, a.width_out, 1, 64);
-  if (e == cudaSuccess) e = encode(&maps[2], a.w, a.sf_ld, a.width_out, 1, 16);
+  p.q_box = 64;
+  if (e == cudaSuccess) e = encode(&maps[1], a.w, a.sf_ld, a.width_out, 1, p.q_box);
   if (e != cudaSuccess) return e;
   return launch<2, 256, true>(maps, p, stream);
 }

@@ -213,6 +213,7 @@ struct GemmParams {
   int p_rows;                    // rows of P of an expert = columns (and pitch) of out
   int q_rows;                    // gradient: rows of Q
   int kblocks;                   // forward: k-blocks of a row
+  int q_box;                     // rows of Q a TMA load brings: 16 or 64
   int num_experts;
   const int32_t* expert_offset;
   const int32_t* expert_count;
