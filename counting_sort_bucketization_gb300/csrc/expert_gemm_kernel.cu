@@ -4,30 +4,36 @@
 //   forward (and input gradient)  out[r, o] = sum_b sx[b, r] sw[e, o/128, b] <x_r, w_o>_b
 //   weight gradient               dw[e, o, i] = sum_b sdy[b, o] sx[b, i] <dy_o, x_i>_b
 //
-// Both are D[p, q] = sum_b sp sq <P_p, Q_q>_b written to out[q * pitch + p]:
-// P = weights (forward) or x^T (gradient) gives the 128 accumulator rows of a
-// CTA, Q = receive rows or dy^T its columns.
-//
-// Why this orientation: the tensor core takes any multiple of 16 columns, so a
-// tile has as many columns as the segment has rows left and an expert with one
-// token does not pay for 128; and a CTA's 128 weight rows are one scale block, so
-// their scale is one number a k-block.
-//
 // A scale that changes every 128 values of K means the tensor core can sum one
 // k-block only.  Each k-block's product lands in tensor memory, and epilogue
 // warps add it, times its scales, to fp32 sums in registers:
 //
 //   warp 0      TMA loads of P and Q tiles (128-byte rows, one k-block wide)
-//   warp 1      tcgen05.mma, 4 per k-block, into one of NBUF tensor-memory buffers
+//   warp 1      tcgen05.mma, 4 per k-block and accumulator
 //   warps 2-3   the k-block's scales to shared memory
-//   warps 4-11  tensor memory -> fp32 sums; at the tile's end bf16 (fp32) rows out
+//   warps 4-11  tensor memory -> fp32 sums; at the tile's end rows of out
 //
-// More than 128 columns are two accumulators, each with its own barriers and 4
-// of the 8 epilogue warps: the tensor core fills one while the other is read.
+// D[p, q] = <P_p, Q_q>: P gives the 128 accumulator rows (tensor-memory lanes) of
+// a CTA, Q its columns.  A tile's columns are two accumulators, each with its own
+// buffers, barriers and 4 of the 8 epilogue warps: the tensor core fills one
+// while the other is read.  Three kinds:
 //
-// One persistent CTA (or pair: CTAS == 2, one 256-row MMA over two SMs, each
-// loading half of Q) per SM walks the tiles of all experts.  All sums are fp32;
-// the result is rounded once.
+//   kMany   P = receive rows, Q = weights; a pair of CTAs shares one 256 x 256 MMA,
+//           each loading half of Q.  A thread owns a receive row, and both scales
+//           of a k-block and 128-column block multiply to one number for it.
+//   kFew    P = weights, Q = receive rows; one CTA.  The tensor core takes any
+//           multiple of 16 columns, so an expert with one token does not pay for
+//           128.  Bound by the reading of the weights.
+//   kWgrad  P = x^T, Q = dy^T (so that columns of dw run along lanes); a pair.
+//
+// What bounds kMany: adding 256 columns of a k-block takes the epilogue warps
+// ~460 cycles (measured alone), about what the MMAs take (512).  Loading 64
+// columns of tensor memory at a time, without a second buffer of registers, is
+// faster than prefetching 32 (458 against 602 cycles), and a scale per row
+// beats one per column (610).
+//
+// One persistent CTA (or pair) per SM walks the tiles of all experts.  All sums
+// are fp32; the result is rounded once.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,34 +49,44 @@
 namespace moe {
 namespace {
 
+enum Kind { kMany, kFew, kWgrad };
+
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
-constexpr int kHalfCols = 128;                     // columns of an accumulator
-constexpr int kBatchCols = 32;                     // columns a warp loads at a time
-constexpr int kBatches = kHalfCols / kBatchCols;
 constexpr int kKBlock = 128;                       // values (and bytes) of K in a scale block
 constexpr int kPRows = 128;                        // accumulator rows of a CTA
 constexpr int kPBytes = kPRows * kKBlock;
-constexpr int kQBytes = 128 * kKBlock;             // Q rows a CTA holds at most: 128
+constexpr int kQBytes = 128 * kKBlock;             // a CTA loads at most 128 rows of Q
 constexpr int kStageBytes = kPBytes + kQBytes;
 constexpr int kStages = 6;
-constexpr int kSlotWords = kHalfCols + kPRows;     // scales of an accumulator's columns, then (gradient) of its rows
+constexpr int kBatchCols = 32;                     // columns of one tensor-memory load
+constexpr int kSlotWords = 128 + kPRows;           // scales of columns or rows, then (kWgrad) of rows
 constexpr int kOutPitch = 96;                      // bytes; 64 of data, 4 rows' 32-byte pieces in different banks
 constexpr int kOutBytes = 8 * kOutPitch;           // a warp's 8 rows x 32 columns of bf16
 constexpr int kTmemCols = 512;
-// Registers a thread: 128 sums, two batches of tensor memory in flight.
+// Registers a thread: 128 sums and 64 values of tensor memory.
 constexpr int kLaunchRegs = 168, kEpilogueRegs = 224, kOtherRegs = 56;
 static_assert(256 * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split above the launch's total");
 
+template <Kind KIND>
+struct Config {
+  static constexpr int kCtas = KIND == kFew ? 1 : 2;
+  static constexpr int kAccCols = KIND == kFew ? 64 : 128;     // columns of an accumulator
+  static constexpr int kTileCols = 2 * kAccCols;
+  static constexpr int kBuffers = kTmemCols / kTileCols;
+  static constexpr int kUnit = 16 * kCtas;                     // column granularity: each CTA of a pair holds n / 2 rows of Q
+  static constexpr int kQRows = kAccCols / kCtas;              // rows of Q of an accumulator a CTA loads at most
+};
+
 struct Smem {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
-  alignas(16) float scale[2][4][kSlotWords];       // [half][buffer]
+  alignas(16) float scale[2][4][kSlotWords];       // [accumulator][buffer]
   alignas(16) uint8_t out[kEpilogueWarps][kOutBytes];
   int tile_end[MOE_MAX_EXPERTS];                   // tiles of experts 0..e
   int seg_start[MOE_MAX_EXPERTS];
   int seg_count[MOE_MAX_EXPERTS];
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2][4], acc_empty[2][4];        // [half][buffer]; full: product and scales are there
+  uint64_t acc_full[2][4], acc_empty[2][4];        // full: product and scales are there
   uint64_t scale_empty[2][4];
   uint32_t tmem;
   int warp_sum[kThreads / 32];
@@ -82,51 +98,67 @@ static_assert(kSmemBytes <= 232448, "shared memory of one SM");
 struct Tile {
   int expert;
   int p0;          // first row of P for this CTA
+  int p_valid;     // rows of P that exist
   int q0;          // first row of Q
   int q_valid;     // rows of Q that exist
   int n[2];        // columns of the two accumulators; the second may have none
-  int k0;          // first k (forward 0, gradient: the segment's first row)
+  int k0;          // first k (kWgrad: the segment's first row)
   int kblocks;
-  bool last_q;     // the expert's last tile along Q
+  bool last;       // the expert's last tile along the receive rows
 };
 
 __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-template <int CTAS, int MAXN, bool WGRAD>
-struct Tiling {
-  static constexpr int kUnit = 16 * CTAS;   // column granularity: each CTA of a pair holds n / 2 rows of Q
+// Tiles along the receive rows (kWgrad: rows of dy) of an expert, and across.
+template <Kind KIND>
+__device__ __forceinline__ int row_tiles(const GemmParams& p, int count) {
+  return ceil_div(KIND == kWgrad ? p.dy_rows : count, KIND == kMany ? 256 : Config<KIND>::kTileCols);
+}
+template <Kind KIND>
+__device__ __forceinline__ int col_tiles(const GemmParams& p) {
+  return ceil_div(p.out_cols, KIND == kMany ? Config<KIND>::kTileCols : kPRows * Config<KIND>::kCtas);
+}
 
-  __device__ static int q_tiles(const GemmParams& p, int count) {
-    return WGRAD ? ceil_div(p.q_rows, MAXN) : ceil_div(count, MAXN);
+template <Kind KIND>
+__device__ __forceinline__ Tile get_tile(const GemmParams& p, const Smem& s, int t, int rank) {
+  using C = Config<KIND>;
+  int lo = 0, hi = p.num_experts - 1;     // first expert whose tiles end after t
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (s.tile_end[mid] > t) hi = mid; else lo = mid + 1;
   }
-  __device__ static Tile get(const GemmParams& p, const Smem& s, int t, uint32_t rank) {
-    int lo = 0, hi = p.num_experts - 1;     // first expert whose tiles end after t
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (s.tile_end[mid] > t) hi = mid; else lo = mid + 1;
-    }
-    const int first = lo == 0 ? 0 : s.tile_end[lo - 1];
-    const int count = s.seg_count[lo], nq = q_tiles(p, count);
-    const int local = t - first, q = local % nq, pt = local / nq;
-    const int q_rows = WGRAD ? p.q_rows : count;
-    // columns shared evenly over the tiles along Q
-    const int per = ceil_div(ceil_div(q_rows, nq), kUnit) * kUnit;
-    Tile r;
-    r.expert = lo;
-    r.p0 = (pt * CTAS + static_cast<int>(rank)) * kPRows;
-    r.q_valid = max(0, min(per, q_rows - q * per));
-    r.q0 = (WGRAD ? 0 : s.seg_start[lo]) + q * per;
-    const int n = max(kUnit, ceil_div(r.q_valid, kUnit) * kUnit);
-    r.n[0] = n <= kHalfCols ? n : ceil_div(n / 2, 32) * 32;
-    r.n[1] = n - r.n[0];
-    r.k0 = WGRAD ? s.seg_start[lo] : 0;
-    r.kblocks = WGRAD ? ceil_div(count, kKBlock) : p.kblocks;
-    r.last_q = q == nq - 1;
-    return r;
+  const int count = s.seg_count[lo], start = s.seg_start[lo], nr = row_tiles<KIND>(p, count);
+  const int local = t - (lo == 0 ? 0 : s.tile_end[lo - 1]);
+  const int row = local % nr, col = local / nr;
+  Tile r;
+  r.expert = lo;
+  r.last = row == nr - 1;
+  r.k0 = KIND == kWgrad ? start : 0;
+  r.kblocks = KIND == kWgrad ? ceil_div(count, kKBlock) : p.kblocks;
+  if (KIND == kMany) {
+    const int at = row * 256 + rank * kPRows;
+    r.p0 = start + at;
+    r.p_valid = max(0, min(kPRows, count - at));
+    r.q0 = col * C::kTileCols;
+    r.q_valid = min(C::kTileCols, p.out_cols - r.q0);
+  } else {
+    // columns shared evenly over the tiles along the rows
+    const int rows = KIND == kWgrad ? p.dy_rows : count;
+    const int per = ceil_div(ceil_div(rows, nr), C::kUnit) * C::kUnit;
+    r.p0 = (col * C::kCtas + rank) * kPRows;
+    r.p_valid = max(0, min(kPRows, p.out_cols - r.p0));
+    r.q0 = (KIND == kWgrad ? 0 : start) + row * per;
+    r.q_valid = max(0, min(per, rows - row * per));
   }
-};
+  // kMany: an accumulator is one scale block of the weights; else the two are of
+  // like size, the first in whole batches
+  const int n = max(C::kUnit, ceil_div(r.q_valid, C::kUnit) * C::kUnit);
+  r.n[0] = n <= C::kAccCols ? n : KIND == kMany ? C::kAccCols : ceil_div(n / 2, kBatchCols) * kBatchCols;
+  r.n[1] = n - r.n[0];
+  return r;
+}
 
-// Place of column j's scale: a lane reads the eight it needs of 32 columns (j % 4
+// Place of a column's scale: a lane reads the eight it needs of 32 columns (j % 4
 // is the same) as two vectors.
 __device__ __forceinline__ int scale_place(int j) {
   return (j & ~31) + ((j & 16) >> 4) * 16 + (j & 3) * 4 + ((j & 15) >> 2);
@@ -146,18 +178,115 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64
   return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, limit_ns));
 }
 
-template <int CTAS, int MAXN, bool WGRAD>
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Rows of out from sums whose thread owns a row (kMany).
+// acc[c][i]: columns 32 c + 2 i, +1 of the accumulator.
+__device__ __forceinline__ void store_rows(const GemmParams& p, const Tile& t, int row, int half, const uint64_t (*acc)[16]) {
+  const int oc = t.q0 + half * 128, n = half == 0 ? t.n[0] : t.n[1];
+  if (row >= t.p_valid || n == 0) return;
+  uint16_t* out = static_cast<uint16_t*>(p.out) + (static_cast<int64_t>(t.p0) + row) * p.out_cols + oc;
+  const int cols = p.out_cols - oc;
+  // 32-byte stores where rows allow: 16-byte ones write each sector in halves
+  const bool wide = p.out_cols % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = tc::unpack2(acc[c][8 * h + i]);
+        v[i] = pack_bf16(f.x, f.y);
+      }
+      const int at = 32 * c + 16 * h;
+      if (wide) {
+        if (at < cols) tc::st_v8(out + at, v);
+      } else {
+        if (at < cols) ptx::st_v4(out + at, make_uint4(v[0], v[1], v[2], v[3]));
+        if (at + 8 < cols) ptx::st_v4(out + at + 8, make_uint4(v[4], v[5], v[6], v[7]));
+      }
+    }
+}
+
+// Rows of out from sums whose columns are rows of out (kFew, kWgrad).
+// acc[c][8 * up + i]: rows 16 * up + lane / 4 and 8 further on of the warp's 32,
+// column 32 * c + 4 * i + lane % 4 of the accumulator.
+template <Kind KIND>
+__device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t, int quarter, int half, int lane,
+                                              uint8_t* stage, const uint64_t (*acc)[16]) {
+  using C = Config<KIND>;
+  const int n = half == 0 ? t.n[0] : t.n[1], first = half == 0 ? 0 : t.n[0];
+  const int col0 = t.p0 + quarter * 32;                     // the warp's first column of out
+  const int64_t row0 = (KIND == kWgrad ? static_cast<int64_t>(t.expert) * p.dy_rows : 0) + t.q0;
+#pragma unroll
+  for (int c = 0; c < C::kAccCols / kBatchCols; ++c) {
+    if (c * kBatchCols >= n) break;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {                           // 8 columns: rows of out
+      const int row = first + c * kBatchCols + 8 * h;
+      if (KIND == kWgrad && p.out_fp32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int up = i / 2, at = row + 4 * (i % 2) + lane % 4;
+          const float2 f = tc::unpack2(acc[c][8 * up + 2 * h + i % 2]);
+          const int oc = col0 + 16 * up + lane / 4;
+          if (at < t.q_valid) {
+            float* o = static_cast<float*>(p.out) + (row0 + at) * p.out_cols + oc;
+            if (oc < p.out_cols) o[0] = p.accumulate ? o[0] + f.x : f.x;
+            if (oc + 8 < p.out_cols) o[8] = p.accumulate ? o[8] + f.y : f.y;
+          }
+        }
+        continue;
+      }
+      // Lanes j and j ^ 4 hold rows k and k + 1 (k = j/4 even) and the rows 8 further
+      // on; they trade so that each has two neighbours: one 32-bit word of out.
+      const bool odd = (lane & 4) != 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {                         // up = i / 2, column 4 * (i % 2) + lane % 4
+        const float2 f = tc::unpack2(acc[c][8 * (i / 2) + 2 * h + i % 2]);
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? f.x : f.y, 4);
+        *reinterpret_cast<uint32_t*>(stage + (4 * (i % 2) + lane % 4) * kOutPitch + 32 * (i / 2) + (odd ? 16 : 0) +
+                                     lane / 8 * 4) = odd ? pack_bf16(other, f.y) : pack_bf16(f.x, other);
+      }
+      __syncwarp();
+      const int r = row + lane / 4, oc = col0 + (lane % 4) * 8;
+      const uint4 w = ptx::ld_shared_v4(stage + lane / 4 * kOutPitch + (lane % 4) * 16);
+      if (r < t.q_valid && oc < p.out_cols) ptx::st_v4(static_cast<uint16_t*>(p.out) + (row0 + r) * p.out_cols + oc, w);
+      __syncwarp();
+    }
+  }
+}
+
+// Alignment-gap rows of the expert's segment: zeros, 16 bytes a lane.
+template <Kind KIND>
+__device__ __forceinline__ void zero_gap(const GemmParams& p, const Smem& s, const Tile& t, int rank, int ew, int lane) {
+  using C = Config<KIND>;
+  const int64_t end = min64(p.expert_offset[t.expert + 1], p.capacity);
+  int64_t r = static_cast<int64_t>(s.seg_start[t.expert]) + s.seg_count[t.expert];
+  // the tile's columns of out, a share of the rows for each warp (of both CTAs)
+  const int c0 = KIND == kMany ? t.q0 : t.p0, cols = KIND == kMany ? t.q_valid : t.p_valid;
+  const int warps = KIND == kMany ? C::kCtas * kEpilogueWarps : kEpilogueWarps;
+  for (r += KIND == kMany ? rank * kEpilogueWarps + ew : ew; r < end; r += warps)
+    for (int c = lane * 8; c < cols; c += 256)
+      ptx::st_v4(static_cast<uint16_t*>(p.out) + r * p.out_cols + c0 + c, make_uint4(0, 0, 0, 0));
+}
+
+template <Kind KIND>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                    const GemmParams p) {
-  constexpr int NBUF = kTmemCols / MAXN;
-  static_assert(NBUF <= 4 && (MAXN <= kHalfCols || CTAS == 2), "tensor memory and shared memory of Q");
-  using T = Tiling<CTAS, MAXN, WGRAD>;
+  using C = Config<KIND>;
+  constexpr int CTAS = C::kCtas, NBUF = C::kBuffers;
+  static_assert(NBUF <= 4 && 2 * C::kQRows * kKBlock <= kQBytes, "buffers of tensor and shared memory");
   extern __shared__ uint8_t smem_raw[];
   // The same offset in both CTAs of a pair: the bases are equal.
   Smem& s = *reinterpret_cast<Smem*>(smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023));
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = CTAS == 2 ? tc::cluster_rank() : 0;
+  const int rank = CTAS == 2 ? static_cast<int>(tc::cluster_rank()) : 0;
   const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
@@ -181,7 +310,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
   // Segments and the running count of tiles.  A segment that does not lie in
   // the buffer (a layout that overflowed its capacity, or a start that is not a
   // block boundary for the gradient) is left out and recorded.
-  const int p_tiles = ceil_div(p.p_rows, kPRows * CTAS);
+  const int across = col_tiles<KIND>(p);
   int running = 0;
   for (int base = 0; base < p.num_experts; base += kThreads) {
     const int e = base + static_cast<int>(threadIdx.x);
@@ -190,14 +319,14 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       const int start = p.expert_offset[e];
       int count = p.expert_count[e];
       const bool fits = start >= 0 && count >= 0 && static_cast<int64_t>(start) + count <= p.capacity;
-      const bool whole = !WGRAD || start % kKBlock == 0;
+      const bool whole = KIND != kWgrad || start % kKBlock == 0;
       if (!fits || !whole) {
         set_error(p.err, fits ? MOE_ERR_INVALID_ARG : MOE_ERR_CAPACITY);
         count = 0;
       }
       s.seg_start[e] = count > 0 ? start : 0;
       s.seg_count[e] = count;
-      tiles = T::q_tiles(p, count) * p_tiles;
+      tiles = row_tiles<KIND>(p, count) * across;
     }
     int sum = tiles;
 #pragma unroll
@@ -233,17 +362,17 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       Ring<kStages> ring;
       uint32_t loads = 0;
       for (int t = first_tile; t < tiles && ok; t += step) {
-        const Tile tile = T::get(p, s, t, rank);
+        const Tile tile = get_tile<KIND>(p, s, t, rank);
         // Q rows of each accumulator, an equal share by each CTA of a pair, in whole boxes
-        int q[CTAS], boxes[CTAS], all = 0;
+        int q[2], boxes[2];
 #pragma unroll
-        for (int h = 0; h < CTAS; ++h) {
+        for (int h = 0; h < 2; ++h) {
           const int rows = tile.n[h] / CTAS;
-          q[h] = tile.q0 + (h == 0 ? 0 : tile.n[0]) + static_cast<int>(rank) * rows;
+          q[h] = tile.q0 + (h == 0 ? 0 : tile.n[0]) + rank * rows;
           boxes[h] = ceil_div(rows, p.q_box);
-          all += boxes[h];
         }
-        const uint32_t bytes = CTAS * (kPBytes + all * p.q_box * kKBlock);
+        const uint32_t bytes = CTAS * (kPBytes + (boxes[0] + boxes[1]) * p.q_box * kKBlock);
+        const int p_plane = KIND == kFew ? tile.expert : 0, q_plane = KIND == kMany ? tile.expert : 0;
         for (int kb = 0; kb < tile.kblocks; ++kb) {
           if (!(ok = wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns))) break;
           if (tc::elect_one()) {
@@ -252,12 +381,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             if (CTAS == 2) bar = tc::map_to_rank(bar, 0);
             const uint32_t dst = ptx::smem_addr(s.stage[ring.i]);
             const int x = tile.k0 + kb * kKBlock;
-            tc::load_box<CTAS>(dst, &map_p, x, tile.p0, WGRAD ? 0 : tile.expert, bar);
+            tc::load_box<CTAS>(dst, &map_p, x, tile.p0, p_plane, bar);
 #pragma unroll
-            for (int h = 0; h < CTAS; ++h)
+            for (int h = 0; h < 2; ++h)
               for (int i = 0; i < boxes[h]; ++i)
-                tc::load_box<CTAS>(dst + kPBytes + (h * (kHalfCols / CTAS) + i * p.q_box) * kKBlock, &map_q, x,
-                                   q[h] + i * p.q_box, 0, bar);
+                tc::load_box<CTAS>(dst + kPBytes + (h * C::kQRows + i * p.q_box) * kKBlock, &map_q, x,
+                                   q[h] + i * p.q_box, q_plane, bar);
           }
           __syncwarp();
           ring.next();
@@ -274,19 +403,19 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       uint32_t used[2] = {0, 0};
       const uint64_t p_desc = tc::operand_desc(ptx::smem_addr(s.stage[0]));
       for (int t = first_tile; t < tiles && ok; t += step) {
-        const Tile tile = T::get(p, s, t, rank);
+        const Tile tile = get_tile<KIND>(p, s, t, rank);
         const uint32_t idesc[2] = {tc::instr_desc(kPRows * CTAS, tile.n[0]), tc::instr_desc(kPRows * CTAS, tile.n[1])};
         for (int kb = 0; kb < tile.kblocks && ok; ++kb) {
           if (!(ok = wait_warp(&s.full[ring.i], ring.phase, p.wait_ns))) break;
           const uint64_t a = p_desc + ring.i * (kStageBytes >> 4);
 #pragma unroll
-          for (int h = 0; h < CTAS; ++h) {
+          for (int h = 0; h < 2; ++h) {
             if (h == 1 && tile.n[1] == 0) continue;
             if (!(ok = wait_warp(&s.acc_empty[h][buf[h].i], buf[h].phase ^ 1, p.wait_ns))) break;
             tc::fence_after();
             if (tc::elect_one()) {
-              const uint64_t q = a + ((kPBytes + h * (kHalfCols / CTAS) * kKBlock) >> 4);
-              const uint32_t d = tmem + buf[h].i * MAXN + h * kHalfCols;
+              const uint64_t q = a + ((kPBytes + h * C::kQRows * kKBlock) >> 4);
+              const uint32_t d = tmem + buf[h].i * C::kTileCols + h * C::kAccCols;
 #pragma unroll
               for (int k = 0; k < kKBlock / 32; ++k) tc::mma_e4m3<CTAS>(d, a + 2 * k, q + 2 * k, idesc[h], k > 0);
               tc::commit<CTAS>(&s.acc_full[h][buf[h].i]);
@@ -307,33 +436,38 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     } else if (warp >= 2) {
       // ---- scales --------------------------------------------------------
       // Warp 2 + h brings those of accumulator h, through registers and kAhead
-      // k-blocks ahead; the forward product's P scale is one number a k-block and
-      // goes into the Q scales here.
-      constexpr int kAhead = 3, kQ = kHalfCols / 32, kP = WGRAD ? kPRows / 32 : 1;
+      // k-blocks ahead: one for each receive row (kMany: accumulator row, else
+      // column), times the weights' one; kWgrad: one for each column and row.
+      constexpr int kAhead = 3, kRows = 128 / 32;
       const int half = warp - 2;
       Ring<NBUF> ring;
       for (int t = first_tile; t < tiles && ok; t += step) {
-        const Tile tile = T::get(p, s, t, rank);
+        const Tile tile = get_tile<KIND>(p, s, t, rank);
         if ((half == 0 ? tile.n[0] : tile.n[1]) == 0) continue;
         const int64_t kb0 = tile.k0 / kKBlock;
-        const int j0 = (half == 0 ? 0 : tile.n[0]) + lane;
-        const float* qs = p.q_sf + kb0 * p.q_sf_pitch + tile.q0 + j0;
-        const float* ps = WGRAD ? p.p_sf + kb0 * p.p_rows + tile.p0 + lane
-                                : p.p_sf + (static_cast<int64_t>(tile.expert) * ceil_div(p.p_rows, kKBlock) +
-                                            tile.p0 / kKBlock) * p.kblocks;
-        float q[kAhead][kQ], w[kAhead][kP];
-        const auto fetch = [&](int kb, float* qv, float* wv) {
+        const int skip = KIND != kMany && half == 1 ? tile.n[0] : 0;
+        const int valid = (KIND == kMany ? tile.p_valid : tile.q_valid) - skip - lane;
+        const float* rs = p.row_sf + kb0 * p.row_sf_pitch + (KIND == kMany ? tile.p0 : tile.q0) + skip + lane;
+        const int block = KIND == kMany ? tile.q0 / 128 + half : tile.p0 / 128;
+        const bool block_in = KIND == kMany || tile.p_valid > 0;
+        const float* ws = KIND == kWgrad
+                              ? p.col_sf + kb0 * p.out_cols + tile.p0 + lane
+                              : p.col_sf + (static_cast<int64_t>(tile.expert) * ceil_div(p.out_cols, 128) + block) * p.kblocks;
+        float r[kAhead][kRows], w[kAhead][KIND == kWgrad ? kRows : 1];
+        const auto fetch = [&](int kb, float* rv, float* wv) {
           const bool in = kb < tile.kblocks;
 #pragma unroll
-          for (int i = 0; i < kQ; ++i)
-            qv[i] = in && j0 + i * 32 < tile.q_valid ? __ldg(qs + kb * p.q_sf_pitch + i * 32) : 0.0f;
+          for (int i = 0; i < kRows; ++i) rv[i] = in && i * 32 < valid ? __ldg(rs + kb * p.row_sf_pitch + i * 32) : 0.0f;
+          if (KIND == kWgrad) {
 #pragma unroll
-          for (int i = 0; i < kP; ++i)
-            wv[i] = !in || tile.p0 + (WGRAD ? lane + i * 32 : 0) >= p.p_rows ? 0.0f
-                    : WGRAD ? __ldg(ps + static_cast<int64_t>(kb) * p.p_rows + i * 32) : __ldg(ps + kb);
+            for (int i = 0; i < kRows; ++i)
+              wv[i] = in && lane + i * 32 < tile.p_valid ? __ldg(ws + static_cast<int64_t>(kb) * p.out_cols + i * 32) : 0.0f;
+          } else {
+            wv[0] = in && block_in ? __ldg(ws + kb) : 0.0f;
+          }
         };
 #pragma unroll
-        for (int d = 0; d < kAhead; ++d) fetch(d, q[d], w[d]);
+        for (int d = 0; d < kAhead; ++d) fetch(d, r[d], w[d]);
         for (int kb = 0; kb < tile.kblocks && ok; kb += kAhead) {
 #pragma unroll
           for (int d = 0; d < kAhead; ++d) {
@@ -341,84 +475,89 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             if (!(ok = wait_warp(&s.scale_empty[half][ring.i], ring.phase ^ 1, p.wait_ns))) break;
             float* to = s.scale[half][ring.i];
 #pragma unroll
-            for (int i = 0; i < kQ; ++i) to[scale_place(lane + i * 32)] = WGRAD ? q[d][i] : q[d][i] * w[d][0];
-            if (WGRAD) {
-#pragma unroll
-              for (int i = 0; i < kP; ++i) to[kHalfCols + lane + i * 32] = w[d][i];
+            for (int i = 0; i < kRows; ++i) {
+              const int j = lane + i * 32;
+              if (KIND == kMany) to[j] = r[d][i] * w[d][0];
+              if (KIND == kFew) to[scale_place(j)] = r[d][i] * w[d][0];
+              if (KIND == kWgrad) to[scale_place(j)] = r[d][i];
+              if (KIND == kWgrad) to[128 + j] = w[d][i];
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.acc_full[half][ring.i]);
             ring.next();
-            fetch(kb + d + kAhead, q[d], w[d]);
+            fetch(kb + d + kAhead, r[d], w[d]);
           }
         }
       }
     }
   } else {
     // ---- epilogue --------------------------------------------------------
-    // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of one accumulator, 32
-    // columns at a time; the next batch is on its way while one is added.
+    // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of one accumulator.
     tc::reg_inc<kEpilogueRegs>();
+    constexpr int kBatches = C::kAccCols / kBatchCols;
     const int ew = warp - 4, quarter = warp % 4, half = ew / 4;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalfCols;
-    uint8_t* stage = s.out[ew];
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * C::kAccCols;
     uint32_t freed = ptx::smem_addr(&s.acc_empty[half][0]);   // the leader's barriers
     if (CTAS == 2) freed = tc::map_to_rank(freed, 0);
     Ring<NBUF> buf;
     for (int t = first_tile; t < tiles && ok; t += step) {
-      // Only these three values stay in registers over the k-blocks.
-      int n, first, kblocks;
+      int n, kblocks;                                         // all that lives over the k-blocks
       {
-        const Tile tile = T::get(p, s, t, rank);
+        const Tile tile = get_tile<KIND>(p, s, t, rank);
         n = half == 0 ? tile.n[0] : tile.n[1];
-        first = half == 0 ? 0 : tile.n[0];                  // column of the tile the accumulator starts at
         kblocks = n > 0 ? tile.kblocks : 0;
       }
-      // acc[c][16 * up + 2 * i + r]: row 16 * up + 8 * r + lane / 4, column 32 * c + 4 * i + lane % 4
-      float acc[kBatches][32];
+      uint64_t acc[kBatches][16];                             // pairs of sums: see store_rows, store_columns
 #pragma unroll
       for (int c = 0; c < kBatches; ++c)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) acc[c][i] = 0;
       for (int kb = 0; kb < kblocks; ++kb) {
         if (!(ok = wait_warp(&s.acc_full[half][buf.i], buf.phase, p.wait_ns))) break;
         tc::fence_after();
         const float* sc = s.scale[half][buf.i];
-        float pw[4];
-        if (WGRAD) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) pw[i] = sc[kHalfCols + quarter * 32 + 8 * i + lane / 4];
+        const uint32_t from = lane_base + buf.i * C::kTileCols;
+        uint64_t ps[2];
+        if (KIND == kMany) {
+          const float v = sc[quarter * 32 + lane];
+          ps[0] = tc::pack2(v, v);
         }
-        sc += (lane % 4) * 4;
-        const uint32_t from = lane_base + buf.i * MAXN;
-        float v[2][32];
-        tc::ld_16x32(from, v[0]);
-        tc::ld_16x32(from + (16u << 16), v[0] + 16);
+        if (KIND == kWgrad) {
+          const float* rows = sc + 128 + quarter * 32 + lane / 4;
+          ps[0] = tc::pack2(rows[0], rows[8]);
+          ps[1] = tc::pack2(rows[16], rows[24]);
+        }
 #pragma unroll
-        for (int c = 0; c < kBatches; ++c) {
-          if (c * kBatchCols < n) {
-            const float4 lo = *reinterpret_cast<const float4*>(sc + c * kBatchCols);
-            const float4 hi = *reinterpret_cast<const float4*>(sc + c * kBatchCols + 16);
-            tc::wait_ld();
-            if (c + 1 < kBatches && (c + 1) * kBatchCols < n) {
-              tc::ld_16x32(from + (c + 1) * kBatchCols, v[(c + 1) % 2]);
-              tc::ld_16x32(from + (c + 1) * kBatchCols + (16u << 16), v[(c + 1) % 2] + 16);
-            } else {   // everything is in registers: the tensor core may have the buffer back
-              tc::fence_before();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+        for (int c = 0; c < kBatches; c += 2) {
+          if (c * kBatchCols >= n) break;
+          float v[2][32];
+          float4 f[2][2];
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            if (KIND == kMany) {
+              tc::ld_32x32(from + (c + d) * kBatchCols, v[d]);
+            } else {
+              tc::ld_16x32(from + (c + d) * kBatchCols, v[d]);
+              tc::ld_16x32(from + (c + d) * kBatchCols + (16u << 16), v[d] + 16);
+              f[d][0] = *reinterpret_cast<const float4*>(sc + (c + d) * kBatchCols + (lane % 4) * 4);
+              f[d][1] = *reinterpret_cast<const float4*>(sc + (c + d) * kBatchCols + 16 + (lane % 4) * 4);
             }
-            const float q[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+          }
+          tc::wait_ld();
+          if ((c + 2) * kBatchCols >= n || c + 2 >= kBatches) {   // all is in registers: the tensor core may have the buffer back
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+          }
 #pragma unroll
-            for (int up = 0; up < 2; ++up)
+          for (int d = 0; d < 2; ++d) {
+            const float q[8] = {f[d][0].x, f[d][0].y, f[d][0].z, f[d][0].w, f[d][1].x, f[d][1].y, f[d][1].z, f[d][1].w};
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  float x = v[c % 2][16 * up + 2 * i + r];
-                  if (WGRAD) x *= pw[2 * up + r];
-                  acc[c][16 * up + 2 * i + r] = fmaf(x, q[i], acc[c][16 * up + 2 * i + r]);
-                }
+            for (int i = 0; i < 16; ++i) {
+              uint64_t v2 = tc::pack2(v[d][2 * i], v[d][2 * i + 1]);
+              if (KIND == kWgrad) v2 = tc::mul2(v2, ps[i / 8]);
+              acc[c + d][i] = tc::fma2(v2, KIND == kMany ? ps[0] : tc::pack2(q[i % 8], q[i % 8]), acc[c + d][i]);
+            }
           }
         }
         __syncwarp();
@@ -427,56 +566,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       }
       if (!ok) break;
 
-      const Tile tile = T::get(p, s, t, rank);
-      const int col0 = tile.p0 + quarter * 32;              // the warp's first column of out
-      const int64_t row0 = (WGRAD ? static_cast<int64_t>(tile.expert) * p.q_rows : 0) + tile.q0;
-#pragma unroll
-      for (int c = 0; c < kBatches; ++c) {
-        const int col = c * kBatchCols;
-        if (col >= n) break;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {                       // 8 columns of the accumulator: rows of out
-          const int row = first + col + 8 * h;
-          if (WGRAD && p.out_fp32) {
-            float* out = static_cast<float*>(p.out) + row0 * p.p_rows;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int up = i / 4, r = i % 2, at = row + 4 * (i / 2 % 2) + lane % 4;
-              const int oc = col0 + 16 * up + 8 * r + lane / 4;
-              if (at < tile.q_valid && oc < p.p_rows) {
-                float* o = out + static_cast<int64_t>(at) * p.p_rows + oc;
-                const float v = acc[c][16 * up + 4 * h + i % 4];
-                *o = p.accumulate ? *o + v : v;
-              }
-            }
-            continue;
-          }
-          // Lanes j and j ^ 4 hold rows k and k + 1 (k = j/4 even) and the rows 8 further
-          // on; they trade so that each has two neighbours: one 32-bit word of out.
-          const bool odd = (lane & 4) != 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {                     // up = i / 2, column 4 * (i % 2) + lane % 4
-            const float lo = acc[c][16 * (i / 2) + 4 * h + 2 * (i % 2)], hi = acc[c][16 * (i / 2) + 4 * h + 2 * (i % 2) + 1];
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 4);
-            const __nv_bfloat162 h2 = odd ? __floats2bfloat162_rn(other, hi) : __floats2bfloat162_rn(lo, other);
-            *reinterpret_cast<__nv_bfloat162*>(stage + (4 * (i % 2) + lane % 4) * kOutPitch + 32 * (i / 2) +
-                                               (odd ? 16 : 0) + lane / 8 * 4) = h2;
-          }
-          __syncwarp();
-          const int r = row + lane / 4, oc = col0 + (lane % 4) * 8;
-          const uint4 w = ptx::ld_shared_v4(stage + lane / 4 * kOutPitch + (lane % 4) * 16);
-          if (r < tile.q_valid && oc < p.p_rows) ptx::st_v4(static_cast<uint16_t*>(p.out) + (row0 + r) * p.p_rows + oc, w);
-          __syncwarp();
-        }
-      }
-      if (!WGRAD && tile.last_q) {
-        // gap rows of the segment: zeros, the two warps of the same columns in turn
-        const int64_t end = min64(p.expert_offset[tile.expert + 1], p.capacity);
-        const int oc = col0 + (lane % 4) * 8;
-        if (oc < p.p_rows)
-          for (int64_t r = static_cast<int64_t>(tile.q0) + tile.q_valid + half * 8 + lane / 4; r < end; r += 16)
-            ptx::st_v4(static_cast<uint16_t*>(p.out) + r * p.p_rows + oc, make_uint4(0, 0, 0, 0));
-      }
+      const Tile tile = get_tile<KIND>(p, s, t, rank);
+      if constexpr (KIND == kMany) store_rows(p, tile, quarter * 32 + lane, half, acc);
+      else store_columns<KIND>(p, tile, quarter, half, lane, s.out[ew], acc);
+      if (KIND != kWgrad && tile.last) zero_gap<KIND>(p, s, tile, rank, ew, lane);
     }
   }
 
@@ -523,9 +616,10 @@ cudaError_t encode(CUtensorMap* m, const void* base, int64_t width, int64_t rows
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int CTAS, int MAXN, bool WGRAD>
-cudaError_t launch(const CUtensorMap* maps, const GemmParams& p, cudaStream_t stream) {
-  const auto kernel = expert_gemm_kernel<CTAS, MAXN, WGRAD>;
+template <Kind KIND>
+cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const GemmParams& p, cudaStream_t stream) {
+  constexpr int CTAS = Config<KIND>::kCtas;
+  const auto kernel = expert_gemm_kernel<KIND>;
   cudaError_t e = ensure_smem_limit(kernel, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -543,45 +637,11 @@ cudaError_t launch(const CUtensorMap* maps, const GemmParams& p, cudaStream_t st
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], p);
+  return cudaLaunchKernelEx(&cfg, kernel, map_p, map_q, p);
 }
 
-}  // namespace
-
-cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream) {
+GemmParams common_params(const ExpertGemmArgs& a) {
   GemmParams p{};
-  p.p_sf = a.w_sf;
-  p.q_sf = a.x_sf;
-  p.q_sf_pitch = a.sf_ld;
-  p.p_rows = static_cast<int>(a.width_out);
-  p.kblocks = static_cast<int>(ceil_div64(a.width_in, kKBlock));
-  p.num_experts = a.num_experts;
-  p.expert_offset = a.expert_offset;
-  p.expert_count = a.expert_count;
-  p.capacity = a.capacity;
-  p.out = a.out;
-  p.err = a.err;
-  p.wait_ns = wait_config().limit_ns;
-  p.extra_tx = wait_config().extra_tx;
-  CUtensorMap maps[2];
-  cudaError_t e = encode(&maps[0], a.w, a.width_in, a.width_out, a.num_experts, kPRows);
-  // Rows an expert has in the mean: many fill the 256 columns of a pair's tile.
-  const int64_t mean = a.pairs / a.num_experts;
-  const bool pair = mean >= 192;
-  p.q_box = pair || mean >= 32 ? 64 : 16;
-  if (e == cudaSuccess) e = encode(&maps[1], a.x, a.width_in, a.capacity, 1, p.q_box);
-  if (e != cudaSuccess) return e;
-  if (pair) return launch<2, 256, false>(maps, p, stream);
-  return launch<1, 128, false>(maps, p, stream);
-}
-
-cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
-  GemmParams p{};
-  p.p_sf = a.x_sf;
-  p.q_sf = a.w_sf;
-  p.q_sf_pitch = a.width_out;
-  p.p_rows = static_cast<int>(a.width_in);
-  p.q_rows = static_cast<int>(a.width_out);
   p.num_experts = a.num_experts;
   p.expert_offset = a.expert_offset;
   p.expert_count = a.expert_count;
@@ -592,12 +652,41 @@ cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
   p.err = a.err;
   p.wait_ns = wait_config().limit_ns;
   p.extra_tx = wait_config().extra_tx;
-  CUtensorMap maps[2];
-  cudaError_t e = encode(&maps[0], a.x, a.sf_ld, a.width_in, 1, kPRows);
-  p.q_box = 64;
-  if (e == cudaSuccess) e = encode(&maps[1], a.w, a.sf_ld, a.width_out, 1, p.q_box);
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream) {
+  GemmParams p = common_params(a);
+  p.row_sf = a.x_sf;
+  p.row_sf_pitch = a.sf_ld;
+  p.col_sf = a.w_sf;
+  p.out_cols = static_cast<int>(a.width_out);
+  p.kblocks = static_cast<int>(ceil_div64(a.width_in, kKBlock));
+  // Rows an expert has in the mean: many fill the 256 rows of a pair's tile.
+  const int64_t mean = a.pairs / a.num_experts;
+  const bool many = mean >= 192;
+  p.q_box = many || mean >= 32 ? 64 : 16;
+  CUtensorMap rows, weights;
+  cudaError_t e = encode(&rows, a.x, a.width_in, a.capacity, 1, many ? kPRows : p.q_box);
+  if (e == cudaSuccess) e = encode(&weights, a.w, a.width_in, a.width_out, a.num_experts, many ? p.q_box : kPRows);
   if (e != cudaSuccess) return e;
-  return launch<2, 256, true>(maps, p, stream);
+  return many ? launch<kMany>(rows, weights, p, stream) : launch<kFew>(weights, rows, p, stream);
+}
+
+cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
+  GemmParams p = common_params(a);
+  p.row_sf = a.w_sf;
+  p.row_sf_pitch = a.width_out;
+  p.col_sf = a.x_sf;
+  p.out_cols = static_cast<int>(a.width_in);
+  p.dy_rows = static_cast<int>(a.width_out);
+  p.q_box = 64;
+  CUtensorMap x, dy;
+  cudaError_t e = encode(&x, a.x, a.sf_ld, a.width_in, 1, kPRows);
+  if (e == cudaSuccess) e = encode(&dy, a.w, a.sf_ld, a.width_out, 1, p.q_box);
+  return e == cudaSuccess ? launch<kWgrad>(x, dy, p, stream) : e;
 }
 
 }  // namespace moe

@@ -205,13 +205,14 @@ struct ExpertGemmArgs {
   int* err;
 };
 
-// The kernel's view: D[p, q] = sum over k-blocks of scales times <P_p, Q_q>.
+// The kernel's view of either product: rows of out come from receive rows
+// (gradient: rows of dy), its columns from the weights (gradient: rows of x^T).
 struct GemmParams {
-  const float* p_sf;
-  const float* q_sf;             // scale of (k-block, row of Q) at k-block * q_sf_pitch + row
-  int64_t q_sf_pitch;
-  int p_rows;                    // rows of P of an expert = columns (and pitch) of out
-  int q_rows;                    // gradient: rows of Q
+  const float* row_sf;           // scale of (k-block, row) at k-block * row_sf_pitch + row
+  int64_t row_sf_pitch;
+  const float* col_sf;           // weights' scales; gradient: x_sf
+  int out_cols;                  // columns (and pitch) of out
+  int dy_rows;                   // gradient: rows of out of an expert
   int kblocks;                   // forward: k-blocks of a row
   int q_box;                     // rows of Q a TMA load brings: 16 or 64
   int num_experts;
