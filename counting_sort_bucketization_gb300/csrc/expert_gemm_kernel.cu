@@ -59,6 +59,7 @@ constexpr int kPBytes = kPRows * kKBlock;
 constexpr int kQBytes = 128 * kKBlock;             // a CTA loads at most 128 rows of Q
 constexpr int kStageBytes = kPBytes + kQBytes;
 constexpr int kStages = 6;
+constexpr int kBuffers = 2;                        // of an accumulator
 constexpr int kBatchCols = 32;                     // columns of one tensor-memory load
 constexpr int kSlotWords = 128 + kPRows;           // scales of columns or rows, then (kWgrad) of rows
 constexpr int kOutPitch = 96;                      // bytes; 64 of data, 4 rows' 32-byte pieces in different banks
@@ -73,21 +74,21 @@ struct Config {
   static constexpr int kCtas = KIND == kFew ? 1 : 2;
   static constexpr int kAccCols = KIND == kFew ? 64 : 128;     // columns of an accumulator
   static constexpr int kTileCols = 2 * kAccCols;
-  static constexpr int kBuffers = kTmemCols / kTileCols;
+  static_assert(kBuffers * kTileCols <= kTmemCols, "tensor memory");
   static constexpr int kUnit = 16 * kCtas;                     // column granularity: each CTA of a pair holds n / 2 rows of Q
   static constexpr int kQRows = kAccCols / kCtas;              // rows of Q of an accumulator a CTA loads at most
 };
 
 struct Smem {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
-  alignas(16) float scale[2][4][kSlotWords];       // [accumulator][buffer]
+  alignas(16) float scale[2][kBuffers][kSlotWords];   // [accumulator][buffer]
   alignas(16) uint8_t out[kEpilogueWarps][kOutBytes];
   int tile_end[MOE_MAX_EXPERTS];                   // tiles of experts 0..e
   int seg_start[MOE_MAX_EXPERTS];
   int seg_count[MOE_MAX_EXPERTS];
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2][4], acc_empty[2][4];        // full: product and scales are there
-  uint64_t scale_empty[2][4];
+  uint64_t acc_full[2][kBuffers], acc_empty[2][kBuffers];   // full: product and scales are there
+  uint64_t scale_empty[2][kBuffers];
   uint32_t tmem;
   int warp_sum[kThreads / 32];
 };
@@ -278,10 +279,10 @@ __device__ __forceinline__ void zero_gap(const GemmParams& p, const Smem& s, con
 template <Kind KIND>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-                   const GemmParams p) {
+                   const __grid_constant__ CUtensorMap map_q16, const GemmParams p) {
   using C = Config<KIND>;
-  constexpr int CTAS = C::kCtas, NBUF = C::kBuffers;
-  static_assert(NBUF <= 4 && 2 * C::kQRows * kKBlock <= kQBytes, "buffers of tensor and shared memory");
+  constexpr int CTAS = C::kCtas, NBUF = kBuffers;
+  static_assert(2 * C::kQRows * kKBlock <= kQBytes, "shared memory of Q");
   extern __shared__ uint8_t smem_raw[];
   // The same offset in both CTAs of a pair: the bases are equal.
   Smem& s = *reinterpret_cast<Smem*>(smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023));
@@ -292,6 +293,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
   if (threadIdx.x == 0) {
     tc::prefetch_map(&map_p);
     tc::prefetch_map(&map_q);
+    if (KIND == kFew) tc::prefetch_map(&map_q16);
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
       ptx::mbar_init(&s.empty[i], 1);
@@ -363,30 +365,24 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       uint32_t loads = 0;
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
-        // Q rows of each accumulator, an equal share by each CTA of a pair, in whole boxes
-        int q[2], boxes[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int rows = tile.n[h] / CTAS;
-          q[h] = tile.q0 + (h == 0 ? 0 : tile.n[0]) + rank * rows;
-          boxes[h] = ceil_div(rows, p.q_box);
-        }
-        const uint32_t bytes = CTAS * (kPBytes + (boxes[0] + boxes[1]) * p.q_box * kKBlock);
+        // Q rows of each accumulator, an equal share by each CTA of a pair, in one box:
+        // 64 rows, or 16 for the shortest segments
+        const bool two = tile.n[1] > 0, small = KIND == kFew && tile.n[0] <= 16;
+        const int q0 = tile.q0 + rank * (tile.n[0] / CTAS), q1 = tile.q0 + tile.n[0] + rank * (tile.n[1] / CTAS);
+        const uint32_t bytes = CTAS * (kPBytes + (two ? 128 : small ? 16 : 64) * kKBlock);
         const int p_plane = KIND == kFew ? tile.expert : 0, q_plane = KIND == kMany ? tile.expert : 0;
-        for (int kb = 0; kb < tile.kblocks; ++kb) {
+        int x = tile.k0;
+        for (int kb = 0; kb < tile.kblocks; ++kb, x += kKBlock) {
           if (!(ok = wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns))) break;
           if (tc::elect_one()) {
-            if (leader) ptx::mbar_arrive_expect_tx(&s.full[ring.i], bytes + (loads == 0 ? p.extra_tx : 0));
             uint32_t bar = ptx::smem_addr(&s.full[ring.i]);
-            if (CTAS == 2) bar = tc::map_to_rank(bar, 0);
             const uint32_t dst = ptx::smem_addr(s.stage[ring.i]);
-            const int x = tile.k0 + kb * kKBlock;
+            if (leader) ptx::mbar_arrive_expect_tx(&s.full[ring.i], bytes + (loads == 0 ? p.extra_tx : 0));
+            if (CTAS == 2) bar = tc::map_to_rank(bar, 0);
             tc::load_box<CTAS>(dst, &map_p, x, tile.p0, p_plane, bar);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              for (int i = 0; i < boxes[h]; ++i)
-                tc::load_box<CTAS>(dst + kPBytes + (h * C::kQRows + i * p.q_box) * kKBlock, &map_q, x,
-                                   q[h] + i * p.q_box, q_plane, bar);
+            if (small) tc::load_box<CTAS>(dst + kPBytes, &map_q16, x, q0, q_plane, bar);
+            else tc::load_box<CTAS>(dst + kPBytes, &map_q, x, q0, q_plane, bar);
+            if (two) tc::load_box<CTAS>(dst + kPBytes + C::kQRows * kKBlock, &map_q, x, q1, q_plane, bar);
           }
           __syncwarp();
           ring.next();
@@ -398,41 +394,61 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         if (loads >= kStages) ok &= wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns);
     } else if (warp == 1 && leader) {
       // ---- MMA -----------------------------------------------------------
+      // The three barriers of a k-block are asked together: a ready one answers after
+      // ~60 cycles, and three in turn would take as long as the MMAs.
       Ring<kStages> ring;
-      Ring<NBUF> buf[2];
-      uint32_t used[2] = {0, 0};
+      Ring<NBUF> buf;
+      uint32_t used = 0;
       const uint64_t p_desc = tc::operand_desc(ptx::smem_addr(s.stage[0]));
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
         const uint32_t idesc[2] = {tc::instr_desc(kPRows * CTAS, tile.n[0]), tc::instr_desc(kPRows * CTAS, tile.n[1])};
-        for (int kb = 0; kb < tile.kblocks && ok; ++kb) {
-          if (!(ok = wait_warp(&s.full[ring.i], ring.phase, p.wait_ns))) break;
-          const uint64_t a = p_desc + ring.i * (kStageBytes >> 4);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1 && tile.n[1] == 0) continue;
-            if (!(ok = wait_warp(&s.acc_empty[h][buf[h].i], buf[h].phase ^ 1, p.wait_ns))) break;
-            tc::fence_after();
-            if (tc::elect_one()) {
-              const uint64_t q = a + ((kPBytes + h * C::kQRows * kKBlock) >> 4);
-              const uint32_t d = tmem + buf[h].i * C::kTileCols + h * C::kAccCols;
-#pragma unroll
-              for (int k = 0; k < kKBlock / 32; ++k) tc::mma_e4m3<CTAS>(d, a + 2 * k, q + 2 * k, idesc[h], k > 0);
-              tc::commit<CTAS>(&s.acc_full[h][buf[h].i]);
-            }
-            __syncwarp();
-            buf[h].next();
-            ++used[h];
+        const bool two = tile.n[1] > 0;
+        for (int kb = 0; kb < tile.kblocks; ++kb) {
+          const bool in = ptx::mbar_try_wait_parity(&s.full[ring.i], ring.phase);
+          const bool free0 = ptx::mbar_try_wait_parity(&s.acc_empty[0][buf.i], buf.phase ^ 1);
+          const bool free1 = ptx::mbar_try_wait_parity(&s.acc_empty[1][buf.i], buf.phase ^ 1);
+          if (!__all_sync(0xffffffffu, in && free0)) {
+            ok = wait_warp(&s.full[ring.i], ring.phase, p.wait_ns) &&
+                 wait_warp(&s.acc_empty[0][buf.i], buf.phase ^ 1, p.wait_ns);
+            if (!ok) break;
           }
-          if (ok && tc::elect_one()) tc::commit<CTAS>(&s.empty[ring.i]);
+          tc::fence_after();
+          const uint64_t a = p_desc + ring.i * (kStageBytes >> 4);
+          const uint32_t d = tmem + buf.i * C::kTileCols;
+          if (tc::elect_one()) {
+            const uint64_t q = a + (kPBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < kKBlock / 32; ++k) tc::mma_e4m3<CTAS>(d, a + 2 * k, q + 2 * k, idesc[0], k > 0);
+            tc::commit<CTAS>(&s.acc_full[0][buf.i]);
+            if (!two) tc::commit<CTAS>(&s.acc_full[1][buf.i]);
+          }
+          __syncwarp();
+          if (!__all_sync(0xffffffffu, free1)) {
+            if (!(ok = wait_warp(&s.acc_empty[1][buf.i], buf.phase ^ 1, p.wait_ns))) break;
+          }
+          tc::fence_after();
+          if (tc::elect_one()) {
+            if (two) {
+              const uint64_t q = a + ((kPBytes + C::kQRows * kKBlock) >> 4);
+#pragma unroll
+              for (int k = 0; k < kKBlock / 32; ++k)
+                tc::mma_e4m3<CTAS>(d + C::kAccCols, a + 2 * k, q + 2 * k, idesc[1], k > 0);
+              tc::commit<CTAS>(&s.acc_full[1][buf.i]);
+            }
+            tc::commit<CTAS>(&s.empty[ring.i]);
+          }
           __syncwarp();
           ring.next();
+          buf.next();
+          ++used;
         }
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)   // the epilogues' last (remote) arrivals
-        for (uint32_t i = 0; i < NBUF; ++i, ++used[h], buf[h].next())
-          if (used[h] >= NBUF) ok &= wait_warp(&s.acc_empty[h][buf[h].i], buf[h].phase ^ 1, p.wait_ns);
+      for (uint32_t i = 0; i < NBUF; ++i, ++used, buf.next())   // the epilogues' last (remote) arrivals
+        if (used >= NBUF) {
+          ok &= wait_warp(&s.acc_empty[0][buf.i], buf.phase ^ 1, p.wait_ns);
+          ok &= wait_warp(&s.acc_empty[1][buf.i], buf.phase ^ 1, p.wait_ns);
+        }
     } else if (warp >= 2) {
       // ---- scales --------------------------------------------------------
       // Warp 2 + h brings those of accumulator h, through registers and kAhead
@@ -443,7 +459,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       Ring<NBUF> ring;
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
-        if ((half == 0 ? tile.n[0] : tile.n[1]) == 0) continue;
         const int64_t kb0 = tile.k0 / kKBlock;
         const int skip = KIND != kMany && half == 1 ? tile.n[0] : 0;
         const int valid = (KIND == kMany ? tile.p_valid : tile.q_valid) - skip - lane;
@@ -505,7 +520,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
         n = half == 0 ? tile.n[0] : tile.n[1];
-        kblocks = n > 0 ? tile.kblocks : 0;
+        kblocks = tile.kblocks;
       }
       uint64_t acc[kBatches][16];                             // pairs of sums: see store_rows, store_columns
 #pragma unroll
@@ -561,7 +576,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
           }
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&s.scale_empty[half][buf.i]);
+        if (lane == 0) {
+          if (n == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+          ptx::mbar_arrive(&s.scale_empty[half][buf.i]);
+        }
         buf.next();
       }
       if (!ok) break;
@@ -617,7 +635,8 @@ cudaError_t encode(CUtensorMap* m, const void* base, int64_t width, int64_t rows
 }
 
 template <Kind KIND>
-cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const GemmParams& p, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const CUtensorMap& map_q16, const GemmParams& p,
+                   cudaStream_t stream) {
   constexpr int CTAS = Config<KIND>::kCtas;
   const auto kernel = expert_gemm_kernel<KIND>;
   cudaError_t e = ensure_smem_limit(kernel, kSmemBytes);
@@ -637,7 +656,7 @@ cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const Gem
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, kernel, map_p, map_q, p);
+  return cudaLaunchKernelEx(&cfg, kernel, map_p, map_q, map_q16, p);
 }
 
 GemmParams common_params(const ExpertGemmArgs& a) {
@@ -667,12 +686,12 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream) {
   // Rows an expert has in the mean: many fill the 256 rows of a pair's tile.
   const int64_t mean = a.pairs / a.num_experts;
   const bool many = mean >= 192;
-  p.q_box = many || mean >= 32 ? 64 : 16;
-  CUtensorMap rows, weights;
-  cudaError_t e = encode(&rows, a.x, a.width_in, a.capacity, 1, many ? kPRows : p.q_box);
-  if (e == cudaSuccess) e = encode(&weights, a.w, a.width_in, a.width_out, a.num_experts, many ? p.q_box : kPRows);
+  CUtensorMap rows, rows16, weights;
+  cudaError_t e = encode(&rows, a.x, a.width_in, a.capacity, 1, many ? kPRows : 64);
+  if (e == cudaSuccess) e = encode(&rows16, a.x, a.width_in, a.capacity, 1, 16);
+  if (e == cudaSuccess) e = encode(&weights, a.w, a.width_in, a.width_out, a.num_experts, many ? 64 : kPRows);
   if (e != cudaSuccess) return e;
-  return many ? launch<kMany>(rows, weights, p, stream) : launch<kFew>(weights, rows, p, stream);
+  return many ? launch<kMany>(rows, weights, weights, p, stream) : launch<kFew>(weights, rows, rows16, p, stream);
 }
 
 cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
@@ -682,11 +701,10 @@ cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
   p.col_sf = a.x_sf;
   p.out_cols = static_cast<int>(a.width_in);
   p.dy_rows = static_cast<int>(a.width_out);
-  p.q_box = 64;
   CUtensorMap x, dy;
   cudaError_t e = encode(&x, a.x, a.sf_ld, a.width_in, 1, kPRows);
-  if (e == cudaSuccess) e = encode(&dy, a.w, a.sf_ld, a.width_out, 1, p.q_box);
-  return e == cudaSuccess ? launch<kWgrad>(x, dy, p, stream) : e;
+  if (e == cudaSuccess) e = encode(&dy, a.w, a.sf_ld, a.width_out, 1, 64);
+  return e == cudaSuccess ? launch<kWgrad>(x, dy, dy, p, stream) : e;
 }
 
 }  // namespace moe

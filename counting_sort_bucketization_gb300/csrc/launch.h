@@ -214,7 +214,6 @@ struct GemmParams {
   int out_cols;                  // columns (and pitch) of out
   int dy_rows;                   // gradient: rows of out of an expert
   int kblocks;                   // forward: k-blocks of a row
-  int q_box;                     // rows of Q a TMA load brings: 16 or 64
   int num_experts;
   const int32_t* expert_offset;
   const int32_t* expert_count;
