@@ -9,13 +9,14 @@
 // warps add it, times its scales, to fp32 sums in registers:
 //
 //   warp 0      TMA loads of P and Q tiles (128-byte rows, one k-block wide)
-//   warp 1      tcgen05.mma, 4 per k-block, into one of kBuffers buffers
+//   warp 1      tcgen05.mma, 4 per k-block and accumulator
 //   warps 2-3   the k-block's scales to shared memory
 //   warps 4-11  tensor memory -> fp32 sums; at the tile's end rows of out
 //
 // D[p, q] = <P_p, Q_q>: P gives the 128 accumulator rows (tensor-memory lanes) of
-// a CTA, Q its columns, half of them for each group of 4 epilogue warps.  Three
-// kinds:
+// a CTA, Q its columns.  A tile's columns are two accumulators, each with its own
+// buffers, barriers and 4 of the 8 epilogue warps: the tensor core fills one
+// while the other is read.  Three kinds:
 //
 //   kMany   P = receive rows, Q = weights; a pair of CTAs shares one 256 x 256 MMA,
 //           each loading half of Q.  A thread owns a receive row, and both scales
@@ -58,6 +59,7 @@ constexpr int kPBytes = kPRows * kKBlock;
 constexpr int kQBytes = 128 * kKBlock;             // a CTA loads at most 128 rows of Q
 constexpr int kStageBytes = kPBytes + kQBytes;
 constexpr int kStages = 6;
+constexpr int kBuffers = 2;                        // of an accumulator
 constexpr int kBatchCols = 32;                     // columns of one tensor-memory load
 constexpr int kSlotWords = 128 + kPRows;           // scales of columns or rows, then (kWgrad) of rows
 constexpr int kOutPitch = 96;                      // bytes; 64 of data, 4 rows' 32-byte pieces in different banks
@@ -70,21 +72,23 @@ static_assert(256 * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, 
 template <Kind KIND>
 struct Config {
   static constexpr int kCtas = KIND == kFew ? 1 : 2;
-  static constexpr int kTileCols = KIND == kFew ? 128 : 256;
-  static constexpr int kGroupCols = kTileCols / 2;             // columns of a group of epilogue warps
-  static constexpr int kBuffers = kTmemCols / kTileCols;       // of the accumulator
+  static constexpr int kAccCols = KIND == kFew ? 64 : 128;     // columns of an accumulator
+  static constexpr int kTileCols = 2 * kAccCols;
+  static_assert(kBuffers * kTileCols <= kTmemCols, "tensor memory");
   static constexpr int kUnit = 16 * kCtas;                     // column granularity: each CTA of a pair holds n / 2 rows of Q
+  static constexpr int kQRows = kAccCols / kCtas;              // rows of Q of an accumulator a CTA loads at most
 };
 
 struct Smem {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
-  alignas(16) float scale[2][4][kSlotWords];       // [group][buffer]
+  alignas(16) float scale[2][kBuffers][kSlotWords];   // [accumulator][buffer]
   alignas(16) uint8_t out[kEpilogueWarps][kOutBytes];
   int tile_end[MOE_MAX_EXPERTS];                   // tiles of experts 0..e
   int seg_start[MOE_MAX_EXPERTS];
   int seg_count[MOE_MAX_EXPERTS];
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[4], acc_empty[4], scale_empty[4];   // full: product and scales are there
+  uint64_t acc_full[2][kBuffers], acc_empty[2][kBuffers];   // full: product and scales are there
+  uint64_t scale_empty[2][kBuffers];
   uint32_t tmem;
   int warp_sum[kThreads / 32];
 };
@@ -98,7 +102,7 @@ struct Tile {
   int p_valid;     // rows of P that exist
   int q0;          // first row of Q
   int q_valid;     // rows of Q that exist
-  int n;           // accumulator columns: q_valid rounded up
+  int n[2];        // columns of the two accumulators; the second may have none
   int k0;          // first k (kWgrad: the segment's first row)
   int kblocks;
   bool last;       // the expert's last tile along the receive rows
@@ -147,7 +151,11 @@ __device__ __forceinline__ Tile get_tile(const GemmParams& p, const Smem& s, int
     r.q0 = (KIND == kWgrad ? 0 : start) + row * per;
     r.q_valid = max(0, min(per, rows - row * per));
   }
-  r.n = max(C::kUnit, ceil_div(r.q_valid, C::kUnit) * C::kUnit);
+  // kMany: an accumulator is one scale block of the weights; else the two are of
+  // like size, the first in whole batches
+  const int n = max(C::kUnit, ceil_div(r.q_valid, C::kUnit) * C::kUnit);
+  r.n[0] = n <= C::kAccCols ? n : KIND == kMany ? C::kAccCols : ceil_div(n / 2, kBatchCols) * kBatchCols;
+  r.n[1] = n - r.n[0];
   return r;
 }
 
@@ -166,6 +174,13 @@ struct Ring {
   }
 };
 
+// A value all lanes have, in a uniform register: addresses, descriptors and loop
+// bounds built on it then stay there.  (From ordinary registers each MMA or TMA
+// operand is moved over one by one, and issuing takes longer than the MMAs.)
+__device__ __forceinline__ int uniform(int v) {
+  return static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(v)));
+}
+
 // The whole warp waits, and leaves together (tcgen05.ld needs all lanes).
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, limit_ns));
@@ -179,8 +194,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // Rows of out from sums whose thread owns a row (kMany).
 // acc[c][i]: columns 32 c + 2 i, +1 of the accumulator.
 __device__ __forceinline__ void store_rows(const GemmParams& p, const Tile& t, int row, int half, const uint64_t (*acc)[16]) {
-  const int oc = t.q0 + half * 128;
-  if (row >= t.p_valid) return;
+  const int oc = t.q0 + half * 128, n = half == 0 ? t.n[0] : t.n[1];
+  if (row >= t.p_valid || n == 0) return;
   uint16_t* out = static_cast<uint16_t*>(p.out) + (static_cast<int64_t>(t.p0) + row) * p.out_cols + oc;
   const int cols = p.out_cols - oc;
   // 32-byte stores where rows allow: 16-byte ones write each sector in halves
@@ -212,12 +227,12 @@ template <Kind KIND>
 __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t, int quarter, int half, int lane,
                                               uint8_t* stage, const uint64_t (*acc)[16]) {
   using C = Config<KIND>;
-  const int first = half * C::kGroupCols;
+  const int n = half == 0 ? t.n[0] : t.n[1], first = half == 0 ? 0 : t.n[0];
   const int col0 = t.p0 + quarter * 32;                     // the warp's first column of out
   const int64_t row0 = (KIND == kWgrad ? static_cast<int64_t>(t.expert) * p.dy_rows : 0) + t.q0;
 #pragma unroll
-  for (int c = 0; c < C::kGroupCols / kBatchCols; ++c) {
-    if (first + c * kBatchCols >= t.n) break;
+  for (int c = 0; c < C::kAccCols / kBatchCols; ++c) {
+    if (c * kBatchCols >= n) break;
 #pragma unroll
     for (int h = 0; h < 4; ++h) {                           // 8 columns: rows of out
       const int row = first + c * kBatchCols + 8 * h;
@@ -273,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_q16, const GemmParams p) {
   using C = Config<KIND>;
-  constexpr int CTAS = C::kCtas, NBUF = C::kBuffers;
-  static_assert(NBUF <= 4 && C::kTileCols / CTAS * kKBlock <= kQBytes, "buffers of tensor and shared memory");
+  constexpr int CTAS = C::kCtas, NBUF = kBuffers;
+  static_assert(2 * C::kQRows * kKBlock <= kQBytes, "shared memory of Q");
   extern __shared__ uint8_t smem_raw[];
   // The same offset in both CTAs of a pair: the bases are equal.
   Smem& s = *reinterpret_cast<Smem*>(smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023));
@@ -290,11 +305,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       ptx::mbar_init(&s.full[i], 1);
       ptx::mbar_init(&s.empty[i], 1);
     }
-    for (int i = 0; i < NBUF; ++i) {
-      ptx::mbar_init(&s.acc_full[i], 3);           // the commit, and the scales' two warps
-      ptx::mbar_init(&s.acc_empty[i], kEpilogueWarps * CTAS);
-      ptx::mbar_init(&s.scale_empty[i], kEpilogueWarps);
-    }
+    for (int i = 0; i < NBUF; ++i)
+      for (int h = 0; h < 2; ++h) {
+        ptx::mbar_init(&s.acc_full[h][i], 2);      // the commit, and the scales' warp
+        ptx::mbar_init(&s.acc_empty[h][i], kEpilogueWarps / 2 * CTAS);
+        ptx::mbar_init(&s.scale_empty[h][i], kEpilogueWarps / 2);
+      }
     ptx::fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc<CTAS>(&s.tmem, kTmemCols);
@@ -337,12 +353,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     if (e < p.num_experts) s.tile_end[e] = before + sum;
     __syncthreads();
   }
-  const int tiles = running;
+  const int tiles = uniform(running);
   tc::fence_before();
   __syncthreads();
   if (CTAS == 2) tc::cluster_sync();   // the pair's barriers and tensor memory exist
   tc::fence_after();
-  const uint32_t tmem = s.tmem;
+  const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(s.tmem)));
   const int first_tile = static_cast<int>(blockIdx.x) / CTAS, step = static_cast<int>(gridDim.x) / CTAS;
   bool ok = true;
 
@@ -356,24 +372,26 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       uint32_t loads = 0;
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
-        // an equal share of Q by each CTA of a pair: 128 rows in one box, whether they
-        // exist or not; kFew: 64 or, for the shortest segments, 16 a box
-        const bool small = KIND == kFew && tile.n <= 16, two = KIND == kFew && tile.n > 64;
-        const int q = tile.q0 + rank * (tile.n / CTAS);
-        const uint32_t bytes = CTAS * (kPBytes + (small ? 16 : KIND == kFew && !two ? 64 : 128) * kKBlock);
-        const int p_plane = KIND == kFew ? tile.expert : 0, q_plane = KIND == kMany ? tile.expert : 0;
-        int x = tile.k0;
-        for (int kb = 0; kb < tile.kblocks; ++kb, x += kKBlock) {
+        // Q rows of each accumulator, an equal share by each CTA of a pair, in one box:
+        // 64 rows, or 16 for the shortest segments
+        const int n0 = uniform(tile.n[0]), n1 = uniform(tile.n[1]);
+        const bool two = n1 > 0, small = KIND == kFew && n0 <= 16;
+        const int q0 = uniform(tile.q0 + rank * (n0 / CTAS)), q1 = uniform(tile.q0 + n0 + rank * (n1 / CTAS));
+        const uint32_t bytes = CTAS * (kPBytes + (two ? 128 : small ? 16 : 64) * kKBlock);
+        const int expert = uniform(tile.expert), p0 = uniform(tile.p0), kblocks = uniform(tile.kblocks);
+        const int p_plane = KIND == kFew ? expert : 0, q_plane = KIND == kMany ? expert : 0;
+        int x = uniform(tile.k0);
+        for (int kb = 0; kb < kblocks; ++kb, x += kKBlock) {
           if (!(ok = wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns))) break;
           if (tc::elect_one()) {
             uint32_t bar = ptx::smem_addr(&s.full[ring.i]);
             const uint32_t dst = ptx::smem_addr(s.stage[ring.i]);
             if (leader) ptx::mbar_arrive_expect_tx(&s.full[ring.i], bytes + (loads == 0 ? p.extra_tx : 0));
             if (CTAS == 2) bar = tc::map_to_rank(bar, 0);
-            tc::load_box<CTAS>(dst, &map_p, x, tile.p0, p_plane, bar);
-            if (small) tc::load_box<CTAS>(dst + kPBytes, &map_q16, x, q, q_plane, bar);
-            else tc::load_box<CTAS>(dst + kPBytes, &map_q, x, q, q_plane, bar);
-            if (two) tc::load_box<CTAS>(dst + kPBytes + 64 * kKBlock, &map_q, x, q + 64, q_plane, bar);
+            tc::load_box<CTAS>(dst, &map_p, x, p0, p_plane, bar);
+            if (small) tc::load_box<CTAS>(dst + kPBytes, &map_q16, x, q0, q_plane, bar);
+            else tc::load_box<CTAS>(dst + kPBytes, &map_q, x, q0, q_plane, bar);
+            if (two) tc::load_box<CTAS>(dst + kPBytes + C::kQRows * kKBlock, &map_q, x, q1, q_plane, bar);
           }
           __syncwarp();
           ring.next();
@@ -385,31 +403,49 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         if (loads >= kStages) ok &= wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns);
     } else if (warp == 1 && leader) {
       // ---- MMA -----------------------------------------------------------
-      // The two barriers of a k-block are asked together: a ready one answers after
-      // ~60 cycles.
+      // The three barriers of a k-block are asked together: a ready one answers after
+      // ~60 cycles, and three in turn would take as long as the MMAs.
       Ring<kStages> ring;
       Ring<NBUF> buf;
       uint32_t used = 0;
       const uint64_t p_desc = tc::operand_desc(ptx::smem_addr(s.stage[0]));
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
-        const uint32_t idesc = tc::instr_desc(kPRows * CTAS, tile.n);
-        for (int kb = 0; kb < tile.kblocks; ++kb) {
+        const int kblocks = uniform(tile.kblocks), n0 = uniform(tile.n[0]), n1 = uniform(tile.n[1]);
+        const uint32_t idesc[2] = {tc::instr_desc(kPRows * CTAS, n0), tc::instr_desc(kPRows * CTAS, n1)};
+        const bool two = n1 > 0;
+        for (int kb = 0; kb < kblocks; ++kb) {
           const bool in = ptx::mbar_try_wait_parity(&s.full[ring.i], ring.phase);
-          const bool free = ptx::mbar_try_wait_parity(&s.acc_empty[buf.i], buf.phase ^ 1);
-          if (!__all_sync(0xffffffffu, in && free)) {
+          const bool free0 = ptx::mbar_try_wait_parity(&s.acc_empty[0][buf.i], buf.phase ^ 1);
+          const bool free1 = ptx::mbar_try_wait_parity(&s.acc_empty[1][buf.i], buf.phase ^ 1);
+          if (!__all_sync(0xffffffffu, in && free0)) {
             ok = wait_warp(&s.full[ring.i], ring.phase, p.wait_ns) &&
-                 wait_warp(&s.acc_empty[buf.i], buf.phase ^ 1, p.wait_ns);
+                 wait_warp(&s.acc_empty[0][buf.i], buf.phase ^ 1, p.wait_ns);
             if (!ok) break;
           }
           tc::fence_after();
+          const uint64_t a = p_desc + ring.i * (kStageBytes >> 4);
+          const uint32_t d = tmem + buf.i * C::kTileCols;
           if (tc::elect_one()) {
-            const uint64_t a = p_desc + ring.i * (kStageBytes >> 4);
             const uint64_t q = a + (kPBytes >> 4);
-            const uint32_t d = tmem + buf.i * C::kTileCols;
 #pragma unroll
-            for (int k = 0; k < kKBlock / 32; ++k) tc::mma_e4m3<CTAS>(d, a + 2 * k, q + 2 * k, idesc, k > 0);
-            tc::commit<CTAS>(&s.acc_full[buf.i]);
+            for (int k = 0; k < kKBlock / 32; ++k) tc::mma_e4m3<CTAS>(d, a + 2 * k, q + 2 * k, idesc[0], k > 0);
+            tc::commit<CTAS>(&s.acc_full[0][buf.i]);
+            if (!two) tc::commit<CTAS>(&s.acc_full[1][buf.i]);
+          }
+          __syncwarp();
+          if (!__all_sync(0xffffffffu, free1)) {
+            if (!(ok = wait_warp(&s.acc_empty[1][buf.i], buf.phase ^ 1, p.wait_ns))) break;
+          }
+          tc::fence_after();
+          if (tc::elect_one()) {
+            if (two) {
+              const uint64_t q = a + ((kPBytes + C::kQRows * kKBlock) >> 4);
+#pragma unroll
+              for (int k = 0; k < kKBlock / 32; ++k)
+                tc::mma_e4m3<CTAS>(d + C::kAccCols, a + 2 * k, q + 2 * k, idesc[1], k > 0);
+              tc::commit<CTAS>(&s.acc_full[1][buf.i]);
+            }
             tc::commit<CTAS>(&s.empty[ring.i]);
           }
           __syncwarp();
@@ -419,10 +455,13 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
       }
       for (uint32_t i = 0; i < NBUF; ++i, ++used, buf.next())   // the epilogues' last (remote) arrivals
-        if (used >= NBUF) ok &= wait_warp(&s.acc_empty[buf.i], buf.phase ^ 1, p.wait_ns);
+        if (used >= NBUF) {
+          ok &= wait_warp(&s.acc_empty[0][buf.i], buf.phase ^ 1, p.wait_ns);
+          ok &= wait_warp(&s.acc_empty[1][buf.i], buf.phase ^ 1, p.wait_ns);
+        }
     } else if (warp >= 2) {
       // ---- scales --------------------------------------------------------
-      // Warp 2 + h brings those of epilogue group h, through registers and kAhead
+      // Warp 2 + h brings those of accumulator h, through registers and kAhead
       // k-blocks ahead: one for each receive row (kMany: accumulator row, else
       // column), times the weights' one; kWgrad: one for each column and row.
       constexpr int kAhead = 3, kRows = 128 / 32;
@@ -431,7 +470,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
         const int64_t kb0 = tile.k0 / kKBlock;
-        const int skip = KIND == kMany ? 0 : half * C::kGroupCols;
+        const int skip = KIND != kMany && half == 1 ? tile.n[0] : 0;
         const int valid = (KIND == kMany ? tile.p_valid : tile.q_valid) - skip - lane;
         const float* rs = p.row_sf + kb0 * p.row_sf_pitch + (KIND == kMany ? tile.p0 : tile.q0) + skip + lane;
         const int block = KIND == kMany ? tile.q0 / 128 + half : tile.p0 / 128;
@@ -458,7 +497,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 #pragma unroll
           for (int d = 0; d < kAhead; ++d) {
             if (kb + d >= tile.kblocks) break;
-            if (!(ok = wait_warp(&s.scale_empty[ring.i], ring.phase ^ 1, p.wait_ns))) break;
+            if (!(ok = wait_warp(&s.scale_empty[half][ring.i], ring.phase ^ 1, p.wait_ns))) break;
             float* to = s.scale[half][ring.i];
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
@@ -469,7 +508,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
               if (KIND == kWgrad) to[128 + j] = w[d][i];
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s.acc_full[ring.i]);
+            if (lane == 0) ptx::mbar_arrive(&s.acc_full[half][ring.i]);
             ring.next();
             fetch(kb + d + kAhead, r[d], w[d]);
           }
@@ -478,19 +517,19 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     }
   } else {
     // ---- epilogue --------------------------------------------------------
-    // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of its group's columns.
+    // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of one accumulator.
     tc::reg_inc<kEpilogueRegs>();
-    constexpr int kBatches = C::kGroupCols / kBatchCols;
+    constexpr int kBatches = C::kAccCols / kBatchCols;
     const int ew = warp - 4, quarter = warp % 4, half = ew / 4;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * C::kGroupCols;
-    uint32_t freed = ptx::smem_addr(&s.acc_empty[0]);   // the leader's barriers
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * C::kAccCols;
+    uint32_t freed = ptx::smem_addr(&s.acc_empty[half][0]);   // the leader's barriers
     if (CTAS == 2) freed = tc::map_to_rank(freed, 0);
     Ring<NBUF> buf;
     for (int t = first_tile; t < tiles && ok; t += step) {
       int n, kblocks;                                         // all that lives over the k-blocks
       {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
-        n = tile.n - half * C::kGroupCols;
+        n = half == 0 ? tile.n[0] : tile.n[1];
         kblocks = tile.kblocks;
       }
       uint64_t acc[kBatches][16];                             // pairs of sums: see store_rows, store_columns
@@ -499,7 +538,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[c][i] = 0;
       for (int kb = 0; kb < kblocks; ++kb) {
-        if (!(ok = wait_warp(&s.acc_full[buf.i], buf.phase, p.wait_ns))) break;
+        if (!(ok = wait_warp(&s.acc_full[half][buf.i], buf.phase, p.wait_ns))) break;
         tc::fence_after();
         const float* sc = s.scale[half][buf.i];
         const uint32_t from = lane_base + buf.i * C::kTileCols;
@@ -548,8 +587,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
         __syncwarp();
         if (lane == 0) {
-          if (n <= 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
-          ptx::mbar_arrive(&s.scale_empty[buf.i]);
+          if (n == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+          ptx::mbar_arrive(&s.scale_empty[half][buf.i]);
         }
         buf.next();
       }
@@ -660,7 +699,7 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream) {
   CUtensorMap rows, rows16, weights;
   cudaError_t e = encode(&rows, a.x, a.width_in, a.capacity, 1, many ? kPRows : 64);
   if (e == cudaSuccess) e = encode(&rows16, a.x, a.width_in, a.capacity, 1, 16);
-  if (e == cudaSuccess) e = encode(&weights, a.w, a.width_in, a.width_out, a.num_experts, 128);
+  if (e == cudaSuccess) e = encode(&weights, a.w, a.width_in, a.width_out, a.num_experts, many ? 64 : kPRows);
   if (e != cudaSuccess) return e;
   return many ? launch<kMany>(rows, weights, weights, p, stream) : launch<kFew>(weights, rows, rows16, p, stream);
 }
@@ -674,7 +713,7 @@ cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
   p.dy_rows = static_cast<int>(a.width_out);
   CUtensorMap x, dy;
   cudaError_t e = encode(&x, a.x, a.sf_ld, a.width_in, 1, kPRows);
-  if (e == cudaSuccess) e = encode(&dy, a.w, a.sf_ld, a.width_out, 1, 128);
+  if (e == cudaSuccess) e = encode(&dy, a.w, a.sf_ld, a.width_out, 1, 64);
   return e == cudaSuccess ? launch<kWgrad>(x, dy, dy, p, stream) : e;
 }
 
