@@ -51,8 +51,6 @@ namespace {
 
 enum Kind { kMany, kFew, kWgrad };
 
-constexpr int kThreads = 384;
-constexpr int kEpilogueWarps = 8;
 constexpr int kKBlock = 128;                       // values (and bytes) of K in a scale block
 constexpr int kPRows = 128;                        // accumulator rows of a CTA
 constexpr int kPBytes = kPRows * kKBlock;
@@ -65,10 +63,6 @@ constexpr int kSlotWords = 128 + kPRows;           // scales of columns or rows,
 constexpr int kOutPitch = 96;                      // bytes; 64 of data, 4 rows' 32-byte pieces in different banks
 constexpr int kOutBytes = 8 * kOutPitch;           // a warp's 8 rows x 32 columns of bf16
 constexpr int kTmemCols = 512;
-// Registers a thread: 128 sums and 64 values of tensor memory.
-constexpr int kLaunchRegs = 168, kEpilogueRegs = 224, kOtherRegs = 56;
-static_assert(256 * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split above the launch's total");
-
 template <Kind KIND>
 struct Config {
   static constexpr int kCtas = KIND == kFew ? 1 : 2;
@@ -77,12 +71,21 @@ struct Config {
   static_assert(kBuffers * kTileCols <= kTmemCols, "tensor memory");
   static constexpr int kUnit = 16 * kCtas;                     // column granularity: each CTA of a pair holds n / 2 rows of Q
   static constexpr int kQRows = kAccCols / kCtas;              // rows of Q of an accumulator a CTA loads at most
+  static constexpr int kSplit = KIND == kMany ? 2 : 1;         // epilogue warps side by side in an accumulator
+  static constexpr int kWarpCols = kAccCols / kSplit;
+  static constexpr int kEpilogueWarps = 8 * kSplit;
+  static constexpr int kThreads = 128 + 32 * kEpilogueWarps;
+  // Registers a thread: sums, and values of tensor memory.
+  static constexpr int kLaunchRegs = KIND == kMany ? 96 : 168;
+  static constexpr int kEpilogueRegs = KIND == kMany ? 104 : 224, kOtherRegs = KIND == kMany ? 64 : 56;
+  static_assert(32 * kEpilogueWarps * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
+                "register split above the launch's total");
 };
 
 struct Smem {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
   alignas(16) float scale[2][kBuffers][kSlotWords];   // [accumulator][buffer]
-  alignas(16) uint8_t out[kEpilogueWarps][kOutBytes];
+  alignas(16) uint8_t out[8][kOutBytes];
   int tile_end[MOE_MAX_EXPERTS];                   // tiles of experts 0..e
   int seg_start[MOE_MAX_EXPERTS];
   int seg_count[MOE_MAX_EXPERTS];
@@ -90,7 +93,7 @@ struct Smem {
   uint64_t acc_full[2][kBuffers], acc_empty[2][kBuffers];   // full: product and scales are there
   uint64_t scale_empty[2][kBuffers];
   uint32_t tmem;
-  int warp_sum[kThreads / 32];
+  int warp_sum[20];
 };
 // The dynamic base is only known to be 16-byte aligned: room to align it.
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
@@ -192,16 +195,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Rows of out from sums whose thread owns a row (kMany).
-// acc[c][i]: columns 32 c + 2 i, +1 of the accumulator.
-__device__ __forceinline__ void store_rows(const GemmParams& p, const Tile& t, int row, int half, const uint64_t (*acc)[16]) {
-  const int oc = t.q0 + half * 128, n = half == 0 ? t.n[0] : t.n[1];
-  if (row >= t.p_valid || n == 0) return;
+// acc[c][i]: column 32 c + 2 i, +1 after column `col` of the tile.
+__device__ __forceinline__ void store_rows(const GemmParams& p, const Tile& t, int row, int col, const uint64_t (*acc)[16]) {
+  using C = Config<kMany>;
+  const int oc = t.q0 + col;
+  if (row >= t.p_valid || oc >= p.out_cols) return;
   uint16_t* out = static_cast<uint16_t*>(p.out) + (static_cast<int64_t>(t.p0) + row) * p.out_cols + oc;
   const int cols = p.out_cols - oc;
   // 32-byte stores where rows allow: 16-byte ones write each sector in halves
   const bool wide = p.out_cols % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+  for (int c = 0; c < C::kWarpCols / kBatchCols; ++c)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t v[8];
@@ -277,18 +281,18 @@ __device__ __forceinline__ void zero_gap(const GemmParams& p, const Smem& s, con
   int64_t r = static_cast<int64_t>(s.seg_start[t.expert]) + s.seg_count[t.expert];
   // the tile's columns of out, a share of the rows for each warp (of both CTAs)
   const int c0 = KIND == kMany ? t.q0 : t.p0, cols = KIND == kMany ? t.q_valid : t.p_valid;
-  const int warps = KIND == kMany ? C::kCtas * kEpilogueWarps : kEpilogueWarps;
-  for (r += KIND == kMany ? rank * kEpilogueWarps + ew : ew; r < end; r += warps)
+  const int warps = KIND == kMany ? C::kCtas * C::kEpilogueWarps : C::kEpilogueWarps;
+  for (r += KIND == kMany ? rank * C::kEpilogueWarps + ew : ew; r < end; r += warps)
     for (int c = lane * 8; c < cols; c += 256)
       ptx::st_v4(static_cast<uint16_t*>(p.out) + r * p.out_cols + c0 + c, make_uint4(0, 0, 0, 0));
 }
 
 template <Kind KIND>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Config<KIND>::kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_q16, const GemmParams p) {
   using C = Config<KIND>;
-  constexpr int CTAS = C::kCtas, NBUF = kBuffers;
+  constexpr int CTAS = C::kCtas, NBUF = kBuffers, kThreads = C::kThreads, kEpilogueWarps = C::kEpilogueWarps;
   static_assert(2 * C::kQRows * kKBlock <= kQBytes, "shared memory of Q");
   extern __shared__ uint8_t smem_raw[];
   // The same offset in both CTAs of a pair: the bases are equal.
@@ -363,7 +367,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
   bool ok = true;
 
   if (warp < 4) {
-    tc::reg_dec<kOtherRegs>();
+    tc::reg_dec<C::kOtherRegs>();
     if (warp == 0) {
       // ---- loads ---------------------------------------------------------
       // The warp stays together so that addresses live in uniform registers; one
@@ -518,10 +522,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
   } else {
     // ---- epilogue --------------------------------------------------------
     // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of one accumulator.
-    tc::reg_inc<kEpilogueRegs>();
-    constexpr int kBatches = C::kAccCols / kBatchCols;
-    const int ew = warp - 4, quarter = warp % 4, half = ew / 4;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * C::kAccCols;
+    tc::reg_inc<C::kEpilogueRegs>();
+    constexpr int kBatches = C::kWarpCols / kBatchCols;
+    const int ew = warp - 4, quarter = warp % 4, half = ew / (4 * C::kSplit), part = ew / 4 % C::kSplit;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * C::kAccCols + part * C::kWarpCols;
     uint32_t freed = ptx::smem_addr(&s.acc_empty[half][0]);   // the leader's barriers
     if (CTAS == 2) freed = tc::map_to_rank(freed, 0);
     Ring<NBUF> buf;
@@ -552,6 +556,23 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
           ps[0] = tc::pack2(rows[0], rows[8]);
           ps[1] = tc::pack2(rows[16], rows[24]);
         }
+        if constexpr (KIND == kMany) {
+          // columns past n are read and added for nothing: only the last tile across has any
+#pragma unroll
+          for (int c = 0; c < C::kWarpCols / 16; ++c) {
+            float v[16];
+            tc::ld_32x16(from + c * 16, v);
+            tc::wait_ld();
+            if (c == C::kWarpCols / 16 - 1) {   // all is in registers: the tensor core may have the buffer back
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              acc[c * 16 / 32][c * 8 % 16 + i] = tc::fma2(tc::pack2(v[2 * i], v[2 * i + 1]), ps[0], acc[c * 16 / 32][c * 8 % 16 + i]);
+          }
+        } else {
 #pragma unroll
         for (int c = 0; c < kBatches; c += 2) {
           if (c * kBatchCols >= n) break;
@@ -559,9 +580,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
           float4 f[2][2];
 #pragma unroll
           for (int d = 0; d < 2; ++d) {
-            if (KIND == kMany) {
-              tc::ld_32x32(from + (c + d) * kBatchCols, v[d]);
-            } else {
+            {
               tc::ld_16x32(from + (c + d) * kBatchCols, v[d]);
               tc::ld_16x32(from + (c + d) * kBatchCols + (16u << 16), v[d] + 16);
               f[d][0] = *reinterpret_cast<const float4*>(sc + (c + d) * kBatchCols + (lane % 4) * 4);
@@ -581,13 +600,14 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             for (int i = 0; i < 16; ++i) {
               uint64_t v2 = tc::pack2(v[d][2 * i], v[d][2 * i + 1]);
               if (KIND == kWgrad) v2 = tc::mul2(v2, ps[i / 8]);
-              acc[c + d][i] = tc::fma2(v2, KIND == kMany ? ps[0] : tc::pack2(q[i % 8], q[i % 8]), acc[c + d][i]);
+              acc[c + d][i] = tc::fma2(v2, tc::pack2(q[i % 8], q[i % 8]), acc[c + d][i]);
             }
           }
         }
+        }
         __syncwarp();
         if (lane == 0) {
-          if (n == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+          if (KIND != kMany && n == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
           ptx::mbar_arrive(&s.scale_empty[half][buf.i]);
         }
         buf.next();
@@ -595,7 +615,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       if (!ok) break;
 
       const Tile tile = get_tile<KIND>(p, s, t, rank);
-      if constexpr (KIND == kMany) store_rows(p, tile, quarter * 32 + lane, half, acc);
+      if constexpr (KIND == kMany) store_rows(p, tile, quarter * 32 + lane, half * C::kAccCols + part * C::kWarpCols, acc);
       else store_columns<KIND>(p, tile, quarter, half, lane, s.out[ew], acc);
       if (KIND != kWgrad && tile.last) zero_gap<KIND>(p, s, tile, rank, ew, lane);
     }
@@ -653,7 +673,7 @@ cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const CUt
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() / CTAS * CTAS));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Config<KIND>::kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
