@@ -9,16 +9,14 @@
 // warps add it, times its scales, to fp32 sums in registers:
 //
 //   warp 0      TMA loads of P and Q tiles (128-byte rows, one k-block wide)
-//   warp 1      tcgen05.mma, 4 per k-block and accumulator
-//   warps 2-3   the k-block's scales to shared memory
-//   warps 4-11  tensor memory -> fp32 sums; at the tile's end rows of out
+//   warps 1-2   tcgen05.mma, 4 per k-block, each into an accumulator of its own
+//   warp 3      the k-block's scales to shared memory
+//   warps 4-    tensor memory -> fp32 sums; at the tile's end rows of out
 //
 // D[p, q] = <P_p, Q_q>: P gives the 128 accumulator rows (tensor-memory lanes) of
-// a CTA, Q its columns.  A tile's columns are two accumulators, each with its own
-// buffers, barriers and 4 of the 8 epilogue warps: the tensor core fills one
-// while the other is read.  Three kinds:
+// a CTA, Q its columns.  Three kinds:
 //
-//   kMany   P = receive rows, Q = weights; a pair of CTAs shares one 256 x 256 MMA,
+//   kMany   P = receive rows, Q = weights; a pair of CTAs shares 256 x 256 tiles,
 //           each loading half of Q.  A thread owns a receive row, and both scales
 //           of a k-block and 128-column block multiply to one number for it.
 //   kFew    P = weights, Q = receive rows; one CTA.  The tensor core takes any
@@ -26,11 +24,19 @@
 //           128.  Bound by the reading of the weights.
 //   kWgrad  P = x^T, Q = dy^T (so that columns of dw run along lanes); a pair.
 //
-// What bounds kMany: adding 256 columns of a k-block takes the epilogue warps
-// ~460 cycles (measured alone), about what the MMAs take (512).  Loading 64
-// columns of tensor memory at a time, without a second buffer of registers, is
-// faster than prefetching 32 (458 against 602 cycles), and a scale per row
-// beats one per column (610).
+// What shaped it, measured on 16 experts of 1024 rows, 7168 -> 4096:
+//  - From an MMA's issue to a waiting warp it takes ~280 cycles more than the MMA
+//    (512 a k-block), and ~210 for the peer's word that a buffer was read.  Tensor
+//    memory has room for two buffers of 256 columns, so a tile is two accumulators of
+//    128 with buffers and barriers of their own: 435 -> 412 us.
+//  - Issuing an MMA takes ~53 cycles whatever its size, so each accumulator has an
+//    MMA warp: 377 -> 367 us.  Loop bounds and tile numbers of the issuing warps are kept in
+//    uniform registers; from ordinary ones every operand is moved over one by one.
+//  - The epilogue is bound by its chain of latencies (wait, load, add), so kMany has 16
+//    warps of 64 columns, 412 -> 386 us; 32 columns of tensor memory in flight,
+//    386 -> 375 us.
+//  - tcgen05.ld of 32x32 and 16x128-bit shapes moves a register of an SM quarter in
+//    1.2 cycles, the 16x256-bit one in 2.0.
 //
 // One persistent CTA (or pair) per SM walks the tiles of all experts.  All sums
 // are fp32; the result is rounded once.
@@ -56,48 +62,57 @@ constexpr int kPRows = 128;                        // accumulator rows of a CTA
 constexpr int kPBytes = kPRows * kKBlock;
 constexpr int kQBytes = 128 * kKBlock;             // a CTA loads at most 128 rows of Q
 constexpr int kStageBytes = kPBytes + kQBytes;
-constexpr int kStages = 6;
-constexpr int kBuffers = 2;                        // of an accumulator
 constexpr int kBatchCols = 32;                     // columns of one tensor-memory load
 constexpr int kSlotWords = 128 + kPRows;           // scales of columns or rows, then (kWgrad) of rows
-constexpr int kOutPitch = 96;                      // bytes; 64 of data, 4 rows' 32-byte pieces in different banks
-constexpr int kOutBytes = 8 * kOutPitch;           // a warp's 8 rows x 32 columns of bf16
 constexpr int kTmemCols = 512;
+constexpr int kAccCols = 128;                      // columns of an accumulator
+constexpr int kOutPitch = 96;                      // bytes; 64 of data, 4 rows' 32-byte pieces in different banks
+constexpr int kOutBytes = 32 * kOutPitch;          // a warp's 32 rows x 32 columns of bf16
+
 template <Kind KIND>
 struct Config {
   static constexpr int kCtas = KIND == kFew ? 1 : 2;
-  static constexpr int kAccCols = KIND == kFew ? 64 : 128;     // columns of an accumulator
-  static constexpr int kTileCols = 2 * kAccCols;
-  static_assert(kBuffers * kTileCols <= kTmemCols, "tensor memory");
+  static constexpr int kAccs = KIND == kFew ? 1 : 2;           // accumulators of a tile
+  static constexpr int kTileCols = kAccs * kAccCols;
+  static constexpr int kBuffers = kTmemCols / kTileCols;       // of an accumulator
   static constexpr int kUnit = 16 * kCtas;                     // column granularity: each CTA of a pair holds n / 2 rows of Q
   static constexpr int kQRows = kAccCols / kCtas;              // rows of Q of an accumulator a CTA loads at most
-  static constexpr int kSplit = KIND == kMany ? 2 : 1;         // epilogue warps side by side in an accumulator
+  static constexpr int kSplit = KIND == kWgrad ? 1 : 2;        // epilogue warps side by side in an accumulator
   static constexpr int kWarpCols = kAccCols / kSplit;
-  static constexpr int kEpilogueWarps = 8 * kSplit;
+  static constexpr int kEpilogueWarps = 4 * kAccs * kSplit;
   static constexpr int kThreads = 128 + 32 * kEpilogueWarps;
+  static constexpr int kStages = KIND == kMany ? 6 : 5;        // what the staging of out leaves room for
   // Registers a thread: sums, and values of tensor memory.
   static constexpr int kLaunchRegs = KIND == kMany ? 96 : 168;
   static constexpr int kEpilogueRegs = KIND == kMany ? 104 : 224, kOtherRegs = KIND == kMany ? 64 : 56;
   static_assert(32 * kEpilogueWarps * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
                 "register split above the launch's total");
+  static_assert(kAccs * kQRows * kKBlock <= kQBytes, "shared memory of Q");
 };
 
-struct Smem {
-  alignas(1024) uint8_t stage[kStages][kStageBytes];
-  alignas(16) float scale[2][kBuffers][kSlotWords];   // [accumulator][buffer]
-  alignas(16) uint8_t out[8][kOutBytes];
+// What the roles share besides the tiles.
+struct Shared {
+  alignas(16) float scale[2][4][kSlotWords];       // [accumulator][buffer]
   int tile_end[MOE_MAX_EXPERTS];                   // tiles of experts 0..e
   int seg_start[MOE_MAX_EXPERTS];
   int seg_count[MOE_MAX_EXPERTS];
-  uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2][kBuffers], acc_empty[2][kBuffers];   // full: product and scales are there
-  uint64_t scale_empty[2][kBuffers];
+  uint64_t full[6], empty[6];
+  uint64_t acc_full[2][4], acc_empty[2][4];        // full: product and scales are there
+  uint64_t scale_empty[2][4];
   uint32_t tmem;
   int warp_sum[20];
 };
+template <Kind KIND>
+struct Smem {
+  alignas(1024) uint8_t stage[Config<KIND>::kStages][kStageBytes];
+  alignas(16) uint8_t out[KIND == kMany ? 16 : Config<KIND>::kEpilogueWarps * kOutBytes];
+  Shared s;
+};
 // The dynamic base is only known to be 16-byte aligned: room to align it.
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory of one SM");
+template <Kind KIND>
+constexpr size_t kSmemBytes = sizeof(Smem<KIND>) + 1024;
+static_assert(kSmemBytes<kMany> <= 232448 && kSmemBytes<kFew> <= 232448 && kSmemBytes<kWgrad> <= 232448,
+              "shared memory of one SM");
 
 struct Tile {
   int expert;
@@ -124,7 +139,7 @@ __device__ __forceinline__ int col_tiles(const GemmParams& p) {
 }
 
 template <Kind KIND>
-__device__ __forceinline__ Tile get_tile(const GemmParams& p, const Smem& s, int t, int rank) {
+__device__ __forceinline__ Tile get_tile(const GemmParams& p, const Shared& s, int t, int rank) {
   using C = Config<KIND>;
   int lo = 0, hi = p.num_experts - 1;     // first expert whose tiles end after t
   while (lo < hi) {
@@ -154,10 +169,10 @@ __device__ __forceinline__ Tile get_tile(const GemmParams& p, const Smem& s, int
     r.q0 = (KIND == kWgrad ? 0 : start) + row * per;
     r.q_valid = max(0, min(per, rows - row * per));
   }
-  // kMany: an accumulator is one scale block of the weights; else the two are of
+  // kMany: an accumulator is one scale block of the weights; kWgrad: the two are of
   // like size, the first in whole batches
   const int n = max(C::kUnit, ceil_div(r.q_valid, C::kUnit) * C::kUnit);
-  r.n[0] = n <= C::kAccCols ? n : KIND == kMany ? C::kAccCols : ceil_div(n / 2, kBatchCols) * kBatchCols;
+  r.n[0] = n <= kAccCols ? n : KIND == kMany ? kAccCols : ceil_div(n / 2, kBatchCols) * kBatchCols;
   r.n[1] = n - r.n[0];
   return r;
 }
@@ -228,54 +243,58 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const Tile& t, i
 // acc[c][8 * up + i]: rows 16 * up + lane / 4 and 8 further on of the warp's 32,
 // column 32 * c + 4 * i + lane % 4 of the accumulator.
 template <Kind KIND>
-__device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t, int quarter, int half, int lane,
+__device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t, int quarter, int acc_id, int part, int lane,
                                               uint8_t* stage, const uint64_t (*acc)[16]) {
   using C = Config<KIND>;
-  const int n = half == 0 ? t.n[0] : t.n[1], first = half == 0 ? 0 : t.n[0];
+  const int n = (acc_id == 0 ? t.n[0] : t.n[1]) - part * C::kWarpCols;
+  const int first = (acc_id == 0 ? 0 : t.n[0]) + part * C::kWarpCols;
   const int col0 = t.p0 + quarter * 32;                     // the warp's first column of out
   const int64_t row0 = (KIND == kWgrad ? static_cast<int64_t>(t.expert) * p.dy_rows : 0) + t.q0;
 #pragma unroll
-  for (int c = 0; c < C::kAccCols / kBatchCols; ++c) {
+  for (int c = 0; c < C::kWarpCols / kBatchCols; ++c) {
     if (c * kBatchCols >= n) break;
+    const int row = first + c * kBatchCols;
+    if (KIND == kWgrad && p.out_fp32) {
+      // 4 rows x 8 columns a store: whole 32-byte sectors
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {                           // 8 columns: rows of out
-      const int row = first + c * kBatchCols + 8 * h;
-      if (KIND == kWgrad && p.out_fp32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int up = i / 2, at = row + 4 * (i % 2) + lane % 4;
-          const float2 f = tc::unpack2(acc[c][8 * up + 2 * h + i % 2]);
-          const int oc = col0 + 16 * up + lane / 4;
-          if (at < t.q_valid) {
-            float* o = static_cast<float*>(p.out) + (row0 + at) * p.out_cols + oc;
-            if (oc < p.out_cols) o[0] = p.accumulate ? o[0] + f.x : f.x;
-            if (oc + 8 < p.out_cols) o[8] = p.accumulate ? o[8] + f.y : f.y;
-          }
+      for (int i = 0; i < 16; ++i) {
+        const int up = i / 8, at = row + 4 * (i % 8) + lane % 4;
+        const float2 f = tc::unpack2(acc[c][i]);
+        const int oc = col0 + 16 * up + lane / 4;
+        if (at < t.q_valid) {
+          float* o = static_cast<float*>(p.out) + (row0 + at) * p.out_cols + oc;
+          if (oc < p.out_cols) o[0] = p.accumulate ? o[0] + f.x : f.x;
+          if (oc + 8 < p.out_cols) o[8] = p.accumulate ? o[8] + f.y : f.y;
         }
-        continue;
       }
-      // Lanes j and j ^ 4 hold rows k and k + 1 (k = j/4 even) and the rows 8 further
-      // on; they trade so that each has two neighbours: one 32-bit word of out.
-      const bool odd = (lane & 4) != 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {                         // up = i / 2, column 4 * (i % 2) + lane % 4
-        const float2 f = tc::unpack2(acc[c][8 * (i / 2) + 2 * h + i % 2]);
-        const float other = __shfl_xor_sync(0xffffffffu, odd ? f.x : f.y, 4);
-        *reinterpret_cast<uint32_t*>(stage + (4 * (i % 2) + lane % 4) * kOutPitch + 32 * (i / 2) + (odd ? 16 : 0) +
-                                     lane / 8 * 4) = odd ? pack_bf16(other, f.y) : pack_bf16(f.x, other);
-      }
-      __syncwarp();
-      const int r = row + lane / 4, oc = col0 + (lane % 4) * 8;
-      const uint4 w = ptx::ld_shared_v4(stage + lane / 4 * kOutPitch + (lane % 4) * 16);
-      if (r < t.q_valid && oc < p.out_cols) ptx::st_v4(static_cast<uint16_t*>(p.out) + (row0 + r) * p.out_cols + oc, w);
-      __syncwarp();
+      continue;
     }
+    // Lanes j and j ^ 4 hold rows k and k + 1 (k = j/4 even) and the rows 8 further
+    // on; they trade so that each has two neighbours: one 32-bit word of out.
+    const bool odd = (lane & 4) != 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {                          // up = i / 8, column 4 * (i % 8) + lane % 4
+      const float2 f = tc::unpack2(acc[c][i]);
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? f.x : f.y, 4);
+      *reinterpret_cast<uint32_t*>(stage + (4 * (i % 8) + lane % 4) * kOutPitch + 32 * (i / 8) + (odd ? 16 : 0) +
+                                   lane / 8 * 4) = odd ? pack_bf16(other, f.y) : pack_bf16(f.x, other);
+    }
+    __syncwarp();
+    const int oc = col0 + (lane % 4) * 8;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int r = 8 * h + lane / 4;
+      const uint4 w = ptx::ld_shared_v4(stage + r * kOutPitch + (lane % 4) * 16);
+      if (row + r < t.q_valid && oc < p.out_cols)
+        ptx::st_v4(static_cast<uint16_t*>(p.out) + (row0 + row + r) * p.out_cols + oc, w);
+    }
+    __syncwarp();
   }
 }
 
 // Alignment-gap rows of the expert's segment: zeros, 16 bytes a lane.
 template <Kind KIND>
-__device__ __forceinline__ void zero_gap(const GemmParams& p, const Smem& s, const Tile& t, int rank, int ew, int lane) {
+__device__ __forceinline__ void zero_gap(const GemmParams& p, const Shared& s, const Tile& t, int rank, int ew, int lane) {
   using C = Config<KIND>;
   const int64_t end = min64(p.expert_offset[t.expert + 1], p.capacity);
   int64_t r = static_cast<int64_t>(s.seg_start[t.expert]) + s.seg_count[t.expert];
@@ -292,11 +311,11 @@ __global__ void __launch_bounds__(Config<KIND>::kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_q16, const GemmParams p) {
   using C = Config<KIND>;
-  constexpr int CTAS = C::kCtas, NBUF = kBuffers, kThreads = C::kThreads, kEpilogueWarps = C::kEpilogueWarps;
-  static_assert(2 * C::kQRows * kKBlock <= kQBytes, "shared memory of Q");
+  constexpr int CTAS = C::kCtas, NBUF = C::kBuffers, ACCS = C::kAccs, kStages = C::kStages, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
   // The same offset in both CTAs of a pair: the bases are equal.
-  Smem& s = *reinterpret_cast<Smem*>(smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023));
+  Smem<KIND>& mem = *reinterpret_cast<Smem<KIND>*>(smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023));
+  Shared& s = mem.s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = CTAS == 2 ? static_cast<int>(tc::cluster_rank()) : 0;
   const bool leader = rank == 0;
@@ -307,13 +326,13 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     if (KIND == kFew) tc::prefetch_map(&map_q16);
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
-      ptx::mbar_init(&s.empty[i], 1);
+      ptx::mbar_init(&s.empty[i], ACCS);           // a commit of each MMA warp
     }
     for (int i = 0; i < NBUF; ++i)
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < ACCS; ++h) {
         ptx::mbar_init(&s.acc_full[h][i], 2);      // the commit, and the scales' warp
-        ptx::mbar_init(&s.acc_empty[h][i], kEpilogueWarps / 2 * CTAS);
-        ptx::mbar_init(&s.scale_empty[h][i], kEpilogueWarps / 2);
+        ptx::mbar_init(&s.acc_empty[h][i], 4 * C::kSplit * CTAS);
+        ptx::mbar_init(&s.scale_empty[h][i], 4 * C::kSplit);
       }
     ptx::fence_mbar_init();
   }
@@ -376,11 +395,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       uint32_t loads = 0;
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
-        // Q rows of each accumulator, an equal share by each CTA of a pair, in one box:
-        // 64 rows, or 16 for the shortest segments
+        // Q rows of each accumulator, an equal share by each CTA of a pair, in boxes of 64;
+        // 16 for the shortest segments
         const int n0 = uniform(tile.n[0]), n1 = uniform(tile.n[1]);
-        const bool two = n1 > 0, small = KIND == kFew && n0 <= 16;
-        const int q0 = uniform(tile.q0 + rank * (n0 / CTAS)), q1 = uniform(tile.q0 + n0 + rank * (n1 / CTAS));
+        const bool small = KIND == kFew && n0 <= 16, two = KIND == kFew ? n0 > 64 : n1 > 0;
+        const int q0 = uniform(tile.q0 + rank * (n0 / CTAS));
+        const int q1 = KIND == kFew ? q0 + 64 : uniform(tile.q0 + n0 + rank * (n1 / CTAS));
         const uint32_t bytes = CTAS * (kPBytes + (two ? 128 : small ? 16 : 64) * kKBlock);
         const int expert = uniform(tile.expert), p0 = uniform(tile.p0), kblocks = uniform(tile.kblocks);
         const int p_plane = KIND == kFew ? expert : 0, q_plane = KIND == kMany ? expert : 0;
@@ -389,13 +409,13 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
           if (!(ok = wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns))) break;
           if (tc::elect_one()) {
             uint32_t bar = ptx::smem_addr(&s.full[ring.i]);
-            const uint32_t dst = ptx::smem_addr(s.stage[ring.i]);
+            const uint32_t dst = ptx::smem_addr(mem.stage[ring.i]);
             if (leader) ptx::mbar_arrive_expect_tx(&s.full[ring.i], bytes + (loads == 0 ? p.extra_tx : 0));
             if (CTAS == 2) bar = tc::map_to_rank(bar, 0);
             tc::load_box<CTAS>(dst, &map_p, x, p0, p_plane, bar);
             if (small) tc::load_box<CTAS>(dst + kPBytes, &map_q16, x, q0, q_plane, bar);
             else tc::load_box<CTAS>(dst + kPBytes, &map_q, x, q0, q_plane, bar);
-            if (two) tc::load_box<CTAS>(dst + kPBytes + C::kQRows * kKBlock, &map_q, x, q1, q_plane, bar);
+            if (two) tc::load_box<CTAS>(dst + kPBytes + 64 * kKBlock, &map_q, x, q1, q_plane, bar);
           }
           __syncwarp();
           ring.next();
@@ -405,114 +425,111 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       // Every stage handed back: no copy or remote arrival is left in flight.
       for (uint32_t i = 0; i < kStages; ++i, ++loads, ring.next())
         if (loads >= kStages) ok &= wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns);
-    } else if (warp == 1 && leader) {
-      // ---- MMA -----------------------------------------------------------
-      // The three barriers of a k-block are asked together: a ready one answers after
-      // ~60 cycles, and three in turn would take as long as the MMAs.
-      Ring<kStages> ring;
-      Ring<NBUF> buf;
-      uint32_t used = 0;
-      const uint64_t p_desc = tc::operand_desc(ptx::smem_addr(s.stage[0]));
-      for (int t = first_tile; t < tiles && ok; t += step) {
-        const Tile tile = get_tile<KIND>(p, s, t, rank);
-        const int kblocks = uniform(tile.kblocks), n0 = uniform(tile.n[0]), n1 = uniform(tile.n[1]);
-        const uint32_t idesc[2] = {tc::instr_desc(kPRows * CTAS, n0), tc::instr_desc(kPRows * CTAS, n1)};
-        const bool two = n1 > 0;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          const bool in = ptx::mbar_try_wait_parity(&s.full[ring.i], ring.phase);
-          const bool free0 = ptx::mbar_try_wait_parity(&s.acc_empty[0][buf.i], buf.phase ^ 1);
-          const bool free1 = ptx::mbar_try_wait_parity(&s.acc_empty[1][buf.i], buf.phase ^ 1);
-          if (!__all_sync(0xffffffffu, in && free0)) {
-            ok = wait_warp(&s.full[ring.i], ring.phase, p.wait_ns) &&
-                 wait_warp(&s.acc_empty[0][buf.i], buf.phase ^ 1, p.wait_ns);
-            if (!ok) break;
-          }
-          tc::fence_after();
-          const uint64_t a = p_desc + ring.i * (kStageBytes >> 4);
-          const uint32_t d = tmem + buf.i * C::kTileCols;
-          if (tc::elect_one()) {
-            const uint64_t q = a + (kPBytes >> 4);
-#pragma unroll
-            for (int k = 0; k < kKBlock / 32; ++k) tc::mma_e4m3<CTAS>(d, a + 2 * k, q + 2 * k, idesc[0], k > 0);
-            tc::commit<CTAS>(&s.acc_full[0][buf.i]);
-            if (!two) tc::commit<CTAS>(&s.acc_full[1][buf.i]);
-          }
-          __syncwarp();
-          if (!__all_sync(0xffffffffu, free1)) {
-            if (!(ok = wait_warp(&s.acc_empty[1][buf.i], buf.phase ^ 1, p.wait_ns))) break;
-          }
-          tc::fence_after();
-          if (tc::elect_one()) {
-            if (two) {
-              const uint64_t q = a + ((kPBytes + C::kQRows * kKBlock) >> 4);
-#pragma unroll
-              for (int k = 0; k < kKBlock / 32; ++k)
-                tc::mma_e4m3<CTAS>(d + C::kAccCols, a + 2 * k, q + 2 * k, idesc[1], k > 0);
-              tc::commit<CTAS>(&s.acc_full[1][buf.i]);
+    } else if (warp < 3) {
+      // ---- MMA: warp 1 + h into accumulator h -----------------------------
+      // The barriers of a k-block are asked together: a ready one answers after ~60
+      // cycles.
+      const int h = warp - 1;
+      if (leader && h < ACCS) {
+        Ring<kStages> ring;
+        Ring<NBUF> buf;
+        uint32_t used = 0;
+        const uint64_t p_desc = tc::operand_desc(ptx::smem_addr(mem.stage[0]));
+        const uint32_t q_off = (kPBytes + h * C::kQRows * kKBlock) >> 4;
+        for (int t = first_tile; t < tiles && ok; t += step) {
+          const Tile tile = get_tile<KIND>(p, s, t, rank);
+          const int kblocks = uniform(tile.kblocks), n = uniform(h == 0 ? tile.n[0] : tile.n[1]);
+          const uint32_t idesc = tc::instr_desc(kPRows * CTAS, n);
+          for (int kb = 0; kb < kblocks; ++kb) {
+            const bool in = ptx::mbar_try_wait_parity(&s.full[ring.i], ring.phase);
+            const bool free = ptx::mbar_try_wait_parity(&s.acc_empty[h][buf.i], buf.phase ^ 1);
+            if (!__all_sync(0xffffffffu, in && free)) {
+              ok = wait_warp(&s.full[ring.i], ring.phase, p.wait_ns) &&
+                   wait_warp(&s.acc_empty[h][buf.i], buf.phase ^ 1, p.wait_ns);
+              if (!ok) break;
             }
-            tc::commit<CTAS>(&s.empty[ring.i]);
+            tc::fence_after();
+            if (tc::elect_one()) {
+              if (n > 0) {
+                const uint64_t a = p_desc + ring.i * (kStageBytes >> 4);
+                const uint64_t q = a + q_off;
+                const uint32_t d = tmem + buf.i * C::kTileCols + h * kAccCols;
+#pragma unroll
+                for (int k = 0; k < kKBlock / 32; ++k) tc::mma_e4m3<CTAS>(d, a + 2 * k, q + 2 * k, idesc, k > 0);
+              }
+              tc::commit<CTAS>(&s.acc_full[h][buf.i]);
+              tc::commit<CTAS>(&s.empty[ring.i]);
+            }
+            __syncwarp();
+            ring.next();
+            buf.next();
+            ++used;
           }
-          __syncwarp();
-          ring.next();
-          buf.next();
-          ++used;
         }
+        for (uint32_t i = 0; i < NBUF; ++i, ++used, buf.next())   // the epilogues' last (remote) arrivals
+          if (used >= NBUF) ok &= wait_warp(&s.acc_empty[h][buf.i], buf.phase ^ 1, p.wait_ns);
       }
-      for (uint32_t i = 0; i < NBUF; ++i, ++used, buf.next())   // the epilogues' last (remote) arrivals
-        if (used >= NBUF) {
-          ok &= wait_warp(&s.acc_empty[0][buf.i], buf.phase ^ 1, p.wait_ns);
-          ok &= wait_warp(&s.acc_empty[1][buf.i], buf.phase ^ 1, p.wait_ns);
-        }
-    } else if (warp >= 2) {
+    } else {
       // ---- scales --------------------------------------------------------
-      // Warp 2 + h brings those of accumulator h, through registers and kAhead
-      // k-blocks ahead: one for each receive row (kMany: accumulator row, else
-      // column), times the weights' one; kWgrad: one for each column and row.
-      constexpr int kAhead = 3, kRows = 128 / 32;
-      const int half = warp - 2;
+      // Through registers and kAhead k-blocks ahead: one for each receive row (kMany:
+      // accumulator row, else column), times the weights' one; kWgrad: one for each
+      // column and row.
+      constexpr int kAhead = 2, kRows = 128 / 32;
+      constexpr int kSets = KIND == kWgrad ? 2 : 1;            // of row scales: kMany's are the same for both accumulators
+      constexpr int kWeights = KIND == kWgrad ? kRows : ACCS;
       Ring<NBUF> ring;
       for (int t = first_tile; t < tiles && ok; t += step) {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
+        const int kblocks = uniform(tile.kblocks);
         const int64_t kb0 = tile.k0 / kKBlock;
-        const int skip = KIND != kMany && half == 1 ? tile.n[0] : 0;
-        const int valid = (KIND == kMany ? tile.p_valid : tile.q_valid) - skip - lane;
-        const float* rs = p.row_sf + kb0 * p.row_sf_pitch + (KIND == kMany ? tile.p0 : tile.q0) + skip + lane;
-        const int block = KIND == kMany ? tile.q0 / 128 + half : tile.p0 / 128;
-        const bool block_in = KIND == kMany || tile.p_valid > 0;
-        const float* ws = KIND == kWgrad
-                              ? p.col_sf + kb0 * p.out_cols + tile.p0 + lane
-                              : p.col_sf + (static_cast<int64_t>(tile.expert) * ceil_div(p.out_cols, 128) + block) * p.kblocks;
-        float r[kAhead][kRows], w[kAhead][KIND == kWgrad ? kRows : 1];
-        const auto fetch = [&](int kb, float* rv, float* wv) {
-          const bool in = kb < tile.kblocks;
+        const int valid = (KIND == kMany ? tile.p_valid : tile.q_valid) - lane;
+        const float* rs = p.row_sf + kb0 * p.row_sf_pitch + (KIND == kMany ? tile.p0 : tile.q0) + lane;
+        const int block = KIND == kMany ? tile.q0 / 128 : tile.p0 / 128;
+        const int blocks = ceil_div(p.out_cols, 128);
+        const float* ws = KIND == kWgrad ? p.col_sf + kb0 * p.out_cols + tile.p0 + lane
+                                         : p.col_sf + (static_cast<int64_t>(tile.expert) * blocks + block) * p.kblocks;
+        float r[kAhead][kSets][kRows], w[kAhead][kWeights];
+        const auto fetch = [&](int kb, float (*rv)[kRows], float* wv) {
+          const bool in = kb < kblocks;
 #pragma unroll
-          for (int i = 0; i < kRows; ++i) rv[i] = in && i * 32 < valid ? __ldg(rs + kb * p.row_sf_pitch + i * 32) : 0.0f;
+          for (int h = 0; h < kSets; ++h)
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+              const int j = (h == 0 ? 0 : tile.n[0]) + i * 32;
+              rv[h][i] = in && j < valid ? __ldg(rs + kb * p.row_sf_pitch + j) : 0.0f;
+            }
           if (KIND == kWgrad) {
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
               wv[i] = in && lane + i * 32 < tile.p_valid ? __ldg(ws + static_cast<int64_t>(kb) * p.out_cols + i * 32) : 0.0f;
           } else {
-            wv[0] = in && block_in ? __ldg(ws + kb) : 0.0f;
+            wv[0] = in && block < blocks ? __ldg(ws + kb) : 0.0f;
+            if (KIND == kMany) wv[ACCS - 1] = in && block + 1 < blocks ? __ldg(ws + p.kblocks + kb) : 0.0f;
           }
         };
 #pragma unroll
         for (int d = 0; d < kAhead; ++d) fetch(d, r[d], w[d]);
-        for (int kb = 0; kb < tile.kblocks && ok; kb += kAhead) {
+        for (int kb = 0; kb < kblocks && ok; kb += kAhead) {
 #pragma unroll
           for (int d = 0; d < kAhead; ++d) {
-            if (kb + d >= tile.kblocks) break;
-            if (!(ok = wait_warp(&s.scale_empty[half][ring.i], ring.phase ^ 1, p.wait_ns))) break;
-            float* to = s.scale[half][ring.i];
+            if (kb + d >= kblocks) break;
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-              const int j = lane + i * 32;
-              if (KIND == kMany) to[j] = r[d][i] * w[d][0];
-              if (KIND == kFew) to[scale_place(j)] = r[d][i] * w[d][0];
-              if (KIND == kWgrad) to[scale_place(j)] = r[d][i];
-              if (KIND == kWgrad) to[128 + j] = w[d][i];
+            for (int h = 0; h < ACCS; ++h) {
+              if (!(ok = wait_warp(&s.scale_empty[h][ring.i], ring.phase ^ 1, p.wait_ns))) break;
+              float* to = s.scale[h][ring.i];
+#pragma unroll
+              for (int i = 0; i < kRows; ++i) {
+                const int j = lane + i * 32;
+                const float v = r[d][kSets == 2 ? h : 0][i];
+                if (KIND == kMany) to[j] = v * w[d][h];
+                if (KIND == kFew) to[scale_place(j)] = v * w[d][h];
+                if (KIND == kWgrad) to[scale_place(j)] = v;
+                if (KIND == kWgrad) to[128 + j] = w[d][i];
+              }
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(&s.acc_full[h][ring.i]);
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s.acc_full[half][ring.i]);
+            if (!ok) break;
             ring.next();
             fetch(kb + d + kAhead, r[d], w[d]);
           }
@@ -524,8 +541,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of one accumulator.
     tc::reg_inc<C::kEpilogueRegs>();
     constexpr int kBatches = C::kWarpCols / kBatchCols;
-    const int ew = warp - 4, quarter = warp % 4, half = ew / (4 * C::kSplit), part = ew / 4 % C::kSplit;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * C::kAccCols + part * C::kWarpCols;
+    const int ew = warp - 4, quarter = warp % 4, half = ew / (4 * C::kSplit), part = ew / 4 % C::kSplit;   // half: the accumulator
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kAccCols + part * C::kWarpCols;
     uint32_t freed = ptx::smem_addr(&s.acc_empty[half][0]);   // the leader's barriers
     if (CTAS == 2) freed = tc::map_to_rank(freed, 0);
     Ring<NBUF> buf;
@@ -533,7 +550,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       int n, kblocks;                                         // all that lives over the k-blocks
       {
         const Tile tile = get_tile<KIND>(p, s, t, rank);
-        n = half == 0 ? tile.n[0] : tile.n[1];
+        n = (half == 0 ? tile.n[0] : tile.n[1]) - part * C::kWarpCols;
         kblocks = tile.kblocks;
       }
       uint64_t acc[kBatches][16];                             // pairs of sums: see store_rows, store_columns
@@ -550,6 +567,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         if (KIND == kMany) {
           const float v = sc[quarter * 32 + lane];
           ps[0] = tc::pack2(v, v);
+          __syncwarp();
+          if (tc::elect_one()) ptx::mbar_arrive(&s.scale_empty[half][buf.i]);
         }
         if (KIND == kWgrad) {
           const float* rows = sc + 128 + quarter * 32 + lane / 4;
@@ -559,18 +578,21 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         if constexpr (KIND == kMany) {
           // columns past n are read and added for nothing: only the last tile across has any
 #pragma unroll
-          for (int c = 0; c < C::kWarpCols / 16; ++c) {
-            float v[16];
-            tc::ld_32x16(from + c * 16, v);
+          for (int c = 0; c < kBatches; ++c) {
+            float v[2][16];
+            tc::ld_32x16(from + c * kBatchCols, v[0]);
+            tc::ld_32x16(from + c * kBatchCols + 16, v[1]);
             tc::wait_ld();
-            if (c == C::kWarpCols / 16 - 1) {   // all is in registers: the tensor core may have the buffer back
+            if (c == kBatches - 1) {   // all is in registers: the tensor core may have the buffer back
               tc::fence_before();
               __syncwarp();
-              if (lane == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+              if (tc::elect_one()) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              acc[c * 16 / 32][c * 8 % 16 + i] = tc::fma2(tc::pack2(v[2 * i], v[2 * i + 1]), ps[0], acc[c * 16 / 32][c * 8 % 16 + i]);
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                acc[c][8 * d + i] = tc::fma2(tc::pack2(v[d][2 * i], v[d][2 * i + 1]), ps[0], acc[c][8 * d + i]);
           }
         } else {
 #pragma unroll
@@ -583,8 +605,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             {
               tc::ld_16x32(from + (c + d) * kBatchCols, v[d]);
               tc::ld_16x32(from + (c + d) * kBatchCols + (16u << 16), v[d] + 16);
-              f[d][0] = *reinterpret_cast<const float4*>(sc + (c + d) * kBatchCols + (lane % 4) * 4);
-              f[d][1] = *reinterpret_cast<const float4*>(sc + (c + d) * kBatchCols + 16 + (lane % 4) * 4);
+              f[d][0] = *reinterpret_cast<const float4*>(sc + part * C::kWarpCols + (c + d) * kBatchCols + (lane % 4) * 4);
+              f[d][1] = *reinterpret_cast<const float4*>(sc + part * C::kWarpCols + (c + d) * kBatchCols + 16 + (lane % 4) * 4);
             }
           }
           tc::wait_ld();
@@ -606,8 +628,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
         }
         __syncwarp();
-        if (lane == 0) {
-          if (KIND != kMany && n == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+        if (KIND != kMany && tc::elect_one()) {
+          if (n <= 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
           ptx::mbar_arrive(&s.scale_empty[half][buf.i]);
         }
         buf.next();
@@ -615,8 +637,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       if (!ok) break;
 
       const Tile tile = get_tile<KIND>(p, s, t, rank);
-      if constexpr (KIND == kMany) store_rows(p, tile, quarter * 32 + lane, half * C::kAccCols + part * C::kWarpCols, acc);
-      else store_columns<KIND>(p, tile, quarter, half, lane, s.out[ew], acc);
+      if constexpr (KIND == kMany) store_rows(p, tile, quarter * 32 + lane, half * kAccCols + part * C::kWarpCols, acc);
+      else store_columns<KIND>(p, tile, quarter, half, part, lane, mem.out + ew * kOutBytes, acc);
       if (KIND != kWgrad && tile.last) zero_gap<KIND>(p, s, tile, rank, ew, lane);
     }
   }
@@ -669,12 +691,12 @@ cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const CUt
                    cudaStream_t stream) {
   constexpr int CTAS = Config<KIND>::kCtas;
   const auto kernel = expert_gemm_kernel<KIND>;
-  cudaError_t e = ensure_smem_limit(kernel, kSmemBytes);
+  cudaError_t e = ensure_smem_limit(kernel, kSmemBytes<KIND>);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() / CTAS * CTAS));
   cfg.blockDim = dim3(Config<KIND>::kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = kSmemBytes<KIND>;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
