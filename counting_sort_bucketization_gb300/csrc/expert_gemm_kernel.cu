@@ -67,7 +67,7 @@ constexpr int kSlotWords = 128 + kPRows;           // scales of columns or rows,
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 128;                      // columns of an accumulator
 constexpr int kOutPitch = 96;                      // bytes; 64 of data, 4 rows' 32-byte pieces in different banks
-constexpr int kOutBytes = 32 * kOutPitch;          // a warp's 32 rows x 32 columns of bf16
+constexpr int kOutBytes = 16 * kOutPitch;          // a warp's 16 rows x 32 columns of bf16
 
 template <Kind KIND>
 struct Config {
@@ -77,14 +77,14 @@ struct Config {
   static constexpr int kBuffers = kTmemCols / kTileCols;       // of an accumulator
   static constexpr int kUnit = 16 * kCtas;                     // column granularity: each CTA of a pair holds n / 2 rows of Q
   static constexpr int kQRows = kAccCols / kCtas;              // rows of Q of an accumulator a CTA loads at most
-  static constexpr int kSplit = KIND == kWgrad ? 1 : 2;        // epilogue warps side by side in an accumulator
+  static constexpr int kSplit = 2;                             // epilogue warps side by side in an accumulator
   static constexpr int kWarpCols = kAccCols / kSplit;
   static constexpr int kEpilogueWarps = 4 * kAccs * kSplit;
   static constexpr int kThreads = 128 + 32 * kEpilogueWarps;
   static constexpr int kStages = KIND == kMany ? 6 : 5;        // what the staging of out leaves room for
   // Registers a thread: sums, and values of tensor memory.
-  static constexpr int kLaunchRegs = KIND == kMany ? 96 : 168;
-  static constexpr int kEpilogueRegs = KIND == kMany ? 104 : 224, kOtherRegs = KIND == kMany ? 64 : 56;
+  static constexpr int kLaunchRegs = KIND == kFew ? 168 : 96;
+  static constexpr int kEpilogueRegs = KIND == kFew ? 224 : 104, kOtherRegs = KIND == kFew ? 56 : 64;
   static_assert(32 * kEpilogueWarps * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
                 "register split above the launch's total");
   static_assert(kAccs * kQRows * kKBlock <= kQBytes, "shared memory of Q");
@@ -183,6 +183,12 @@ __device__ __forceinline__ int scale_place(int j) {
   return (j & ~31) + ((j & 16) >> 4) * 16 + (j & 3) * 4 + ((j & 15) >> 2);
 }
 
+// The eight scales of a lane's columns among 32; `at` is the lane's place in them.
+__device__ __forceinline__ void load_scales(const float* at, float* q) {
+  const float4 lo = *reinterpret_cast<const float4*>(at), hi = *reinterpret_cast<const float4*>(at + 16);
+  q[0] = lo.x, q[1] = lo.y, q[2] = lo.z, q[3] = lo.w, q[4] = hi.x, q[5] = hi.y, q[6] = hi.z, q[7] = hi.w;
+}
+
 // Position in a ring of N buffers, and the parity of the phase it is in.
 template <int N>
 struct Ring {
@@ -272,23 +278,26 @@ __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t
     // Lanes j and j ^ 4 hold rows k and k + 1 (k = j/4 even) and the rows 8 further
     // on; they trade so that each has two neighbours: one 32-bit word of out.
     const bool odd = (lane & 4) != 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {                          // up = i / 8, column 4 * (i % 8) + lane % 4
-      const float2 f = tc::unpack2(acc[c][i]);
-      const float other = __shfl_xor_sync(0xffffffffu, odd ? f.x : f.y, 4);
-      *reinterpret_cast<uint32_t*>(stage + (4 * (i % 8) + lane % 4) * kOutPitch + 32 * (i / 8) + (odd ? 16 : 0) +
-                                   lane / 8 * 4) = odd ? pack_bf16(other, f.y) : pack_bf16(f.x, other);
-    }
-    __syncwarp();
     const int oc = col0 + (lane % 4) * 8;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int r = 8 * h + lane / 4;
-      const uint4 w = ptx::ld_shared_v4(stage + r * kOutPitch + (lane % 4) * 16);
-      if (row + r < t.q_valid && oc < p.out_cols)
-        ptx::st_v4(static_cast<uint16_t*>(p.out) + (row0 + row + r) * p.out_cols + oc, w);
+    for (int half = 0; half < 2; ++half) {                  // 16 columns: rows of out
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {                         // up = i / 4, column 16 * half + 4 * (i % 4) + lane % 4
+        const float2 f = tc::unpack2(acc[c][8 * (i / 4) + 4 * half + i % 4]);
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? f.x : f.y, 4);
+        *reinterpret_cast<uint32_t*>(stage + (4 * (i % 4) + lane % 4) * kOutPitch + 32 * (i / 4) + (odd ? 16 : 0) +
+                                     lane / 8 * 4) = odd ? pack_bf16(other, f.y) : pack_bf16(f.x, other);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 8 * h + lane / 4, at = row + 16 * half + r;
+        const uint4 w = ptx::ld_shared_v4(stage + r * kOutPitch + (lane % 4) * 16);
+        if (at < t.q_valid && oc < p.out_cols)
+          ptx::st_v4(static_cast<uint16_t*>(p.out) + (row0 + at) * p.out_cols + oc, w);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
@@ -595,37 +604,50 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 acc[c][8 * d + i] = tc::fma2(tc::pack2(v[d][2 * i], v[d][2 * i + 1]), ps[0], acc[c][8 * d + i]);
           }
         } else {
+          sc += part * C::kWarpCols + (lane % 4) * 4;
+          if constexpr (KIND == kFew) {
+            if (n > 0) {
+              float v[kBatches][32];
 #pragma unroll
-        for (int c = 0; c < kBatches; c += 2) {
-          if (c * kBatchCols >= n) break;
-          float v[2][32];
-          float4 f[2][2];
+              for (int c = 0; c < kBatches; ++c) {
+                tc::ld_16x32(from + c * kBatchCols, v[c]);
+                tc::ld_16x32(from + c * kBatchCols + (16u << 16), v[c] + 16);
+              }
+              float q[kBatches][8];
 #pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            {
-              tc::ld_16x32(from + (c + d) * kBatchCols, v[d]);
-              tc::ld_16x32(from + (c + d) * kBatchCols + (16u << 16), v[d] + 16);
-              f[d][0] = *reinterpret_cast<const float4*>(sc + part * C::kWarpCols + (c + d) * kBatchCols + (lane % 4) * 4);
-              f[d][1] = *reinterpret_cast<const float4*>(sc + part * C::kWarpCols + (c + d) * kBatchCols + 16 + (lane % 4) * 4);
+              for (int c = 0; c < kBatches; ++c) load_scales(sc + c * kBatchCols, q[c]);
+              tc::wait_ld();
+              tc::fence_before();
+              __syncwarp();
+              if (tc::elect_one()) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+#pragma unroll
+              for (int c = 0; c < kBatches; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  acc[c][i] = tc::fma2(tc::pack2(v[c][2 * i], v[c][2 * i + 1]), tc::pack2(q[c][i % 8], q[c][i % 8]), acc[c][i]);
+            }
+          } else if (n > 0) {
+#pragma unroll
+            for (int c = 0; c < kBatches; ++c) {
+              float q[8];
+              load_scales(sc + c * kBatchCols, q);
+#pragma unroll
+              for (int up = 0; up < 2; ++up) {
+                float v[16];
+                tc::ld_16x32(from + c * kBatchCols + (static_cast<uint32_t>(16 * up) << 16), v);
+                tc::wait_ld();
+                if (c == kBatches - 1 && up == 1) {
+                  tc::fence_before();
+                  __syncwarp();
+                  if (tc::elect_one()) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  acc[c][8 * up + i] = tc::fma2(tc::mul2(tc::pack2(v[2 * i], v[2 * i + 1]), ps[up]), tc::pack2(q[i], q[i]),
+                                                acc[c][8 * up + i]);
+              }
             }
           }
-          tc::wait_ld();
-          if ((c + 2) * kBatchCols >= n || c + 2 >= kBatches) {   // all is in registers: the tensor core may have the buffer back
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster_relaxed(freed + buf.i * 8);
-          }
-#pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            const float q[8] = {f[d][0].x, f[d][0].y, f[d][0].z, f[d][0].w, f[d][1].x, f[d][1].y, f[d][1].z, f[d][1].w};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              uint64_t v2 = tc::pack2(v[d][2 * i], v[d][2 * i + 1]);
-              if (KIND == kWgrad) v2 = tc::mul2(v2, ps[i / 8]);
-              acc[c + d][i] = tc::fma2(v2, tc::pack2(q[i % 8], q[i % 8]), acc[c + d][i]);
-            }
-          }
-        }
         }
         __syncwarp();
         if (KIND != kMany && tc::elect_one()) {
