@@ -35,8 +35,8 @@
 //  - The epilogue is bound by its chain of latencies (wait, load, add), so kMany has 16
 //    warps of 64 columns, 412 -> 386 us; 32 columns of tensor memory in flight,
 //    386 -> 375 us.
-//  - tcgen05.ld of 32x32 and 16x128-bit shapes moves a register of an SM quarter in
-//    1.2 cycles, the 16x256-bit one in 2.0.
+//  - tcgen05.ld of the 32x32-bit shape moves a register of an SM quarter in 1.2 cycles,
+//    the 16x256-bit one in 2.0; kFew and kWgrad take the latter for its pairs of columns.
 //
 // One persistent CTA (or pair) per SM walks the tiles of all experts.  All sums
 // are fp32; the result is rounded once.
@@ -66,7 +66,7 @@ constexpr int kBatchCols = 32;                     // columns of one tensor-memo
 constexpr int kSlotWords = 128 + kPRows;           // scales of columns or rows, then (kWgrad) of rows
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 128;                      // columns of an accumulator
-constexpr int kOutPitch = 96;                      // bytes; 64 of data, 4 rows' 32-byte pieces in different banks
+constexpr int kOutPitch = 80;                      // bytes; 64 of data, conflict-free for stmatrix
 constexpr int kOutBytes = 16 * kOutPitch;          // a warp's 16 rows x 32 columns of bf16
 
 template <Kind KIND>
@@ -177,16 +177,14 @@ __device__ __forceinline__ Tile get_tile(const GemmParams& p, const Shared& s, i
   return r;
 }
 
-// Place of a column's scale: a lane reads the eight it needs of 32 columns (j % 4
-// is the same) as two vectors.
+// Place of a column's scale: a lane reads those of its four pairs among 32
+// columns as two vectors.
 __device__ __forceinline__ int scale_place(int j) {
-  return (j & ~31) + ((j & 16) >> 4) * 16 + (j & 3) * 4 + ((j & 15) >> 2);
+  return (j & ~15) + ((j & 7) >> 1) * 4 + ((j & 8) >> 3) * 2 + (j & 1);
 }
-
-// The eight scales of a lane's columns among 32; `at` is the lane's place in them.
-__device__ __forceinline__ void load_scales(const float* at, float* q) {
+__device__ __forceinline__ void load_scales(const float* at, uint64_t* q) {
   const float4 lo = *reinterpret_cast<const float4*>(at), hi = *reinterpret_cast<const float4*>(at + 16);
-  q[0] = lo.x, q[1] = lo.y, q[2] = lo.z, q[3] = lo.w, q[4] = hi.x, q[5] = hi.y, q[6] = hi.z, q[7] = hi.w;
+  q[0] = tc::pack2(lo.x, lo.y), q[1] = tc::pack2(lo.z, lo.w), q[2] = tc::pack2(hi.x, hi.y), q[3] = tc::pack2(hi.z, hi.w);
 }
 
 // Position in a ring of N buffers, and the parity of the phase it is in.
@@ -246,8 +244,8 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const Tile& t, i
 }
 
 // Rows of out from sums whose columns are rows of out (kFew, kWgrad).
-// acc[c][8 * up + i]: rows 16 * up + lane / 4 and 8 further on of the warp's 32,
-// column 32 * c + 4 * i + lane % 4 of the accumulator.
+// acc[c][8 * up + 2 * h + r]: row 16 * up + 8 * r + lane / 4 of the warp's 32,
+// columns 32 * c + 8 * h + 2 * (lane % 4), +1 of its accumulator columns.
 template <Kind KIND>
 __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t, int quarter, int acc_id, int part, int lane,
                                               uint8_t* stage, const uint64_t (*acc)[16]) {
@@ -264,29 +262,30 @@ __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t
       // 4 rows x 8 columns a store: whole 32-byte sectors
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int up = i / 8, at = row + 4 * (i % 8) + lane % 4;
+        const int oc = col0 + 16 * (i / 8) + 8 * (i % 2) + lane / 4, at = row + 8 * (i / 2 % 4) + 2 * (lane % 4);
         const float2 f = tc::unpack2(acc[c][i]);
-        const int oc = col0 + 16 * up + lane / 4;
-        if (at < t.q_valid) {
+        if (oc < p.out_cols) {
           float* o = static_cast<float*>(p.out) + (row0 + at) * p.out_cols + oc;
-          if (oc < p.out_cols) o[0] = p.accumulate ? o[0] + f.x : f.x;
-          if (oc + 8 < p.out_cols) o[8] = p.accumulate ? o[8] + f.y : f.y;
+          if (at < t.q_valid) o[0] = p.accumulate ? o[0] + f.x : f.x;
+          if (at + 1 < t.q_valid) o[p.out_cols] = p.accumulate ? o[p.out_cols] + f.y : f.y;
         }
       }
       continue;
     }
-    // Lanes j and j ^ 4 hold rows k and k + 1 (k = j/4 even) and the rows 8 further
-    // on; they trade so that each has two neighbours: one 32-bit word of out.
-    const bool odd = (lane & 4) != 0;
     const int oc = col0 + (lane % 4) * 8;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {                  // 16 columns: rows of out
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {                         // up = i / 4, column 16 * half + 4 * (i % 4) + lane % 4
-        const float2 f = tc::unpack2(acc[c][8 * (i / 4) + 4 * half + i % 4]);
-        const float other = __shfl_xor_sync(0xffffffffu, odd ? f.x : f.y, 4);
-        *reinterpret_cast<uint32_t*>(stage + (4 * (i % 4) + lane % 4) * kOutPitch + 32 * (i / 4) + (odd ? 16 : 0) +
-                                     lane / 8 * 4) = odd ? pack_bf16(other, f.y) : pack_bf16(f.x, other);
+      for (int h = 2 * half; h < 2 * half + 2; ++h) {
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = tc::unpack2(acc[c][8 * (i / 2) + 2 * h + i % 2]);
+          v[i] = pack_bf16(f.x, f.y);
+        }
+        // four matrices of 8 columns of out, transposed to 8 rows of 64 bytes
+        tc::stmatrix_x4_trans(ptx::smem_addr(stage) + (8 * (h % 2) + lane % 8) * kOutPitch + (lane / 8) * 16, v[0], v[1], v[2],
+                              v[3]);
       }
       __syncwarp();
 #pragma unroll
@@ -572,7 +571,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         tc::fence_after();
         const float* sc = s.scale[half][buf.i];
         const uint32_t from = lane_base + buf.i * C::kTileCols;
-        uint64_t ps[2];
+        uint64_t ps[4];
         if (KIND == kMany) {
           const float v = sc[quarter * 32 + lane];
           ps[0] = tc::pack2(v, v);
@@ -581,8 +580,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
         if (KIND == kWgrad) {
           const float* rows = sc + 128 + quarter * 32 + lane / 4;
-          ps[0] = tc::pack2(rows[0], rows[8]);
-          ps[1] = tc::pack2(rows[16], rows[24]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ps[i] = tc::pack2(rows[8 * i], rows[8 * i]);
         }
         if constexpr (KIND == kMany) {
           // columns past n are read and added for nothing: only the last tile across has any
@@ -613,7 +612,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 tc::ld_16x32(from + c * kBatchCols, v[c]);
                 tc::ld_16x32(from + c * kBatchCols + (16u << 16), v[c] + 16);
               }
-              float q[kBatches][8];
+              uint64_t q[kBatches][4];
 #pragma unroll
               for (int c = 0; c < kBatches; ++c) load_scales(sc + c * kBatchCols, q[c]);
               tc::wait_ld();
@@ -624,12 +623,13 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
               for (int c = 0; c < kBatches; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                  acc[c][i] = tc::fma2(tc::pack2(v[c][2 * i], v[c][2 * i + 1]), tc::pack2(q[c][i % 8], q[c][i % 8]), acc[c][i]);
+                  acc[c][i] = tc::fma2(tc::pack2(v[c][16 * (i / 8) + 4 * (i / 2 % 4) + 2 * (i % 2)],
+                                                    v[c][16 * (i / 8) + 4 * (i / 2 % 4) + 2 * (i % 2) + 1]), q[c][i / 2 % 4], acc[c][i]);
             }
           } else if (n > 0) {
 #pragma unroll
             for (int c = 0; c < kBatches; ++c) {
-              float q[8];
+              uint64_t q[4];
               load_scales(sc + c * kBatchCols, q);
 #pragma unroll
               for (int up = 0; up < 2; ++up) {
@@ -643,7 +643,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  acc[c][8 * up + i] = tc::fma2(tc::mul2(tc::pack2(v[2 * i], v[2 * i + 1]), ps[up]), tc::pack2(q[i], q[i]),
+                  acc[c][8 * up + i] = tc::fma2(tc::mul2(tc::pack2(v[2 * i], v[2 * i + 1]), ps[2 * up + i % 2]), q[i / 2],
                                                 acc[c][8 * up + i]);
               }
             }

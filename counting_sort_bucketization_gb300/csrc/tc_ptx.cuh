@@ -120,20 +120,21 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// 16 lanes x 32 fp32 columns.  Lane j of the warp gets, for i = 0..7: v[2i] =
-// row j/4, column 4i + j%4, and v[2i+1] the same column of row j/4 + 8.  (The
-// 256-bit shape, whose pairs are neighbouring columns, measures half the rate:
-// 2.0 against 1.2 cycles a register of an SM quarter.)
+// 16 lanes x 32 fp32 columns.  Lane j of the warp gets, for each group h of 8
+// columns: v[4h], v[4h+1] = row j/4, columns 8h + 2(j%4), +1; v[4h+2], v[4h+3]
+// the same columns of row j/4 + 8.  (2.0 cycles a register of an SM quarter
+// against 1.2 of the other shapes, but its pairs take a pair of column scales and
+// suit stmatrix.)
 __device__ __forceinline__ void ld_16x32(uint32_t addr, float* v) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
       "[%16];"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(addr));
 }
 
-// 32 lanes x 16 (32) fp32 columns: lane j gets its row.
+// 32 lanes x 16 fp32 columns: lane j gets its row.
 __device__ __forceinline__ void ld_32x16(uint32_t addr, float* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -141,21 +142,6 @@ __device__ __forceinline__ void ld_32x16(uint32_t addr, float* v) {
       : "r"(addr));
 }
 
-
-__device__ __forceinline__ void ld_32x32(uint32_t addr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
-      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31 "
-      "}, [%32];"
-      :
-        "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
-        "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]),
-        "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]),
-        "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(addr));
-}
 
 // ------------------------------------------------------------- MMA
 // Shared-memory operand, K-major, rows of 128 bytes in 128-byte swizzle atoms of
@@ -218,6 +204,14 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
+}
+
+// Four 8x8 matrices of 16-bit values, transposed, to the rows at the addresses
+// that lanes 8i..8i+7 give for matrix i.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
 }
 
 // 32-byte store; p 32-byte aligned.
