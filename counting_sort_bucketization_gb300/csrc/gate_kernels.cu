@@ -4,9 +4,12 @@
 // One warp owns a token; lane j holds the columns j, j+32, ... in registers,
 // so a row is read once and every reduction over experts is a warp reduction.
 //
-//   key_e = l_e + bias_e (one fp32 addition); the K largest keys are taken one
-//   after the other as integers that sort like the floats: redux.max gives the
-//   key and redux.min the lowest id that has it.  A key of -inf is not taken.
+//   key_e = l_e + bias_e (one fp32 addition), as integers that sort like the
+//   floats.  The K-th largest of the lanes' own maxima bounds the K-th largest key
+//   from below; the few keys that reach it are listed in shared memory and each
+//   counts those before it (larger, or equal with a lower id): its slot.  If more
+//   than 32 reach it, the keys are taken one after the other by redux.max /
+//   redux.min.  A key of -inf is not taken.
 //   s = softmax(l) or sigmoid(l), q = s / sum(s); w_k = scale * s_k / D.
 //   Balance loss: coef * E * sum_e f_e P_e with P_e the mean of q over the
 //   routed tokens and f_e = count_e / (K * routed tokens).
@@ -67,7 +70,9 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float sigmoid_acc(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
+// ex2 of a rounded product: the argument's rounding adds 2^-24 |x| to the result's
+// relative error, which leaves scores good to 2^-18 down to e^-32 of the largest.
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 // One row's logits in registers: columns lane, lane + 32, ...; -inf past E.
 template <int VPL, typename T>
@@ -86,8 +91,8 @@ __device__ __forceinline__ float scores(float* l, float m) {
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    // expf(-inf) = 0, and sigmoid(-inf) = 1 / (1 + inf) = 0: closed experts score nothing
-    l[i] = SIGMOID ? sigmoid_acc(l[i]) : expf(l[i] - m);
+    // exp(-inf) = 0, and sigmoid(-inf) = 1 / (1 + inf) = 0: closed experts score nothing
+    l[i] = SIGMOID ? sigmoid_fast(l[i]) : __expf(l[i] - m);
     s += l[i];
   }
   return fmaxf(warp_sum(s), kTiny);
@@ -108,8 +113,10 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
   float* sum_s = reinterpret_cast<float*>(smem);       // [E]
   int* cnt_s = reinterpret_cast<int*>(smem) + E;       // [E + 1]: picks of each expert, routed tokens
   __shared__ bool last_s;
+  __shared__ uint64_t list_s[kGateWarps][32];
   __shared__ float red_s[kGateWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  uint64_t* list = list_s[warp];
   for (int e = threadIdx.x; e < E; e += kGateThreads) sum_s[e] = 0.0f;
   for (int e = threadIdx.x; e <= E; e += kGateThreads) cnt_s[e] = 0;
   __syncthreads();
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
     for (int i = 0; i < VPL; ++i) l[i] = next[i];
     load_row<VPL, T>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
 
-    unsigned u[VPL];
+    unsigned u[VPL], best = 0;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -143,17 +150,13 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
       const bool in = lane + 32 * i < E;
       bad |= in && !(key < INFINITY);
       u[i] = in ? sortable(key) : 0u;
+      best = max(best, u[i]);
     }
     bad = __any_sync(kFull, bad);
     if (bad && lane == 0) set_error(a.err, MOE_ERR_INVALID_ARG);
-    unsigned best = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (u[i] > best) best = u[i], at = i;
     unsigned top = __reduce_max_sync(kFull, best);
     const bool route = !bad && top > kKeyNegInf;
-    int mine = -1;
+    int mine = -1, slot = lane;            // this lane's pick and its place among the K
     float w = 0.0f;
     if (route) {
       // without a bias the largest key is the largest logit
@@ -164,32 +167,65 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
       for (int i = 0; i < VPL; ++i) acc[i] += l[i] * inv;
       ++routed;
 
-      for (int k = 0; k < K && top > kKeyNegInf; ++k) {
-        const unsigned id = __reduce_min_sync(kFull, best == top ? static_cast<unsigned>(lane + 32 * at) : kFull);
-        if (lane == k) mine = static_cast<int>(id);
-        if (static_cast<int>(id % 32) == lane) {
-          const int gone = static_cast<int>(id / 32);
+      // The K-th largest lane maximum (equal ones go together: a lower bound still).
+      unsigned floor = top;
+      {
+        unsigned rest = best;
+        for (int k = 1; k < K && floor > kKeyNegInf; ++k) {
+          if (rest == floor) rest = 0;
+          floor = __reduce_max_sync(kFull, rest);
+        }
+        floor = max(floor, kKeyNegInf + 1);
+      }
+      int found = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const unsigned who = __ballot_sync(kFull, u[i] >= floor);
+        if (u[i] >= floor) {
+          const int at = found + __popc(who & ptx::lanemask_lt());
+          if (at < 32) list[at] = static_cast<uint64_t>(u[i]) << 32 | ~static_cast<unsigned>(lane + 32 * i);
+        }
+        found += __popc(who);
+      }
+      __syncwarp();
+      if (found <= 32) {
+        const uint64_t own = lane < found ? list[lane] : 0;
+        int before = 0;
+        for (int j = 0; j < found; ++j) before += list[j] > own;
+        if (lane < found) {
+          if (before < K) mine = static_cast<int>(~static_cast<unsigned>(own));
+          slot = before;
+        }
+      } else {
+        for (int k = 0; k < K && top > kKeyNegInf; ++k) {
+          unsigned lowest = kFull;
+#pragma unroll
+          for (int i = VPL - 1; i >= 0; --i)
+            if (u[i] == top) lowest = static_cast<unsigned>(lane + 32 * i);
+          const unsigned id = __reduce_min_sync(kFull, lowest);
+          if (lane == k) mine = static_cast<int>(id);
           best = 0;
 #pragma unroll
           for (int i = 0; i < VPL; ++i) {
-            if (i == gone) u[i] = 0;
-            if (u[i] > best) best = u[i], at = i;
+            if (lane + 32 * i == static_cast<int>(id)) u[i] = 0;
+            best = max(best, u[i]);
           }
+          top = __reduce_max_sync(kFull, best);
         }
-        top = __reduce_max_sync(kFull, best);
       }
+      __syncwarp();   // the list is read
       float s = 0.0f;
       if (mine >= 0) {
         const float lk = load_logit(row + mine);
-        s = SIGMOID ? sigmoid_acc(lk) : expf(lk - m) * inv;
+        s = SIGMOID ? sigmoid_fast(lk) : __expf(lk - m) * inv;
         atomicAdd(&cnt_s[mine], 1);
       }
       const float den = a.normalize ? fmaxf(warp_sum(s), kTiny) : 1.0f;
       w = a.scale * s / den;
     }
-    if (lane < K) {
-      a.topk_idx[t * K + lane] = mine;
-      a.weights[t * K + lane] = w;
+    if (slot < K) {
+      a.topk_idx[t * K + slot] = mine;
+      a.weights[t * K + slot] = w;
     }
   }
 
@@ -205,29 +241,40 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
     }
     __syncthreads();
   }
-  float* part_sum = a.part_sum + static_cast<int64_t>(blockIdx.x) * E;
-  int* part_cnt = a.part_cnt + static_cast<int64_t>(blockIdx.x) * (E + 1);
-  for (int e = threadIdx.x; e < E; e += kGateThreads) part_sum[e] = sum_s[e];
-  for (int e = threadIdx.x; e <= E; e += kGateThreads) part_cnt[e] = cnt_s[e];
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last_s = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
-  __syncthreads();
-  if (!last_s) return;
-  __threadfence();
-
-  // The last CTA to finish: the other CTAs' partials in CTA order.
-  for (int e = threadIdx.x; e <= E; e += kGateThreads) {
-    float s = 0.0f;
-    int c = 0;
-    for (unsigned b = 0; b < gridDim.x; ++b) {
-      if (e < E) s += __ldcg(a.part_sum + static_cast<int64_t>(b) * E + e);
-      c += __ldcg(a.part_cnt + static_cast<int64_t>(b) * (E + 1) + e);
+  // Partials of CTAs, then of groups of CTAs: whoever finishes last in a group (and the
+  // last group) adds them in their order.
+  const int groups = (static_cast<int>(gridDim.x) + kGateGroup - 1) / kGateGroup;
+  const int group = static_cast<int>(blockIdx.x) / kGateGroup;
+  for (int level = 0; level < 2; ++level) {
+    const int first = level == 0 ? group * kGateGroup : kGateMaxCtas;   // rows of partials; the groups' follow the CTAs'
+    const int rows = level == 0 ? min(kGateGroup, static_cast<int>(gridDim.x) - first) : groups;
+    const int64_t own = level == 0 ? static_cast<int64_t>(blockIdx.x) : kGateMaxCtas + group;
+    if (rows == 1) continue;               // the partial in shared memory is the sum
+    for (int e = threadIdx.x; e < E; e += kGateThreads) a.part_sum[own * E + e] = sum_s[e];
+    for (int e = threadIdx.x; e <= E; e += kGateThreads) a.part_cnt[own * (E + 1) + e] = cnt_s[e];
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      unsigned* ticket = a.ticket + (level == 0 ? 1 + group : 0);
+      last_s = atomicAdd(ticket, 1u) == static_cast<unsigned>(rows) - 1;
+      if (last_s) *ticket = 0;
     }
-    if (e < E) sum_s[e] = s;
-    cnt_s[e] = c;
+    __syncthreads();
+    if (!last_s) return;
+    __threadfence();
+    for (int e = threadIdx.x; e <= E; e += kGateThreads) {
+      float sum = 0.0f;
+      int c = 0;
+#pragma unroll 8
+      for (int b = first; b < first + rows; ++b) {
+        if (e < E) sum += __ldcg(a.part_sum + static_cast<int64_t>(b) * E + e);
+        c += __ldcg(a.part_cnt + static_cast<int64_t>(b) * (E + 1) + e);
+      }
+      if (e < E) sum_s[e] = sum;
+      cnt_s[e] = c;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   const float inv_tokens = 1.0f / static_cast<float>(max(cnt_s[E], 1));
   float part = 0.0f;
   for (int e = threadIdx.x; e < E; e += kGateThreads) {
@@ -244,7 +291,6 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
     for (int w = 0; w < kGateWarps; ++w) s += red_s[w];
     *a.routed_tokens = cnt_s[E];
     *a.balance_loss = a.balance_coef * static_cast<float>(E) * s * inv_tokens / static_cast<float>(K);
-    *a.ticket = 0;
   }
 }
 
@@ -302,7 +348,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_backward_kernel(GateArgs a)
     float s = 0.0f, dw = 0.0f;
     if (mine >= 0) {
       const float lk = load_logit(row + mine);
-      s = SIGMOID ? sigmoid_acc(lk) : expf(lk - m) * inv;
+      s = SIGMOID ? sigmoid_fast(lk) : __expf(lk - m) * inv;
       if (a.dweights != nullptr) dw = a.dweights[t * K + lane];
     }
     float ds = a.scale * dw;

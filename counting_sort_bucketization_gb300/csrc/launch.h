@@ -110,9 +110,13 @@ T* at(void* ws, size_t off) {
 
 // ------------------------------------------------ gate (gate_kernels.cu)
 // CTAs of the forward kernel at most: each leaves one partial of the sums over
-// tokens in the gate's workspace, [error word | ticket | pad to 256 B]
-// [fp32 kGateMaxCtas x E][int32 kGateMaxCtas x (E + 1)].
+// tokens in the gate's workspace, and each group of kGateGroup CTAs one of its own:
+// [error word | tickets | pad to 256 B][fp32 kGatePartials x E]
+// [int32 kGatePartials x (E + 1)].
 constexpr int kGateMaxCtas = 304;
+constexpr int kGateGroup = 16;
+constexpr int kGatePartials = kGateMaxCtas + (kGateMaxCtas + kGateGroup - 1) / kGateGroup;
+static_assert(16 + 4 * (1 + (kGateMaxCtas + kGateGroup - 1) / kGateGroup) <= 256, "tickets");
 
 struct GateArgs {
   const void* logits;
@@ -134,7 +138,7 @@ struct GateArgs {
   float* balance_loss;
   float* part_sum;
   int32_t* part_cnt;
-  unsigned* ticket;              // zero between launches
+  unsigned* ticket;              // of all, then of each group; zero between launches
   int* err;
   const float* dweights;         // backward; may be null
   const float* dloss;            // backward; may be null

@@ -12,7 +12,7 @@ namespace moe {
 namespace {
 
 size_t gate_workspace(int E) {
-  const size_t words = static_cast<size_t>(kGateMaxCtas) * static_cast<size_t>(2 * E + 1);
+  const size_t words = static_cast<size_t>(kGatePartials) * static_cast<size_t>(2 * E + 1);
   return (256 + 4 * words + 255) / 256 * 256;
 }
 
@@ -40,7 +40,7 @@ int gate_args(const moe_layout_desc* desc, const moe_gate_desc* gate, const void
   a.err = at<int>(workspace, 0);
   a.ticket = at<unsigned>(workspace, 16);
   a.part_sum = at<float>(workspace, 256);
-  a.part_cnt = at<int32_t>(workspace, 256 + 4 * static_cast<size_t>(kGateMaxCtas) * desc->num_experts);
+  a.part_cnt = at<int32_t>(workspace, 256 + 4 * static_cast<size_t>(kGatePartials) * desc->num_experts);
   *out = a;
   return MOE_OK;
 }
