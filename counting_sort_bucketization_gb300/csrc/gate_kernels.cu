@@ -35,7 +35,7 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kGateThreads = 512;
+constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
 constexpr float kTiny = 1e-30f;              // floor of a sum of scores that divides
 constexpr unsigned kKeyNegInf = 0x007fffffu; // sortable key of -inf
@@ -107,28 +107,31 @@ __device__ __forceinline__ float row_max(const float* l) {
 }
 
 template <int VPL, typename T, bool SIGMOID>
-__global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) {
+__global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2) gate_forward_kernel(GateArgs a) {
   extern __shared__ uint8_t smem[];
   const int E = a.num_experts, K = a.topk;
   float* sum_s = reinterpret_cast<float*>(smem);       // [E]
   int* cnt_s = reinterpret_cast<int*>(smem) + E;       // [E + 1]: picks of each expert, routed tokens
   __shared__ bool last_s;
   __shared__ uint64_t list_s[kGateWarps][32];
+  __shared__ float list_l_s[kGateWarps][32];
   __shared__ float red_s[kGateWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   uint64_t* list = list_s[warp];
+  float* list_l = list_l_s[warp];
+  float* bias_s = reinterpret_cast<float*>(smem) + 2 * E + 1;   // [E], with a bias
   for (int e = threadIdx.x; e < E; e += kGateThreads) sum_s[e] = 0.0f;
   for (int e = threadIdx.x; e <= E; e += kGateThreads) cnt_s[e] = 0;
   __syncthreads();
   ptx::grid_dependency_wait();
+  const bool biased = a.bias != nullptr;
+  if (biased)
+    for (int e = threadIdx.x; e < E; e += kGateThreads) bias_s[e] = a.bias[e];
+  __syncthreads();
 
-  float bias[VPL], acc[VPL];
+  float acc[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int col = lane + 32 * i;
-    bias[i] = a.bias != nullptr && col < E ? a.bias[col] : 0.0f;
-    acc[i] = 0.0f;
-  }
+  for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
   const T* logits = static_cast<const T*>(a.logits);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
@@ -146,8 +149,8 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const float key = l[i] + bias[i];   // also turns -0 into +0: they tie
       const bool in = lane + 32 * i < E;
+      const float key = l[i] + (biased && in ? bias_s[lane + 32 * i] : 0.0f);   // also turns -0 into +0: they tie
       bad |= in && !(key < INFINITY);
       u[i] = in ? sortable(key) : 0u;
       best = max(best, u[i]);
@@ -160,12 +163,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
     float w = 0.0f;
     if (route) {
       // without a bias the largest key is the largest logit
-      const float m = SIGMOID ? 0.0f : a.bias == nullptr ? unsortable(top) : row_max<VPL>(l);
-      const float total = scores<VPL, SIGMOID>(l, m);
-      const float inv = 1.0f / total;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] += l[i] * inv;
-      ++routed;
+      const float m = SIGMOID ? 0.0f : !biased ? unsortable(top) : row_max<VPL>(l);
 
       // The K-th largest lane maximum (equal ones go together: a lower bound still).
       unsigned floor = top;
@@ -178,18 +176,23 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
         floor = max(floor, kKeyNegInf + 1);
       }
       int found = 0;
+      float picked = 0.0f;                 // the pick's logit
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         const unsigned who = __ballot_sync(kFull, u[i] >= floor);
         if (u[i] >= floor) {
           const int at = found + __popc(who & ptx::lanemask_lt());
-          if (at < 32) list[at] = static_cast<uint64_t>(u[i]) << 32 | ~static_cast<unsigned>(lane + 32 * i);
+          if (at < 32) {
+            list[at] = static_cast<uint64_t>(u[i]) << 32 | ~static_cast<unsigned>(lane + 32 * i);
+            list_l[at] = l[i];
+          }
         }
         found += __popc(who);
       }
       __syncwarp();
       if (found <= 32) {
         const uint64_t own = lane < found ? list[lane] : 0;
+        picked = list_l[lane];
         int before = 0;
         for (int j = 0; j < found; ++j) before += list[j] > own;
         if (lane < found) {
@@ -203,7 +206,10 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
           for (int i = VPL - 1; i >= 0; --i)
             if (u[i] == top) lowest = static_cast<unsigned>(lane + 32 * i);
           const unsigned id = __reduce_min_sync(kFull, lowest);
-          if (lane == k) mine = static_cast<int>(id);
+          if (lane == k) {
+            mine = static_cast<int>(id);
+            picked = load_logit(row + mine);
+          }
           best = 0;
 #pragma unroll
           for (int i = 0; i < VPL; ++i) {
@@ -214,10 +220,14 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
         }
       }
       __syncwarp();   // the list is read
+      const float total = scores<VPL, SIGMOID>(l, m);
+      const float inv = 1.0f / total;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) acc[i] += l[i] * inv;
+      ++routed;
       float s = 0.0f;
       if (mine >= 0) {
-        const float lk = load_logit(row + mine);
-        s = SIGMOID ? sigmoid_fast(lk) : __expf(lk - m) * inv;
+        s = SIGMOID ? sigmoid_fast(picked) : __expf(picked - m) * inv;
         atomicAdd(&cnt_s[mine], 1);
       }
       const float den = a.normalize ? fmaxf(warp_sum(s), kTiny) : 1.0f;
@@ -301,7 +311,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_forward_kernel(GateArgs a) 
 // balance part is zero; sigmoid: dl = s (1 - s) ds.  The picked columns are
 // written by lane k after the row, over the value the row store left there.
 template <int VPL, typename T, bool SIGMOID>
-__global__ void __launch_bounds__(kGateThreads) gate_backward_kernel(GateArgs a) {
+__global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2) gate_backward_kernel(GateArgs a) {
   const int E = a.num_experts, K = a.topk;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   ptx::grid_dependency_wait();
@@ -377,15 +387,17 @@ __global__ void __launch_bounds__(kGateThreads) gate_backward_kernel(GateArgs a)
 template <typename T, bool SIGMOID>
 cudaError_t launch_gate(const GateArgs& a, bool backward, cudaStream_t stream) {
   const int vpl = (a.num_experts + 31) / 32;
-  const int64_t want = ceil_div64(a.num_tokens, kGateWarps);
-  const int64_t most = backward ? 4 * static_cast<int64_t>(device_sm_count()) : kGateMaxCtas;
-  const unsigned grid = static_cast<unsigned>(max64(1, min64(want, most)));
-  const size_t smem = backward ? 0 : 4 * static_cast<size_t>(2 * a.num_experts + 1);
+  const size_t smem = backward ? 0 : 4 * static_cast<size_t>(3 * a.num_experts + 1);
   count_launch();
-#define MOE_GATE_CASE(V)                                                                                     \
-  if (vpl <= V)                                                                                              \
-    return backward ? launch_pdl(gate_backward_kernel<V, T, SIGMOID>, grid, kGateThreads, smem, stream, a)   \
-                    : launch_pdl(gate_forward_kernel<V, T, SIGMOID>, grid, kGateThreads, smem, stream, a);
+  // One wave of CTAs walks the tokens.
+  const auto run = [&](auto kernel) {
+    const int ctas = cached_occupancy(kernel, kGateThreads, smem);
+    const int64_t most = min64(static_cast<int64_t>(ctas > 0 ? ctas : 1) * device_sm_count(), kGateMaxCtas);
+    const int64_t grid = max64(1, min64(ceil_div64(a.num_tokens, kGateWarps), most));
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kGateThreads, smem, stream, a);
+  };
+#define MOE_GATE_CASE(V) \
+  if (vpl <= V) return backward ? run(gate_backward_kernel<V, T, SIGMOID>) : run(gate_forward_kernel<V, T, SIGMOID>);
   MOE_GATE_CASE(1)
   MOE_GATE_CASE(2)
   MOE_GATE_CASE(4)

@@ -113,8 +113,8 @@ T* at(void* ws, size_t off) {
 // tokens in the gate's workspace, and each group of kGateGroup CTAs one of its own:
 // [error word | tickets | pad to 256 B][fp32 kGatePartials x E]
 // [int32 kGatePartials x (E + 1)].
-constexpr int kGateMaxCtas = 304;
-constexpr int kGateGroup = 16;
+constexpr int kGateMaxCtas = 608;
+constexpr int kGateGroup = 24;
 constexpr int kGatePartials = kGateMaxCtas + (kGateMaxCtas + kGateGroup - 1) / kGateGroup;
 static_assert(16 + 4 * (1 + (kGateMaxCtas + kGateGroup - 1) / kGateGroup) <= 256, "tickets");
 
