@@ -37,8 +37,10 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
+constexpr int kGateMaxVpl = 32;              // columns of a lane: MOE_MAX_EXPERTS / 32
 constexpr float kTiny = 1e-30f;              // floor of a sum of scores that divides
-constexpr unsigned kKeyNegInf = 0x007fffffu; // sortable key of -inf
+constexpr unsigned kKeyNegInf = 0x007fffffu; // sortable keys of -inf and +inf
+constexpr unsigned kKeyInf = 0xff800000u;
 
 template <typename T>
 __device__ __forceinline__ float load_logit(const T* p);
@@ -55,10 +57,11 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) {
   *p = *reinterpret_cast<const uint16_t*>(&b);
 }
 
-// Unsigned integers in the order of the floats (no NaN); never 0.
+// Unsigned integers in the order of the floats; never 0.  The NaN of an addition
+// (0x7fffffff) comes after +inf.
 __device__ __forceinline__ unsigned sortable(float f) {
-  const unsigned b = __float_as_uint(f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const int b = __float_as_int(f);
+  return static_cast<unsigned>(b ^ (b >> 31 | static_cast<int>(0x80000000u)));
 }
 __device__ __forceinline__ float unsortable(unsigned u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
@@ -119,14 +122,14 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   uint64_t* list = list_s[warp];
   float* list_l = list_l_s[warp];
-  float* bias_s = reinterpret_cast<float*>(smem) + 2 * E + 1;   // [E], with a bias
+  float* bias_s = reinterpret_cast<float*>(smem) + 2 * E + 1;   // [32 * VPL], with a bias
   for (int e = threadIdx.x; e < E; e += kGateThreads) sum_s[e] = 0.0f;
   for (int e = threadIdx.x; e <= E; e += kGateThreads) cnt_s[e] = 0;
   __syncthreads();
   ptx::grid_dependency_wait();
   const bool biased = a.bias != nullptr;
   if (biased)
-    for (int e = threadIdx.x; e < E; e += kGateThreads) bias_s[e] = a.bias[e];
+    for (int e = threadIdx.x; e < 32 * VPL; e += kGateThreads) bias_s[e] = e < E ? a.bias[e] : 0.0f;
   __syncthreads();
 
   float acc[VPL];
@@ -146,19 +149,16 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
     load_row<VPL, T>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
 
     unsigned u[VPL], best = 0;
-    bool bad = false;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const bool in = lane + 32 * i < E;
-      const float key = l[i] + (biased && in ? bias_s[lane + 32 * i] : 0.0f);   // also turns -0 into +0: they tie
-      bad |= in && !(key < INFINITY);
-      u[i] = in ? sortable(key) : 0u;
+      // the addition turns -0 into +0 (they tie) and any NaN into the one that sorts above +inf
+      const float key = l[i] + (biased ? bias_s[lane + 32 * i] : 0.0f);
+      u[i] = sortable(key);
       best = max(best, u[i]);
     }
-    bad = __any_sync(kFull, bad);
-    if (bad && lane == 0) set_error(a.err, MOE_ERR_INVALID_ARG);
     unsigned top = __reduce_max_sync(kFull, best);
-    const bool route = !bad && top > kKeyNegInf;
+    if (top >= kKeyInf && lane == 0) set_error(a.err, MOE_ERR_INVALID_ARG);
+    const bool route = top < kKeyInf && top > kKeyNegInf;
     int mine = -1, slot = lane;            // this lane's pick and its place among the K
     float w = 0.0f;
     if (route) {
@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         const unsigned who = __ballot_sync(kFull, u[i] >= floor);
+        if (who == 0) continue;
         if (u[i] >= floor) {
           const int at = found + __popc(who & ptx::lanemask_lt());
           if (at < 32) {
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
         const uint64_t own = lane < found ? list[lane] : 0;
         picked = list_l[lane];
         int before = 0;
+#pragma unroll 4
         for (int j = 0; j < found; ++j) before += list[j] > own;
         if (lane < found) {
           if (before < K) mine = static_cast<int>(~static_cast<unsigned>(own));
@@ -329,6 +331,15 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
   int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
   float next[VPL];
   load_row<VPL, T>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
+  // the token's picks and their gradients, also a token ahead
+  const auto load_pick = [&](int64_t tok, int64_t* id, float* d) {
+    const bool in = lane < K && tok < a.num_tokens;
+    *id = in ? a.topk_idx[tok * K + lane] : -1;
+    *d = in && a.dweights != nullptr ? a.dweights[tok * K + lane] : 0.0f;
+  };
+  int64_t next_id;
+  float next_dw;
+  load_pick(t, &next_id, &next_dw);
   for (; t < a.num_tokens; t += stride) {
     const T* row = logits + t * a.logits_stride;
     T* out = static_cast<T*>(a.dlogits) + t * a.dlogits_stride;
@@ -336,7 +347,9 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
 #pragma unroll
     for (int i = 0; i < VPL; ++i) l[i] = next[i];
     load_row<VPL, T>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
-    int64_t mine = lane < K ? a.topk_idx[t * K + lane] : -1;
+    int64_t mine = next_id;
+    float dw = next_dw;
+    load_pick(t + stride, &next_id, &next_dw);
     if (mine >= E) {
       mine = -1;
       set_error(a.err, MOE_ERR_BAD_EXPERT_ID);
@@ -355,11 +368,12 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
     for (int i = 0; i < VPL; ++i) dot += l[i] * g[i];
     const float A = warp_sum(dot) * inv;
 
-    float s = 0.0f, dw = 0.0f;
+    float s = 0.0f;
     if (mine >= 0) {
       const float lk = load_logit(row + mine);
       s = SIGMOID ? sigmoid_fast(lk) : __expf(lk - m) * inv;
-      if (a.dweights != nullptr) dw = a.dweights[t * K + lane];
+    } else {
+      dw = 0.0f;
     }
     float ds = a.scale * dw;
     if (a.normalize) {
@@ -387,7 +401,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
 template <typename T, bool SIGMOID>
 cudaError_t launch_gate(const GateArgs& a, bool backward, cudaStream_t stream) {
   const int vpl = (a.num_experts + 31) / 32;
-  const size_t smem = backward ? 0 : 4 * static_cast<size_t>(3 * a.num_experts + 1);
+  const size_t smem = backward ? 0 : 4 * (static_cast<size_t>(2 * a.num_experts + 1) + 32 * kGateMaxVpl);
   count_launch();
   // One wave of CTAs walks the tokens.
   const auto run = [&](auto kernel) {
