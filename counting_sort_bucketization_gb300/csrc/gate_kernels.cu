@@ -73,9 +73,15 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// ex2 of a rounded product: the argument's rounding adds 2^-24 |x| to the result's
-// relative error, which leaves scores good to 2^-18 down to e^-32 of the largest.
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// e^x as 2^(x log2 e): the product's rounding adds 2^-24 |x| to the result's relative
+// error, which leaves scores good to 2^-18 down to e^-32 of the largest.  Results
+// below 2^-126 are zero.
+__device__ __forceinline__ float exp_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + exp_fast(-x)); }
 
 // One row's logits in registers: columns lane, lane + 32, ...; -inf past E.
 template <int VPL, typename T>
@@ -95,7 +101,7 @@ __device__ __forceinline__ float scores(float* l, float m) {
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     // exp(-inf) = 0, and sigmoid(-inf) = 1 / (1 + inf) = 0: closed experts score nothing
-    l[i] = SIGMOID ? sigmoid_fast(l[i]) : __expf(l[i] - m);
+    l[i] = SIGMOID ? sigmoid_fast(l[i]) : exp_fast(l[i] - m);
     s += l[i];
   }
   return fmaxf(warp_sum(s), kTiny);
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
           const int at = found + __popc(who & ptx::lanemask_lt());
           if (at < 32) {
             list[at] = static_cast<uint64_t>(u[i]) << 32 | ~static_cast<unsigned>(lane + 32 * i);
-            list_l[at] = l[i];
+            if (biased) list_l[at] = l[i];
           }
         }
         found += __popc(who);
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
       __syncwarp();
       if (found <= 32) {
         const uint64_t own = lane < found ? list[lane] : 0;
-        picked = list_l[lane];
+        picked = biased ? list_l[lane] : unsortable(static_cast<unsigned>(own >> 32));
         int before = 0;
 #pragma unroll 4
         for (int j = 0; j < found; ++j) before += list[j] > own;
@@ -223,17 +229,17 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
       }
       __syncwarp();   // the list is read
       const float total = scores<VPL, SIGMOID>(l, m);
-      const float inv = 1.0f / total;
+      const float inv = __fdividef(1.0f, total);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) acc[i] += l[i] * inv;
       ++routed;
       float s = 0.0f;
       if (mine >= 0) {
-        s = SIGMOID ? sigmoid_fast(picked) : __expf(picked - m) * inv;
+        s = SIGMOID ? sigmoid_fast(picked) : exp_fast(picked - m) * inv;
         atomicAdd(&cnt_s[mine], 1);
       }
       const float den = a.normalize ? fmaxf(warp_sum(s), kTiny) : 1.0f;
-      w = a.scale * s / den;
+      w = __fdividef(a.scale * s, den);
     }
     if (slot < K) {
       a.topk_idx[t * K + slot] = mine;
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
     }
     const float m = SIGMOID ? 0.0f : row_max<VPL>(l);
     const float total = scores<VPL, SIGMOID>(l, m);
-    const float inv = 1.0f / total;
+    const float inv = __fdividef(1.0f, total);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) dot += l[i] * g[i];
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
     float s = 0.0f;
     if (mine >= 0) {
       const float lk = load_logit(row + mine);
-      s = SIGMOID ? sigmoid_fast(lk) : __expf(lk - m) * inv;
+      s = SIGMOID ? sigmoid_fast(lk) : exp_fast(lk - m) * inv;
     } else {
       dw = 0.0f;
     }
