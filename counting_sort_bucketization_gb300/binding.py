@@ -79,6 +79,8 @@ def library_path() -> str:
 def load_library() -> ctypes.CDLL:
     """Open libmoe_layout.so (built by ``build.build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -158,9 +160,17 @@ def _check(status: int, what: str) -> None:
         raise LayoutError(what, status)
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+# The current stream's handle without building a torch Stream (4 us of a call's host time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and _current_device is not None:
+        return _raw_stream(_current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _nbytes(t: torch.Tensor) -> int:
@@ -182,7 +192,7 @@ def _dev(t: torch.Tensor | None, name: str, dtype=None, numel=None, allow_none=F
         raise ValueError(f"{name} needs at least {numel} elements, has {t.numel()}")
     if nbytes is not None and _nbytes(t) < nbytes:
         raise ValueError(f"{name} needs at least {nbytes} bytes, has {_nbytes(t)}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def workspace_bytes(desc) -> int:
@@ -450,7 +460,7 @@ def _matrix(t, name, rows, cols, dtypes):
     ld = t.stride(0) if rows > 1 else cols
     if ld < cols:
         raise ValueError(f"{name}'s rows overlap")
-    return ctypes.c_void_p(t.data_ptr()), int(ld)
+    return t.data_ptr(), int(ld)
 
 
 _LOGITS = (torch.float32, torch.bfloat16)
