@@ -133,89 +133,113 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_rows_kernel(QuantRowsAr
 }
 
 // ---------------------------------------------------------------- columns
-// A CTA transposes a tile of 128 rows (one scale block; segments start at
-// multiples of 128, so it lies in one expert) x 64 columns.  A thread holds 4
+// A CTA transposes tiles of 128 rows (one scale block; segments start at
+// multiples of 128, so it lies in one expert) x 64 columns, kColTiles of them
+// side by side with the next tile's rows on their way.  A thread holds 4
 // consecutive rows x 8 columns, so its codes of a column make one 32-bit word
 // of the transposed tile; words go through shared memory at a pitch of 33 and
 // leave as 128-byte runs of a transposed row.
 constexpr int kColsThreads = 256;
 constexpr int kTileCols = 64;
+constexpr int kColTiles = 4;
 constexpr int kPitch = 33;
+
+// Larger magnitudes of two pairs of bf16 (exact: no rounding); NaN stays.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+  return r;
+}
 
 __global__ void __launch_bounds__(kColsThreads) quantize_cols_kernel(QuantColsArgs a) {
   __shared__ uint32_t tile[kTileCols * kPitch];
-  __shared__ float wmax[kColsThreads / 32][kTileCols];
+  __shared__ uint32_t wmax[kColsThreads / 32][kTileCols / 2];
+  __shared__ float inv_s[kTileCols];
   __shared__ int valid_s;
   ptx::grid_dependency_wait();
-  const int64_t chunks = (a.cols + kTileCols - 1) / kTileCols;
+  const int64_t chunks = (a.cols + kColTiles * kTileCols - 1) / (kColTiles * kTileCols);
   const int64_t rb = static_cast<int64_t>(blockIdx.x) / chunks;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) % chunks * kTileCols;
+  const int64_t c_first = static_cast<int64_t>(blockIdx.x) % chunks * (kColTiles * kTileCols);
   const int64_t r0 = rb * kBlock;
+  const int g = threadIdx.x / 8, c8 = threadIdx.x % 8;   // rows 4g..4g+3, columns 8*c8..+7
+  const int warp = threadIdx.x / 32;
+  const uint16_t* src = a.x + (r0 + 4 * g) * a.cols + c8 * 8;
+  uint4 v[4], next[4];
+  // Rows in the buffer; gap rows among them are dropped below.
+  const auto load = [&](int64_t c0, uint4* to) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      to[p] = make_uint4(0, 0, 0, 0);
+      if (r0 + 4 * g + p < a.capacity && c0 + c8 * 8 < a.cols) to[p] = ptx::ld_nc_v4(src + p * a.cols + c0);
+    }
+  };
+  load(c_first, next);
+  // The expert whose segment holds row r0 says how many of the block's rows are real.
   const int total = a.expert_offset[a.num_experts];
+  if (threadIdx.x == 0) valid_s = 0;
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.num_experts; e += kColsThreads) {
+    const int start = a.expert_offset[e];
+    if (start <= r0 && r0 < a.expert_offset[e + 1])
+      valid_s = static_cast<int>(max64(0, min64(kBlock, static_cast<int64_t>(start) + a.expert_count[e] - r0)));
+  }
   if (r0 >= total || total > a.capacity) {
     if (total > a.capacity && blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, MOE_ERR_CAPACITY);
     return;
   }
-  if (threadIdx.x == 0) {
-    // The expert whose segment holds row r0: the last one that starts at or before it.
-    int lo = 0, hi = a.num_experts;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.expert_offset[mid] <= r0) lo = mid; else hi = mid;
-    }
-    const int64_t end = static_cast<int64_t>(a.expert_offset[lo]) + a.expert_count[lo];
-    valid_s = static_cast<int>(max64(0, min64(kBlock, end - r0)));
-  }
   __syncthreads();
   const int valid = valid_s;
-  const int g = threadIdx.x / 8, c8 = threadIdx.x % 8;   // rows 4g..4g+3, columns 8*c8..+7
-  const int64_t c = c0 + c8 * 8;
-  uint4 v[4];
+  for (int ct = 0; ct < kColTiles; ++ct) {
+    const int64_t c0 = c_first + ct * kTileCols;
+    if (c0 >= a.cols) break;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int r = 4 * g + p;
-    v[p] = make_uint4(0, 0, 0, 0);
-    if (r < valid && c < a.cols) v[p] = ptx::ld_nc_v4(a.x + (r0 + r) * a.cols + c);
-  }
-  float f[4][8], m[8];
+    for (int p = 0; p < 4; ++p) v[p] = 4 * g + p < valid ? next[p] : make_uint4(0, 0, 0, 0);
+    if (ct + 1 < kColTiles) load(c0 + kTileCols, next);
+    uint32_t m[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-  for (int p = 0; p < 4; ++p) unpack8(v[p], f[p]);
+    for (int p = 0; p < 4; ++p) {
+      m[0] = max_abs_bf16x2(m[0], v[p].x);
+      m[1] = max_abs_bf16x2(m[1], v[p].y);
+      m[2] = max_abs_bf16x2(m[2], v[p].z);
+      m[3] = max_abs_bf16x2(m[3], v[p].w);
+    }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m[i] = kAmaxFloor;
+    for (int i = 0; i < 4; ++i) {
+      m[i] = max_abs_bf16x2(m[i], __shfl_xor_sync(0xffffffffu, m[i], 8));
+      m[i] = max_abs_bf16x2(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+    }
+    if (threadIdx.x % 32 < 8) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) m[i] = max_nan(m[i], fabsf(f[p][i]));
-    m[i] = max_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], 8));
-    m[i] = max_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
-  }
-  const int warp = threadIdx.x / 32;
-  if (threadIdx.x % 32 < 8) {
+      for (int i = 0; i < 4; ++i) wmax[warp][c8 * 4 + i] = m[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < kTileCols) {
+      uint32_t t = wmax[0][threadIdx.x / 2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wmax[warp][c8 * 8 + i] = m[i];
-  }
-  __syncthreads();
-  if (threadIdx.x < kTileCols) {
-    float t = wmax[0][threadIdx.x];
+      for (int w = 1; w < kColsThreads / 32; ++w) t = max_abs_bf16x2(t, wmax[w][threadIdx.x / 2]);
+      const float amax = __uint_as_float(threadIdx.x % 2 ? t & 0xffff0000u : t << 16);
+      const float sf = __fdiv_rn(max_nan(amax, kAmaxFloor), kE4m3Max);
+      if (c0 + threadIdx.x < a.cols) a.sf[rb * a.cols + c0 + threadIdx.x] = sf;
+      inv_s[threadIdx.x] = __fdiv_rn(1.0f, sf);
+    }
+    __syncthreads();
+    float f[4][8];
 #pragma unroll
-    for (int w = 1; w < kColsThreads / 32; ++w) t = max_nan(t, wmax[w][threadIdx.x]);
-    const float sf = __fdiv_rn(t, kE4m3Max);
-    if (c0 + threadIdx.x < a.cols) a.sf[rb * a.cols + c0 + threadIdx.x] = sf;
-    wmax[0][threadIdx.x] = __fdiv_rn(1.0f, sf);
-  }
-  __syncthreads();
+    for (int p = 0; p < 4; ++p) unpack8(v[p], f[p]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float inv = wmax[0][c8 * 8 + i];
-    tile[(c8 * 8 + i) * kPitch + g] = cvt_e4m3x4(f[0][i] * inv, f[1][i] * inv, f[2][i] * inv, f[3][i] * inv);
-  }
-  __syncthreads();
+    for (int i = 0; i < 8; ++i) {
+      const float inv = inv_s[c8 * 8 + i];
+      tile[(c8 * 8 + i) * kPitch + g] = cvt_e4m3x4(f[0][i] * inv, f[1][i] * inv, f[2][i] * inv, f[3][i] * inv);
+    }
+    __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kTileCols * 8 / kColsThreads; ++j) {
-    const int unit = threadIdx.x + j * kColsThreads;
-    const int col = unit / 8, part = unit % 8;
-    if (c0 + col < a.cols) {
-      const uint32_t* t = tile + col * kPitch + part * 4;
-      ptx::st_v4(a.q + (c0 + col) * a.ld + r0 + part * 16, make_uint4(t[0], t[1], t[2], t[3]));
+    for (int j = 0; j < kTileCols * 8 / kColsThreads; ++j) {
+      const int unit = threadIdx.x + j * kColsThreads;
+      const int col = unit / 8, part = unit % 8;
+      if (c0 + col < a.cols) {
+        const uint32_t* t = tile + col * kPitch + part * 4;
+        ptx::st_v4(a.q + (c0 + col) * a.ld + r0 + part * 16, make_uint4(t[0], t[1], t[2], t[3]));
+      }
     }
   }
 }
@@ -272,7 +296,7 @@ cudaError_t launch_quantize_rows(const QuantRowsArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_quantize_cols(const QuantColsArgs& a, cudaStream_t stream) {
   if (a.capacity == 0) return cudaSuccess;
-  const int64_t grid = ceil_div64(a.capacity, kBlock) * ceil_div64(a.cols, kTileCols);
+  const int64_t grid = ceil_div64(a.capacity, kBlock) * ceil_div64(a.cols, kColTiles * kTileCols);
   if (grid > kMaxGrid) return cudaErrorInvalidConfiguration;
   count_launch();
   return launch_pdl(quantize_cols_kernel, dim3(static_cast<unsigned>(grid)), kColsThreads, 0, stream, a);
