@@ -57,7 +57,12 @@ __device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float 
   return cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + 2^(-g log2 e)); the exponent's rounding adds 2^-24 |g| where e^-g counts.
+__device__ __forceinline__ float sigmoid(float g) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  return __fdividef(1.0f, 1.0f + e);
+}
 
 // The larger of two magnitudes; a NaN on either side stays (fmaxf would drop it).
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -151,7 +156,7 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-__global__ void __launch_bounds__(kColsThreads) quantize_cols_kernel(QuantColsArgs a) {
+__global__ void __launch_bounds__(kColsThreads, 4) quantize_cols_kernel(QuantColsArgs a) {
   __shared__ uint32_t tile[kTileCols * kPitch];
   __shared__ uint32_t wmax[kColsThreads / 32][kTileCols / 2];
   __shared__ float inv_s[kTileCols];
