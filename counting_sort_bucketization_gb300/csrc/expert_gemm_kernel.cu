@@ -21,7 +21,10 @@
 //           of a k-block and 128-column block multiply to one number for it.
 //   kFew    P = weights, Q = receive rows; one CTA.  The tensor core takes any
 //           multiple of 16 columns, so an expert with one token does not pay for
-//           128.  Bound by the reading of the weights.
+//           128.  Bound by the reading of the weights.  With fewer tiles than half
+//           the SMs, a cluster of CTAs takes a tile, each a share of K, and the
+//           first adds the others' sums, in their order, from distributed shared
+//           memory.
 //   kWgrad  P = x^T, Q = dy^T (so that columns of dw run along lanes); a pair.
 //
 // What shaped it, measured on 16 experts of 1024 rows, 7168 -> 4096:
@@ -139,7 +142,7 @@ __device__ __forceinline__ int col_tiles(const GemmParams& p) {
 }
 
 template <Kind KIND>
-__device__ __forceinline__ Tile get_tile(const GemmParams& p, const Shared& s, int t, int rank) {
+__device__ __forceinline__ Tile get_tile(const GemmParams& p, const Shared& s, int t, int rank, int split) {
   using C = Config<KIND>;
   int lo = 0, hi = p.num_experts - 1;     // first expert whose tiles end after t
   while (lo < hi) {
@@ -154,6 +157,11 @@ __device__ __forceinline__ Tile get_tile(const GemmParams& p, const Shared& s, i
   r.last = row == nr - 1;
   r.k0 = KIND == kWgrad ? start : 0;
   r.kblocks = KIND == kWgrad ? ceil_div(count, kKBlock) : p.kblocks;
+  if (KIND == kFew) {   // this CTA's share of K
+    const int first = p.kblocks * split / p.splits;
+    r.k0 = first * kKBlock;
+    r.kblocks = p.kblocks * (split + 1) / p.splits - first;
+  }
   if (KIND == kMany) {
     const int at = row * 256 + rank * kPRows;
     r.p0 = start + at;
@@ -390,8 +398,16 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
   if (CTAS == 2) tc::cluster_sync();   // the pair's barriers and tensor memory exist
   tc::fence_after();
   const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(s.tmem)));
-  const int first_tile = static_cast<int>(blockIdx.x) / CTAS, step = static_cast<int>(gridDim.x) / CTAS;
+  const int splits = KIND == kFew ? p.splits : 1;   // CTAs that share a tile's K
+  const int split = splits > 1 ? static_cast<int>(tc::cluster_rank()) : 0;
+  const int first_tile = static_cast<int>(blockIdx.x) / (CTAS * splits), step = static_cast<int>(gridDim.x) / (CTAS * splits);
   bool ok = true;
+  // Every warp of a cluster that shares tiles meets twice at a tile's end: when the
+  // sums are in shared memory, and when they are read.  A warp whose wait ran out
+  // still comes.
+  const auto meet = [&] {
+    if (KIND == kFew && splits > 1) tc::cluster_sync();
+  };
 
   if (warp < 4) {
     tc::reg_dec<C::kOtherRegs>();
@@ -401,8 +417,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       // lane issues.
       Ring<kStages> ring;
       uint32_t loads = 0;
-      for (int t = first_tile; t < tiles && ok; t += step) {
-        const Tile tile = get_tile<KIND>(p, s, t, rank);
+      for (int t = first_tile; t < tiles; t += step, meet(), meet()) {
+        if (!ok) continue;
+        const Tile tile = get_tile<KIND>(p, s, t, rank, split);
         // Q rows of each accumulator, an equal share by each CTA of a pair, in boxes of 64;
         // 16 for the shortest segments
         const int n0 = uniform(tile.n[0]), n1 = uniform(tile.n[1]);
@@ -444,8 +461,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         uint32_t used = 0;
         const uint64_t p_desc = tc::operand_desc(ptx::smem_addr(mem.stage[0]));
         const uint32_t q_off = (kPBytes + h * C::kQRows * kKBlock) >> 4;
-        for (int t = first_tile; t < tiles && ok; t += step) {
-          const Tile tile = get_tile<KIND>(p, s, t, rank);
+        for (int t = first_tile; t < tiles; t += step, meet(), meet()) {
+          if (!ok) continue;
+          const Tile tile = get_tile<KIND>(p, s, t, rank, split);
           const int kblocks = uniform(tile.kblocks), n = uniform(h == 0 ? tile.n[0] : tile.n[1]);
           const uint32_t idesc = tc::instr_desc(kPRows * CTAS, n);
           for (int kb = 0; kb < kblocks; ++kb) {
@@ -476,6 +494,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
         for (uint32_t i = 0; i < NBUF; ++i, ++used, buf.next())   // the epilogues' last (remote) arrivals
           if (used >= NBUF) ok &= wait_warp(&s.acc_empty[h][buf.i], buf.phase ^ 1, p.wait_ns);
+      } else {
+        for (int t = first_tile; t < tiles; t += step, meet(), meet()) {}
       }
     } else {
       // ---- scales --------------------------------------------------------
@@ -486,8 +506,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       constexpr int kSets = KIND == kWgrad ? 2 : 1;            // of row scales: kMany's are the same for both accumulators
       constexpr int kWeights = KIND == kWgrad ? kRows : ACCS;
       Ring<NBUF> ring;
-      for (int t = first_tile; t < tiles && ok; t += step) {
-        const Tile tile = get_tile<KIND>(p, s, t, rank);
+      for (int t = first_tile; t < tiles; t += step, meet(), meet()) {
+        if (!ok) continue;
+        const Tile tile = get_tile<KIND>(p, s, t, rank, split);
         const int kblocks = uniform(tile.kblocks);
         const int64_t kb0 = tile.k0 / kKBlock;
         const int valid = (KIND == kMany ? tile.p_valid : tile.q_valid) - lane;
@@ -511,7 +532,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             for (int i = 0; i < kRows; ++i)
               wv[i] = in && lane + i * 32 < tile.p_valid ? __ldg(ws + static_cast<int64_t>(kb) * p.out_cols + i * 32) : 0.0f;
           } else {
-            wv[0] = in && block < blocks ? __ldg(ws + kb) : 0.0f;
+            wv[0] = in && block < blocks ? __ldg(ws + kb0 + kb) : 0.0f;
             if (KIND == kMany) wv[ACCS - 1] = in && block + 1 < blocks ? __ldg(ws + p.kblocks + kb) : 0.0f;
           }
         };
@@ -554,10 +575,15 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     uint32_t freed = ptx::smem_addr(&s.acc_empty[half][0]);   // the leader's barriers
     if (CTAS == 2) freed = tc::map_to_rank(freed, 0);
     Ring<NBUF> buf;
-    for (int t = first_tile; t < tiles && ok; t += step) {
+    for (int t = first_tile; t < tiles; t += step) {
+      if (!ok) {
+        meet();
+        meet();
+        continue;
+      }
       int n, kblocks;                                         // all that lives over the k-blocks
       {
-        const Tile tile = get_tile<KIND>(p, s, t, rank);
+        const Tile tile = get_tile<KIND>(p, s, t, rank, split);
         n = (half == 0 ? tile.n[0] : tile.n[1]) - part * C::kWarpCols;
         kblocks = tile.kblocks;
       }
@@ -656,9 +682,32 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
         buf.next();
       }
-      if (!ok) break;
+      if (KIND == kFew && splits > 1) {
+        // pair r of epilogue thread j at r * 256 + j of the stages, which are free
+        uint64_t* sums = reinterpret_cast<uint64_t*>(mem.stage) + (threadIdx.x - 128);
+        if (split > 0 && n > 0)
+#pragma unroll
+          for (int c = 0; c < kBatches; ++c)
+            if (c * kBatchCols < n)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sums[(c * 16 + i) * 256] = acc[c][i];
+        meet();
+        if (split == 0 && n > 0)
+          for (int q = 1; q < splits; ++q) {
+            const uint32_t from = tc::map_to_rank(ptx::smem_addr(sums), q);
+#pragma unroll
+            for (int c = 0; c < kBatches; ++c)
+              if (c * kBatchCols < n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[c][i] = tc::add2(acc[c][i], tc::ld_cluster(from + (c * 16 + i) * 256 * 8));
+          }
+        ptx::fence_proxy_async_smem();   // the next tile's loads come through the async proxy
+        meet();
+      }
+      if (!ok) continue;
+      if (split > 0) continue;
 
-      const Tile tile = get_tile<KIND>(p, s, t, rank);
+      const Tile tile = get_tile<KIND>(p, s, t, rank, split);
       if constexpr (KIND == kMany) store_rows(p, tile, quarter * 32 + lane, half * kAccCols + part * C::kWarpCols, acc);
       else store_columns<KIND>(p, tile, quarter, half, part, lane, mem.out + ew * kOutBytes, acc);
       if (KIND != kWgrad && tile.last) zero_gap<KIND>(p, s, tile, rank, ew, lane);
@@ -711,12 +760,12 @@ cudaError_t encode(CUtensorMap* m, const void* base, int64_t width, int64_t rows
 template <Kind KIND>
 cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const CUtensorMap& map_q16, const GemmParams& p,
                    cudaStream_t stream) {
-  constexpr int CTAS = Config<KIND>::kCtas;
+  const int cluster = Config<KIND>::kCtas * p.splits;
   const auto kernel = expert_gemm_kernel<KIND>;
   cudaError_t e = ensure_smem_limit(kernel, kSmemBytes<KIND>);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() / CTAS * CTAS));
+  cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() / cluster * cluster));
   cfg.blockDim = dim3(Config<KIND>::kThreads);
   cfg.dynamicSmemBytes = kSmemBytes<KIND>;
   cfg.stream = stream;
@@ -724,7 +773,7 @@ cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const CUt
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -745,6 +794,7 @@ GemmParams common_params(const ExpertGemmArgs& a) {
   p.err = a.err;
   p.wait_ns = wait_config().limit_ns;
   p.extra_tx = wait_config().extra_tx;
+  p.splits = 1;
   return p;
 }
 
@@ -757,9 +807,17 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream) {
   p.col_sf = a.w_sf;
   p.out_cols = static_cast<int>(a.width_out);
   p.kblocks = static_cast<int>(ceil_div64(a.width_in, kKBlock));
-  // Rows an expert has in the mean: many fill the 256 rows of a pair's tile.
+  // kFew's tile holds 128 rows of an expert, kMany's 256.  Up to a mean of 112 rows
+  // (nearly all experts in one tile) kFew measured faster, from 128 on kMany: 32 experts,
+  // 7168 -> 4096, 112 rows 187 against 218 us, 128 rows 224 against 217, 256 rows 349
+  // against 283; 2048 -> 7168 the same.
   const int64_t mean = a.pairs / a.num_experts;
-  const bool many = mean >= 192;
+  const bool many = mean >= 120;
+  if (!many) {
+    // The tiles if the pairs are what they are said to be; at least 4 k-blocks a share.
+    const int64_t tiles = (min64(a.num_experts, max64(a.pairs, 1)) + a.pairs / 128) * ceil_div64(a.width_out, kPRows);
+    while (p.splits < 8 && 2 * p.splits * tiles <= device_sm_count() && 8 * p.splits <= p.kblocks) p.splits *= 2;
+  }
   CUtensorMap rows, rows16, weights;
   cudaError_t e = encode(&rows, a.x, a.width_in, a.capacity, 1, many ? kPRows : 64);
   if (e == cudaSuccess) e = encode(&rows16, a.x, a.width_in, a.capacity, 1, 16);

@@ -218,6 +218,7 @@ struct GemmParams {
   int out_cols;                  // columns (and pitch) of out
   int dy_rows;                   // gradient: rows of out of an expert
   int kblocks;                   // forward: k-blocks of a row
+  int splits;                    // CTAs that share a tile's k-blocks (kFew)
   int num_experts;
   const int32_t* expert_offset;
   const int32_t* expert_count;

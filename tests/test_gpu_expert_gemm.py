@@ -119,6 +119,23 @@ def test_any_tiling_serves_any_segments(pairs):
     check_forward(c, counts)
 
 
+@pytest.mark.parametrize("n,wi,wo", [(1, 1024, 128), (3, 1040, 136), (33, 2064, 264), (64, 7168, 128), (65, 1536, 512),
+                                     (119, 4096, 200)])
+def test_tiles_shared_by_a_cluster(n, wi, wo):
+    """Few rows and few tiles: each CTA of a cluster takes a share of K."""
+    c = forward_case([n], 16, wi, wo, n + wi)
+    assert run_forward(c) == 0
+    check_forward(c, [n])
+
+
+def test_a_shared_tile_for_each_of_too_many_tiles():
+    """More tiles than the pair count promised: each cluster takes several, one after the other."""
+    counts = [100, 0, 130, 257, 1]
+    c = forward_case(counts, 8, 2048, 4096, 5, pairs=1)
+    assert run_forward(c) == 0
+    check_forward(c, counts)
+
+
 def test_many_experts():
     g = np.random.default_rng(5)
     counts = [int(v) for v in g.integers(0, 4, 1024)]
@@ -345,9 +362,9 @@ def test_refusals():
     assert e.value.status == 6
 
 
-@pytest.mark.parametrize("counts", [[20, 9], [600, 300]], ids=["one_cta", "pair"])
-def test_a_wait_that_runs_out_is_reported(counts):
-    c = forward_case(counts, 16, 256, 256, 2)
+@pytest.mark.parametrize("counts,wi", [([20, 9], 256), ([600, 300], 256), ([20], 2048)], ids=["one_cta", "pair", "shared_tile"])
+def test_a_wait_that_runs_out_is_reported(counts, wi):
+    c = forward_case(counts, 16, wi, 256, 2)
     try:
         binding.debug_set_waits(limit_ns=2_000_000, extra_tx=16)
         assert run_forward(c) == 5
