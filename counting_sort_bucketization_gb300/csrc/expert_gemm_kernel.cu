@@ -69,8 +69,7 @@ constexpr int kBatchCols = 32;                     // columns of one tensor-memo
 constexpr int kSlotWords = 128 + kPRows;           // scales of columns or rows, then (kWgrad) of rows
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 128;                      // columns of an accumulator
-constexpr int kOutPitch = 80;                      // bytes; 64 of data, conflict-free for stmatrix
-constexpr int kOutBytes = 16 * kOutPitch;          // a warp's 16 rows x 32 columns of bf16
+constexpr int kOutBytes = 64 * 64;                 // a warp's 64 rows x 32 columns of bf16
 
 template <Kind KIND>
 struct Config {
@@ -84,7 +83,7 @@ struct Config {
   static constexpr int kWarpCols = kAccCols / kSplit;
   static constexpr int kEpilogueWarps = 4 * kAccs * kSplit;
   static constexpr int kThreads = 128 + 32 * kEpilogueWarps;
-  static constexpr int kStages = KIND == kMany ? 6 : 5;        // what the staging of out leaves room for
+  static constexpr int kStages = KIND == kMany ? 6 : KIND == kFew ? 5 : 4;   // what the staging of out leaves room for
   // Registers a thread: sums, and values of tensor memory.
   static constexpr int kLaunchRegs = KIND == kFew ? 168 : 96;
   static constexpr int kEpilogueRegs = KIND == kFew ? 224 : 104, kOtherRegs = KIND == kFew ? 56 : 64;
@@ -259,52 +258,51 @@ __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t
                                               uint8_t* stage, const uint64_t (*acc)[16]) {
   using C = Config<KIND>;
   const int n = (acc_id == 0 ? t.n[0] : t.n[1]) - part * C::kWarpCols;
-  const int first = (acc_id == 0 ? 0 : t.n[0]) + part * C::kWarpCols;
+  const int row = (acc_id == 0 ? 0 : t.n[0]) + part * C::kWarpCols;   // of the tile
   const int col0 = t.p0 + quarter * 32;                     // the warp's first column of out
-  const int64_t row0 = (KIND == kWgrad ? static_cast<int64_t>(t.expert) * p.dy_rows : 0) + t.q0;
+  const int64_t row0 = (KIND == kWgrad ? static_cast<int64_t>(t.expert) * p.dy_rows : 0) + t.q0 + row;
+  const int rows = min(n, t.q_valid - row);
+  if (KIND == kWgrad && p.out_fp32) {
+    // 4 rows x 8 columns a store: whole 32-byte sectors
 #pragma unroll
-  for (int c = 0; c < C::kWarpCols / kBatchCols; ++c) {
-    if (c * kBatchCols >= n) break;
-    const int row = first + c * kBatchCols;
-    if (KIND == kWgrad && p.out_fp32) {
-      // 4 rows x 8 columns a store: whole 32-byte sectors
+    for (int c = 0; c < C::kWarpCols / kBatchCols; ++c)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int oc = col0 + 16 * (i / 8) + 8 * (i % 2) + lane / 4, at = row + 8 * (i / 2 % 4) + 2 * (lane % 4);
+        const int oc = col0 + 16 * (i / 8) + 8 * (i % 2) + lane / 4, at = c * kBatchCols + 8 * (i / 2 % 4) + 2 * (lane % 4);
         const float2 f = tc::unpack2(acc[c][i]);
         if (oc < p.out_cols) {
           float* o = static_cast<float*>(p.out) + (row0 + at) * p.out_cols + oc;
-          if (at < t.q_valid) o[0] = p.accumulate ? o[0] + f.x : f.x;
-          if (at + 1 < t.q_valid) o[p.out_cols] = p.accumulate ? o[p.out_cols] + f.y : f.y;
+          if (at < rows) o[0] = p.accumulate ? o[0] + f.x : f.x;
+          if (at + 1 < rows) o[p.out_cols] = p.accumulate ? o[p.out_cols] + f.y : f.y;
         }
       }
-      continue;
-    }
-    const int oc = col0 + (lane % 4) * 8;
+    return;
+  }
+  // All of the warp's rows through shared memory at once: 64 bytes a row, its 16-byte
+  // pieces swapped by the row so that stmatrix meets no bank twice.
+  __syncwarp();   // the last tile's rows are read
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {                  // 16 columns: rows of out
+  for (int c = 0; c < C::kWarpCols / kBatchCols; ++c)
 #pragma unroll
-      for (int h = 2 * half; h < 2 * half + 2; ++h) {
-        uint32_t v[4];
+    for (int h = 0; h < 4; ++h) {
+      uint32_t v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = tc::unpack2(acc[c][8 * (i / 2) + 2 * h + i % 2]);
-          v[i] = pack_bf16(f.x, f.y);
-        }
-        // four matrices of 8 columns of out, transposed to 8 rows of 64 bytes
-        tc::stmatrix_x4_trans(ptx::smem_addr(stage) + (8 * (h % 2) + lane % 8) * kOutPitch + (lane / 8) * 16, v[0], v[1], v[2],
-                              v[3]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = tc::unpack2(acc[c][8 * (i / 2) + 2 * h + i % 2]);
+        v[i] = pack_bf16(f.x, f.y);
       }
-      __syncwarp();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 8 * h + lane / 4, at = row + 16 * half + r;
-        const uint4 w = ptx::ld_shared_v4(stage + r * kOutPitch + (lane % 4) * 16);
-        if (at < t.q_valid && oc < p.out_cols)
-          ptx::st_v4(static_cast<uint16_t*>(p.out) + (row0 + at) * p.out_cols + oc, w);
-      }
-      __syncwarp();
+      // four matrices of 8 columns of out, transposed to 8 rows of 64 bytes
+      const int r = c * kBatchCols + 8 * h + lane % 8, piece = (lane / 8) ^ (r / 2 % 4);
+      tc::stmatrix_x4_trans(ptx::smem_addr(stage) + r * 64 + piece * 16, v[0], v[1], v[2], v[3]);
     }
+  __syncwarp();
+  const int oc = col0 + (lane % 4) * 8;
+  uint16_t* out = static_cast<uint16_t*>(p.out) + row0 * p.out_cols + oc;
+#pragma unroll
+  for (int h = 0; h < C::kWarpCols / 8; ++h) {
+    const int r = 8 * h + lane / 4;
+    const uint4 w = ptx::ld_shared_v4(stage + r * 64 + ((lane % 4) ^ (r / 2 % 4)) * 16);
+    if (r < rows && oc < p.out_cols) ptx::st_v4(out + static_cast<int64_t>(r) * p.out_cols, w);
   }
 }
 
