@@ -428,6 +428,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         const int expert = uniform(tile.expert), p0 = uniform(tile.p0), kblocks = uniform(tile.kblocks);
         const int p_plane = KIND == kFew ? expert : 0, q_plane = KIND == kMany ? expert : 0;
         int x = uniform(tile.k0);
+#pragma unroll 1
         for (int kb = 0; kb < kblocks; ++kb, x += kKBlock) {
           if (!(ok = wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns))) break;
           if (tc::elect_one()) {
@@ -464,6 +465,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
           const Tile tile = get_tile<KIND>(p, s, t, rank, split);
           const int kblocks = uniform(tile.kblocks), n = uniform(h == 0 ? tile.n[0] : tile.n[1]);
           const uint32_t idesc = tc::instr_desc(kPRows * CTAS, n);
+#pragma unroll 1
           for (int kb = 0; kb < kblocks; ++kb) {
             const bool in = ptx::mbar_try_wait_parity(&s.full[ring.i], ring.phase);
             const bool free = ptx::mbar_try_wait_parity(&s.acc_empty[h][buf.i], buf.phase ^ 1);
@@ -590,6 +592,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       for (int c = 0; c < kBatches; ++c)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[c][i] = 0;
+#pragma unroll 1
       for (int kb = 0; kb < kblocks; ++kb) {
         if (!(ok = wait_warp(&s.acc_full[half][buf.i], buf.phase, p.wait_ns))) break;
         tc::fence_after();
