@@ -1,8 +1,9 @@
 // gate_kernels.cu -- the top-k gate of a mixture-of-experts layer with its
 // balance loss, and the gradient of both with respect to the logits.
 //
-// One warp owns a token; lane j holds the columns j, j+32, ... in registers,
-// so a row is read once and every reduction over experts is a warp reduction.
+// One warp owns a token; lane j holds the columns j, j+32, ... in registers (or
+// 4j..4j+3, 4j+128.., where rows can be read four values at a time), so a row is
+// read once and every reduction over experts is a warp reduction.
 //
 //   key_e = l_e + bias_e (one fp32 addition), as integers that sort like the
 //   floats.  The K-th largest of the lanes' own maxima bounds the K-th largest key
@@ -83,13 +84,50 @@ __device__ __forceinline__ float exp_fast(float x) {
 }
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + exp_fast(-x)); }
 
-// One row's logits in registers: columns lane, lane + 32, ...; -inf past E.
-template <int VPL, typename T>
+// The column of a lane's i-th value.
+template <bool VEC>
+__device__ __forceinline__ int column(int lane, int i) {
+  return VEC ? (i / 4) * 128 + lane * 4 + i % 4 : lane + 32 * i;
+}
+
+__device__ __forceinline__ void load4(const float* p, float* l) {
+  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+  l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float* l) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+  l[0] = __uint_as_float(v.x << 16), l[1] = __uint_as_float(v.x & 0xffff0000u);
+  l[2] = __uint_as_float(v.y << 16), l[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) { *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void store4(uint16_t* p, const float* v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// One row's logits in registers; -inf past E (a multiple of 4 with VEC).
+template <int VPL, typename T, bool VEC>
 __device__ __forceinline__ void load_row(const T* row, bool live, int lane, int E, float* l) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int col = lane + 32 * i;
-    l[i] = live && col < E ? load_logit(row + col) : -INFINITY;
+  for (int i = 0; i < VPL; i += VEC ? 4 : 1) {
+    const int col = column<VEC>(lane, i);
+    if constexpr (VEC) {
+      l[i] = l[i + 1] = l[i + 2] = l[i + 3] = -INFINITY;
+      if (live && col < E) load4(row + col, l + i);
+    } else {
+      l[i] = live && col < E ? load_logit(row + col) : -INFINITY;
+    }
+  }
+}
+template <int VPL, typename T, bool VEC>
+__device__ __forceinline__ void store_row(T* row, int lane, int E, const float* v) {
+#pragma unroll
+  for (int i = 0; i < VPL; i += VEC ? 4 : 1) {
+    const int col = column<VEC>(lane, i);
+    if (col < E) {
+      if constexpr (VEC) store4(row + col, v + i);
+      else store_logit(row + col, v[i]);
+    }
   }
 }
 
@@ -115,7 +153,7 @@ __device__ __forceinline__ float row_max(const float* l) {
   return unsortable(__reduce_max_sync(kFull, sortable(m)));
 }
 
-template <int VPL, typename T, bool SIGMOID>
+template <int VPL, typename T, bool SIGMOID, bool VEC>
 __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2) gate_forward_kernel(GateArgs a) {
   extern __shared__ uint8_t smem[];
   const int E = a.num_experts, K = a.topk;
@@ -146,19 +184,19 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
   int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
   int routed = 0;
   float next[VPL];
-  load_row<VPL, T>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
+  load_row<VPL, T, VEC>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
   for (; t < a.num_tokens; t += stride) {
     const T* row = logits + t * a.logits_stride;
     float l[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) l[i] = next[i];
-    load_row<VPL, T>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
+    load_row<VPL, T, VEC>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
 
     unsigned u[VPL], best = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       // the addition turns -0 into +0 (they tie) and any NaN into the one that sorts above +inf
-      const float key = l[i] + (biased ? bias_s[lane + 32 * i] : 0.0f);
+      const float key = l[i] + (biased ? bias_s[column<VEC>(lane, i)] : 0.0f);
       u[i] = sortable(key);
       best = max(best, u[i]);
     }
@@ -190,7 +228,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
         if (u[i] >= floor) {
           const int at = found + __popc(who & ptx::lanemask_lt());
           if (at < 32) {
-            list[at] = static_cast<uint64_t>(u[i]) << 32 | ~static_cast<unsigned>(lane + 32 * i);
+            list[at] = static_cast<uint64_t>(u[i]) << 32 | ~static_cast<unsigned>(column<VEC>(lane, i));
             if (biased) list_l[at] = l[i];
           }
         }
@@ -212,7 +250,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
           unsigned lowest = kFull;
 #pragma unroll
           for (int i = VPL - 1; i >= 0; --i)
-            if (u[i] == top) lowest = static_cast<unsigned>(lane + 32 * i);
+            if (u[i] == top) lowest = static_cast<unsigned>(column<VEC>(lane, i));
           const unsigned id = __reduce_min_sync(kFull, lowest);
           if (lane == k) {
             mine = static_cast<int>(id);
@@ -221,7 +259,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
           best = 0;
 #pragma unroll
           for (int i = 0; i < VPL; ++i) {
-            if (lane + 32 * i == static_cast<int>(id)) u[i] = 0;
+            if (column<VEC>(lane, i) == static_cast<int>(id)) u[i] = 0;
             best = max(best, u[i]);
           }
           top = __reduce_max_sync(kFull, best);
@@ -253,7 +291,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
     if (w == warp) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const int col = lane + 32 * i;
+        const int col = column<VEC>(lane, i);
         if (col < E) sum_s[col] += acc[i];
       }
     }
@@ -318,7 +356,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
 // not normalised).  softmax: dl = p (ds - c) with c = sum p ds, of which the
 // balance part is zero; sigmoid: dl = s (1 - s) ds.  The picked columns are
 // written by lane k after the row, over the value the row store left there.
-template <int VPL, typename T, bool SIGMOID>
+template <int VPL, typename T, bool SIGMOID, bool VEC>
 __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2) gate_backward_kernel(GateArgs a) {
   const int E = a.num_experts, K = a.topk;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -329,14 +367,14 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
                                               (static_cast<float>(K) * routed * routed) : 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int col = lane + 32 * i;
+    const int col = column<VEC>(lane, i);
     g[i] = col < E ? coef * static_cast<float>(a.expert_count[col]) : 0.0f;
   }
   const T* logits = static_cast<const T*>(a.logits);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
   float next[VPL];
-  load_row<VPL, T>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
+  load_row<VPL, T, VEC>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
   // the token's picks and their gradients, also a token ahead
   const auto load_pick = [&](int64_t tok, int64_t* id, float* d) {
     const bool in = lane < K && tok < a.num_tokens;
@@ -352,7 +390,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
     float l[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) l[i] = next[i];
-    load_row<VPL, T>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
+    load_row<VPL, T, VEC>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
     int64_t mine = next_id;
     float dw = next_dw;
     load_pick(t + stride, &next_id, &next_dw);
@@ -361,9 +399,8 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
       set_error(a.err, MOE_ERR_BAD_EXPERT_ID);
     }
     if (!__any_sync(kFull, mine >= 0)) {   // routed nowhere: no gradient
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < E) store_logit(out + lane + 32 * i, 0.0f);
+      const float zero[VPL] = {};
+      store_row<VPL, T, VEC>(out, lane, E, zero);
       continue;
     }
     const float m = SIGMOID ? 0.0f : row_max<VPL>(l);
@@ -389,12 +426,10 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
     }
     const float c = SIGMOID ? 0.0f : warp_sum(mine >= 0 ? s * ds : 0.0f);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int col = lane + 32 * i;
+    for (int i = 0; i < VPL; ++i)
       // softmax: sum(s) is 1, so (g - A) is the balance part of ds
-      const float d = SIGMOID ? l[i] * (1.0f - l[i]) * ((g[i] - A) * inv) : l[i] * inv * ((g[i] - A) - c);
-      if (col < E) store_logit(out + col, d);
-    }
+      l[i] = SIGMOID ? l[i] * (1.0f - l[i]) * ((g[i] - A) * inv) : l[i] * inv * ((g[i] - A) - c);
+    store_row<VPL, T, VEC>(out, lane, E, l);
     __syncwarp();
     if (mine >= 0) {
       const float gk = coef * static_cast<float>(a.expert_count[mine]);
@@ -416,10 +451,16 @@ cudaError_t launch_gate(const GateArgs& a, bool backward, cudaStream_t stream) {
     const int64_t grid = max64(1, min64(ceil_div64(a.num_tokens, kGateWarps), most));
     return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kGateThreads, smem, stream, a);
   };
-#define MOE_GATE_CASE(V) \
-  if (vpl <= V) return backward ? run(gate_backward_kernel<V, T, SIGMOID>) : run(gate_forward_kernel<V, T, SIGMOID>);
-  MOE_GATE_CASE(1)
-  MOE_GATE_CASE(2)
+  // Four values at a time where every row starts on a vector's boundary.
+  const uintptr_t vec = 4 * sizeof(T);
+  const bool wide = a.num_experts % 4 == 0 && a.logits_stride % 4 == 0 && aligned(a.logits, vec) &&
+                    (!backward || (a.dlogits_stride % 4 == 0 && aligned(a.dlogits, vec)));
+#define MOE_GATE_CASE(V)                                                                            \
+  if (vpl <= V)                                                                                     \
+    return backward ? (wide ? run(gate_backward_kernel<V, T, SIGMOID, true>)                        \
+                            : run(gate_backward_kernel<V, T, SIGMOID, false>))                      \
+                    : (wide ? run(gate_forward_kernel<V, T, SIGMOID, true>)                         \
+                            : run(gate_forward_kernel<V, T, SIGMOID, false>));
   MOE_GATE_CASE(4)
   MOE_GATE_CASE(8)
   MOE_GATE_CASE(12)
