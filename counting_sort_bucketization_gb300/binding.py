@@ -440,10 +440,10 @@ def new_gate_workspace(desc, device="cuda") -> torch.Tensor:
     return torch.zeros(gate_workspace_bytes(desc), dtype=torch.uint8, device=device)
 
 
-def _gate_desc(cfg, logits) -> _CGateDesc:
+def _gate_desc(cfg, dtype) -> _CGateDesc:
     if cfg.score not in ("softmax", "sigmoid"):
         raise ValueError(f"unknown score {cfg.score!r}")
-    return _CGateDesc(int(logits.dtype == torch.bfloat16), int(cfg.score == "sigmoid"), int(bool(cfg.normalize)),
+    return _CGateDesc(int(dtype == torch.bfloat16), int(cfg.score == "sigmoid"), int(bool(cfg.normalize)),
                       float(cfg.scale), float(cfg.balance_coef))
 
 
@@ -453,11 +453,13 @@ def _matrix(t, name, rows, cols, dtypes):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous columns")
-    ld = t.stride(0) if rows > 1 else cols
+    if rows <= 1:
+        ld = cols
     if ld < cols:
         raise ValueError(f"{name}'s rows overlap")
     return t.data_ptr(), int(ld)
@@ -472,7 +474,7 @@ def gate_forward(desc, cfg, logits, topk_idx, weights, expert_count, prob_mean, 
     N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
     lp, ld = _matrix(logits, "logits", N, E, _LOGITS)
     st = load_library().moe_gate_forward(
-        ctypes.byref(_desc(desc)), ctypes.byref(_gate_desc(cfg, logits)), lp, ld,
+        ctypes.byref(_desc(desc)), ctypes.byref(_gate_desc(cfg, logits.dtype)), lp, ld,
         _dev(bias, "bias", torch.float32, E, allow_none=True), _dev(topk_idx, "topk_idx", torch.int64, N * K),
         _dev(weights, "weights", torch.float32, N * K), _dev(expert_count, "expert_count", torch.int32, E),
         _dev(prob_mean, "prob_mean", torch.float32, E), _dev(routed_tokens, "routed_tokens", torch.int32, 1),
@@ -488,7 +490,7 @@ def gate_backward(desc, cfg, logits, topk_idx, expert_count, routed_tokens, dlog
     lp, ld = _matrix(logits, "logits", N, E, _LOGITS)
     gp, gld = _matrix(dlogits, "dlogits", N, E, (logits.dtype,))
     st = load_library().moe_gate_backward(
-        ctypes.byref(_desc(desc)), ctypes.byref(_gate_desc(cfg, logits)), lp, ld,
+        ctypes.byref(_desc(desc)), ctypes.byref(_gate_desc(cfg, logits.dtype)), lp, ld,
         _dev(topk_idx, "topk_idx", torch.int64, N * K), _dev(expert_count, "expert_count", torch.int32, E),
         _dev(routed_tokens, "routed_tokens", torch.int32, 1),
         _dev(dweights, "dweights", torch.float32, N * K, allow_none=True),
@@ -714,7 +716,8 @@ class Gate:
 
     ``forward(logits)`` fills ``topk_idx`` [N, K] (int64, ready for ``Layout.build``), ``weights`` [N, K] (for
     ``Layout.combine``), ``expert_count`` [E], ``prob_mean`` [E], ``routed_tokens`` [1] and ``loss`` [1];
-    ``backward`` reads them and the same logits."""
+    ``backward`` reads them and the same logits.  The buffers are written in place: copy out what must
+    outlive the next call, and do not rebind them."""
 
     def __init__(self, desc, cfg: GateConfig = GateConfig(), device="cuda"):
         N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
@@ -726,10 +729,20 @@ class Gate:
         self.prob_mean = torch.empty(E, dtype=torch.float32, device=device)
         self.routed_tokens = torch.empty(1, dtype=torch.int32, device=device)
         self.loss = torch.empty(1, dtype=torch.float32, device=device)
+        # What every call passes of this object's own: a serving step's gate is host time.
+        self._shape = (N, E)
+        self._cdesc = ctypes.byref(_desc(desc))
+        self._cgate = {t: ctypes.byref(_gate_desc(cfg, t)) for t in _LOGITS}
+        self._own = tuple(t.data_ptr() for t in (self.topk_idx, self.weights, self.expert_count, self.prob_mean,
+                                                 self.routed_tokens, self.loss, self.workspace))
+        self._ws_bytes = self.workspace.numel()
 
     def forward(self, logits, bias=None, stream=None) -> "Gate":
-        gate_forward(self.desc, self.cfg, logits, self.topk_idx, self.weights, self.expert_count, self.prob_mean,
-                     self.routed_tokens, self.loss, self.workspace, bias, stream)
+        lp, ld = _matrix(logits, "logits", *self._shape, _LOGITS)
+        _check(load_library().moe_gate_forward(
+            self._cdesc, self._cgate[logits.dtype], lp, ld,
+            _dev(bias, "bias", torch.float32, self._shape[1], allow_none=True), *self._own, self._ws_bytes,
+            _stream(stream)), "moe_gate_forward")
         return self
 
     def backward(self, logits, dlogits, dweights=None, dloss=None, stream=None):
