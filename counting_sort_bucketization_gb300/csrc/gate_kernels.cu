@@ -22,6 +22,13 @@
 // The sums over tokens are kept in fp32 a lane and column while a warp walks
 // its tokens, then summed over warps, CTAs and last over the CTAs' partials in
 // a fixed order, so results do not change from run to run.
+//
+// 131072 x 384 fp32, top-8: forward 108 us (214 MB), backward 70 us (415 MB, 5.9
+// TB/s).  The backward pass is bound by HBM, the forward pass by the issue of its
+// ~675 instructions a token, most of them for the choice.  Listing the candidates
+// took it from 210 us, where each pick was a pass over all keys, to 131 us; the
+// cheaper exponential, rows four values at a time and the next row's loads a token
+// ahead did the rest.  64 x 256, top-8: 7 us, the launch and one reduction.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kLayoutThreads)
 }
 
 // The rank kernels stage their tile's ids and rank them inside each warp
-// before griddepcontrol.wait: the ids come from no kernel of this library, so
+// before griddepcontrol.wait: no kernel that releases its dependents early writes ids, so
 // that part runs while the kernel before them (the column scan, or the layout)
 // is still working, and only the reads of the counts wait for it.
 template <typename IdT>

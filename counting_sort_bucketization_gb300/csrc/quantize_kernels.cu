@@ -15,7 +15,11 @@
 // codes are zeros; 448 is e4m3's largest value.  The one rounding to 8 bits is
 // the purpose of the kernel; everything before it is fp32.
 //
-// All of them move a few bytes an element once and are bound by HBM.
+// All of them move a few bytes an element once and are bound by HBM (a copy
+// reaches 6.76 TB/s): rows of 32768 x 7168 in 113 us (6.3 TB/s), SwiGLU of
+// 34816 x (2 x 2048) in 57.5 us (6.2), its gradient on 10007 x (2 x 1936) in
+// 29.9 us (6.5), the columns of 32768 receive rows x 4096 in 72 us (5.8; the
+// barriers between the steps of a tile are what is left).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -75,14 +79,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // A half-warp owns one block of 128 columns (16 bytes of bf16 a lane); a CTA
 // of 8 warps covers 16 rows x 4 blocks.  Each half-warp takes the four blocks
 // of its row in turn with all loads issued first, so a lane has 4 (SWIGLU: 8)
-// 16-byte loads in flight, and the 16 rows of a CTA make 64-byte runs of a
-// column-major scale column.
+// 16-byte loads in flight (with 2 and 4 the same rows took 138 us, not 117), and
+// the 16 rows of a CTA make 64-byte runs of a column-major scale column.
 constexpr int kRowsThreads = 256;
 constexpr int kRowsPerCta = kRowsThreads / 16;
 constexpr int kBlocksPerLane = 4;
 
 template <bool SWIGLU>
-__global__ void __launch_bounds__(kRowsThreads) quantize_rows_kernel(QuantRowsArgs a) {
+__global__ void __launch_bounds__(kRowsThreads, SWIGLU ? 4 : 6) quantize_rows_kernel(QuantRowsArgs a) {
   ptx::grid_dependency_wait();
   const int64_t nb = (a.cols + kBlock - 1) / kBlock;
   const int64_t chunks = (nb + kBlocksPerLane - 1) / kBlocksPerLane;
@@ -143,7 +147,9 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_rows_kernel(QuantRowsAr
 // side by side with the next tile's rows on their way.  A thread holds 4
 // consecutive rows x 8 columns, so its codes of a column make one 32-bit word
 // of the transposed tile; words go through shared memory at a pitch of 33 and
-// leave as 128-byte runs of a transposed row.
+// leave as 128-byte runs of a transposed row.  (Five CTAs an SM: 76 us where four
+// take 83 and three 87.  A warp a tile of 16 columns, without barriers, took 115: its
+// 32-byte pieces of rows cost more than the barriers.)
 constexpr int kColsThreads = 256;
 constexpr int kTileCols = 64;
 constexpr int kColTiles = 4;
@@ -156,7 +162,7 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-__global__ void __launch_bounds__(kColsThreads, 4) quantize_cols_kernel(QuantColsArgs a) {
+__global__ void __launch_bounds__(kColsThreads, 5) quantize_cols_kernel(QuantColsArgs a) {
   __shared__ uint32_t tile[kTileCols * kPitch];
   __shared__ uint32_t wmax[kColsThreads / 32][kTileCols / 2];
   __shared__ float inv_s[kTileCols];

@@ -38,8 +38,9 @@
  *    them start reading their inputs topk_idx, x and sf before the kernel in
  *    front of them on the stream has finished: the dispatch permutes prefetch
  *    token rows, the rank kernels stage ids.  This is safe after copies, after
- *    this library's own kernels (none of which writes those inputs) and after
- *    any kernel that does not release its dependents early.  The kernel
+ *    this library's own kernels (the gate and the quantisers, which write those
+ *    inputs, do not release their dependents early) and after any other
+ *    kernel that does not release its dependents early.  The kernel
  *    launched on the stream directly before one of these calls must not write
  *    the call's topk_idx, x or sf and also release its dependents before it
  *    ends (griddepcontrol.launch_dependents /
