@@ -114,7 +114,7 @@ struct Shared {
 template <Kind KIND>
 struct Smem {
   alignas(1024) uint8_t stage[Config<KIND>::kStages][kStageBytes];
-  alignas(16) uint8_t out[KIND == kMany ? 16 : Config<KIND>::kEpilogueWarps * kOutBytes];
+  alignas(1024) uint8_t out[KIND == kMany ? 16 : Config<KIND>::kEpilogueWarps * kOutBytes];
   Shared s;
 };
 // The dynamic base is only known to be 16-byte aligned: room to align it.
@@ -262,7 +262,7 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const Tile& t, i
 // columns 32 * c + 8 * h + 2 * (lane % 4), +1 of its accumulator columns.
 template <Kind KIND>
 __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t, int quarter, int acc_id, int part, int lane,
-                                              uint8_t* stage, const uint64_t (*acc)[16]) {
+                                              uint8_t* stage, const CUtensorMap* map_out, const uint64_t (*acc)[16]) {
   using C = Config<KIND>;
   const int n = (acc_id == 0 ? t.n[0] : t.n[1]) - part * C::kWarpCols;
   const int row = (acc_id == 0 ? 0 : t.n[0]) + part * C::kWarpCols;   // of the tile
@@ -286,7 +286,9 @@ __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t
     return;
   }
   // All of the warp's rows through shared memory at once: 64 bytes a row, its 16-byte
-  // pieces swapped by the row so that stmatrix meets no bank twice.
+  // pieces swapped by the row so that stmatrix meets no bank twice (as the tensor map of
+  // out has them).
+  if (KIND == kWgrad && lane == 0) ptx::bulk_wait_read<0>();
   __syncwarp();   // the last tile's rows are read
 #pragma unroll
   for (int c = 0; c < C::kWarpCols / kBatchCols; ++c)
@@ -302,6 +304,20 @@ __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t
       const int r = c * kBatchCols + 8 * h + lane % 8, piece = (lane / 8) ^ (r / 2 % 4);
       tc::stmatrix_x4_trans(ptx::smem_addr(stage) + r * 64 + piece * 16, v[0], v[1], v[2], v[3]);
     }
+  if (KIND == kWgrad) {
+    // Boxes of 32 rows, which the next tile's k-blocks do not wait for.  A tile's rows end
+    // at a multiple of 32 or with the matrix, whose edges the tensor map clips.
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+#pragma unroll
+      for (int c = 0; c < C::kWarpCols / kBatchCols; ++c)
+        if (c * kBatchCols < rows && col0 < p.out_cols)
+          tc::store_box(map_out, col0, t.q0 + row + c * kBatchCols, t.expert, ptx::smem_addr(stage) + c * kBatchCols * 64);
+      ptx::bulk_commit();
+    }
+    return;
+  }
   __syncwarp();
   const int oc = col0 + (lane % 4) * 8;
   uint16_t* out = static_cast<uint16_t*>(p.out) + row0 * p.out_cols + oc;
@@ -330,7 +346,7 @@ __device__ __forceinline__ void zero_gap(const GemmParams& p, const Shared& s, c
 template <Kind KIND>
 __global__ void __launch_bounds__(Config<KIND>::kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-                   const __grid_constant__ CUtensorMap map_q16, const GemmParams p) {
+                   const __grid_constant__ CUtensorMap map_c /* kFew: Q in boxes of 16 rows; kWgrad: out */, const GemmParams p) {
   using C = Config<KIND>;
   constexpr int CTAS = C::kCtas, NBUF = C::kBuffers, ACCS = C::kAccs, kStages = C::kStages, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
@@ -344,7 +360,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
   if (threadIdx.x == 0) {
     tc::prefetch_map(&map_p);
     tc::prefetch_map(&map_q);
-    if (KIND == kFew) tc::prefetch_map(&map_q16);
+    if (KIND == kFew) tc::prefetch_map(&map_c);
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
       ptx::mbar_init(&s.empty[i], ACCS);           // a commit of each MMA warp
@@ -444,7 +460,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             if (leader) ptx::mbar_arrive_expect_tx(&s.full[ring.i], bytes + (loads == 0 ? p.extra_tx : 0));
             if (CTAS == 2) bar = tc::map_to_rank(bar, 0);
             tc::load_box<CTAS>(dst, &map_p, x, p0, p_plane, bar);
-            if (small) tc::load_box<CTAS>(dst + kPBytes, &map_q16, x, q0, q_plane, bar);
+            if (small) tc::load_box<CTAS>(dst + kPBytes, &map_c, x, q0, q_plane, bar);
             else tc::load_box<CTAS>(dst + kPBytes, &map_q, x, q0, q_plane, bar);
             if (two) tc::load_box<CTAS>(dst + kPBytes + 64 * kKBlock, &map_q, x, q1, q_plane, bar);
           }
@@ -717,9 +733,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 
       const Tile tile = get_tile<KIND>(p, s, t, rank, split);
       if constexpr (KIND == kMany) store_rows(p, tile, quarter * 32 + lane, half * kAccCols + part * C::kWarpCols, acc);
-      else store_columns<KIND>(p, tile, quarter, half, part, lane, mem.out + ew * kOutBytes, acc);
+      else store_columns<KIND>(p, tile, quarter, half, part, lane, mem.out + ew * kOutBytes, &map_c, acc);
       if (KIND != kWgrad && tile.last) zero_gap<KIND>(p, s, tile, rank, ew, lane);
     }
+    if (KIND == kWgrad && lane == 0) ptx::bulk_wait<0>();
   }
 
   if (!ok) set_error(p.err, MOE_ERR_TIMEOUT);
@@ -750,23 +767,27 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Bytes [planes, rows, width] with boxes of box_rows x 128 bytes, 128-byte swizzle;
-// what lies outside reads as zero.
-cudaError_t encode(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int64_t planes, int box_rows) {
+// [planes, rows, width] with boxes of box_rows x 128 bytes (operands, 128-byte swizzle)
+// or of 32 rows x 32 bf16 (the weight gradient, 64-byte swizzle); what lies outside reads
+// as zero and is not written.
+cudaError_t encode(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int64_t planes, int box_rows,
+                   bool out = false) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
+  const int64_t pitch = out ? 2 * width : width;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(width * rows)};
-  const cuuint32_t box[3] = {kKBlock, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(pitch * rows)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(out ? kBatchCols : kKBlock), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t unit[3] = {1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, unit,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = fn(m, out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base),
+                        dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <Kind KIND>
-cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const CUtensorMap& map_q16, const GemmParams& p,
+cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const CUtensorMap& map_c, const GemmParams& p,
                    cudaStream_t stream) {
   const int cluster = Config<KIND>::kCtas * p.splits;
   const auto kernel = expert_gemm_kernel<KIND>;
@@ -787,7 +808,7 @@ cudaError_t launch(const CUtensorMap& map_p, const CUtensorMap& map_q, const CUt
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, kernel, map_p, map_q, map_q16, p);
+  return cudaLaunchKernelEx(&cfg, kernel, map_p, map_q, map_c, p);
 }
 
 GemmParams common_params(const ExpertGemmArgs& a) {
@@ -841,10 +862,11 @@ cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
   p.col_sf = a.x_sf;
   p.out_cols = static_cast<int>(a.width_in);
   p.dy_rows = static_cast<int>(a.width_out);
-  CUtensorMap x, dy;
+  CUtensorMap x, dy, out;
   cudaError_t e = encode(&x, a.x, a.sf_ld, a.width_in, 1, kPRows);
   if (e == cudaSuccess) e = encode(&dy, a.w, a.sf_ld, a.width_out, 1, 64);
-  return e == cudaSuccess ? launch<kWgrad>(x, dy, dy, p, stream) : e;
+  if (e == cudaSuccess && !a.out_fp32) e = encode(&out, a.out, a.width_in, a.width_out, a.num_experts, kBatchCols, true);
+  return e == cudaSuccess ? launch<kWgrad>(x, dy, a.out_fp32 ? dy : out, p, stream) : e;
 }
 
 }  // namespace moe

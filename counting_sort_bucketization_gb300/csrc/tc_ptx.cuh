@@ -103,6 +103,13 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, int
   }
 }
 
+// A 3-D box from this CTA's shared memory, in the thread's bulk group.
+__device__ __forceinline__ void store_box(const CUtensorMap* m, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x), "r"(y),
+               "r"(z), "r"(src)
+               : "memory");
+}
+
 // ------------------------------------------------------------- tensor memory
 template <int CTAS>
 __device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t cols) {
