@@ -267,22 +267,33 @@ __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t
   const int n = (acc_id == 0 ? t.n[0] : t.n[1]) - part * C::kWarpCols;
   const int row = (acc_id == 0 ? 0 : t.n[0]) + part * C::kWarpCols;   // of the tile
   const int col0 = t.p0 + quarter * 32;                     // the warp's first column of out
-  const int64_t row0 = (KIND == kWgrad ? static_cast<int64_t>(t.expert) * p.dy_rows : 0) + t.q0 + row;
   const int rows = min(n, t.q_valid - row);
   if (KIND == kWgrad && p.out_fp32) {
-    // 4 rows x 8 columns a store: whole 32-byte sectors
+    // A block of 32 x 32 at a time, 128 bytes a row, pieces swapped as the tensor map has
+    // them: a store meets no bank twice.
 #pragma unroll
-    for (int c = 0; c < C::kWarpCols / kBatchCols; ++c)
+    for (int c = 0; c < C::kWarpCols / kBatchCols; ++c) {
+      if (lane == 0) ptx::bulk_wait_read<0>();
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int oc = col0 + 16 * (i / 8) + 8 * (i % 2) + lane / 4, at = c * kBatchCols + 8 * (i / 2 % 4) + 2 * (lane % 4);
+        const int at = 8 * (i / 2 % 4) + 2 * (lane % 4), piece = 4 * (i / 8) + 2 * (i % 2) + lane / 16;
         const float2 f = tc::unpack2(acc[c][i]);
-        if (oc < p.out_cols) {
-          float* o = static_cast<float*>(p.out) + (row0 + at) * p.out_cols + oc;
-          if (at < rows) o[0] = p.accumulate ? o[0] + f.x : f.x;
-          if (at + 1 < rows) o[p.out_cols] = p.accumulate ? o[p.out_cols] + f.y : f.y;
-        }
+        float* to = reinterpret_cast<float*>(stage + at * 128) + lane / 4 % 4;
+        to[(piece ^ at % 8) * 4] = f.x;
+        to[32 + (piece ^ (at + 1) % 8) * 4] = f.y;
       }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (c * kBatchCols < rows && col0 < p.out_cols) {
+          const uint32_t from = ptx::smem_addr(stage);
+          if (p.accumulate) tc::add_box(map_out, col0, t.q0 + row + c * kBatchCols, t.expert, from);
+          else tc::store_box(map_out, col0, t.q0 + row + c * kBatchCols, t.expert, from);
+        }
+        ptx::bulk_commit();
+      }
+    }
     return;
   }
   // All of the warp's rows through shared memory at once: 64 bytes a row, its 16-byte
@@ -320,7 +331,7 @@ __device__ __forceinline__ void store_columns(const GemmParams& p, const Tile& t
   }
   __syncwarp();
   const int oc = col0 + (lane % 4) * 8;
-  uint16_t* out = static_cast<uint16_t*>(p.out) + row0 * p.out_cols + oc;
+  uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(t.q0 + row) * p.out_cols + oc;
 #pragma unroll
   for (int h = 0; h < C::kWarpCols / 8; ++h) {
     const int r = 8 * h + lane / 4;
@@ -767,22 +778,24 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// [planes, rows, width] with boxes of box_rows x 128 bytes (operands, 128-byte swizzle)
-// or of 32 rows x 32 bf16 (the weight gradient, 64-byte swizzle); what lies outside reads
-// as zero and is not written.
+// [planes, rows, width] of 1 (operands), 2 or 4 bytes (bf16 or fp32 results), with boxes
+// of box_rows x 128 values of an operand or 32 of a result; what lies outside reads as zero
+// and is not written.
 cudaError_t encode(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int64_t planes, int box_rows,
-                   bool out = false) {
+                   int bytes = 1) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
-  const int64_t pitch = out ? 2 * width : width;
+  const int64_t pitch = bytes * width;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(pitch * rows)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(out ? kBatchCols : kKBlock), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(bytes == 1 ? kKBlock : kBatchCols), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t unit[3] = {1, 1, 1};
-  const CUresult r = fn(m, out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base),
-                        dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUtensorMapDataType type = bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const CUresult r = fn(m, type, 3, const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -865,8 +878,8 @@ cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
   CUtensorMap x, dy, out;
   cudaError_t e = encode(&x, a.x, a.sf_ld, a.width_in, 1, kPRows);
   if (e == cudaSuccess) e = encode(&dy, a.w, a.sf_ld, a.width_out, 1, 64);
-  if (e == cudaSuccess && !a.out_fp32) e = encode(&out, a.out, a.width_in, a.width_out, a.num_experts, kBatchCols, true);
-  return e == cudaSuccess ? launch<kWgrad>(x, dy, a.out_fp32 ? dy : out, p, stream) : e;
+  if (e == cudaSuccess) e = encode(&out, a.out, a.width_in, a.width_out, a.num_experts, kBatchCols, a.out_fp32 ? 4 : 2);
+  return e == cudaSuccess ? launch<kWgrad>(x, dy, out, p, stream) : e;
 }
 
 }  // namespace moe

@@ -110,6 +110,13 @@ __device__ __forceinline__ void store_box(const CUtensorMap* m, int x, int y, in
                : "memory");
 }
 
+// The same, added to the fp32 values that are there (subnormal ones may count as zeros).
+__device__ __forceinline__ void add_box(const CUtensorMap* m, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+
 // ------------------------------------------------------------- tensor memory
 template <int CTAS>
 __device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t cols) {
