@@ -35,6 +35,10 @@
 //  - Issuing an MMA takes ~53 cycles whatever its size, so each accumulator has an
 //    MMA warp: 377 -> 367 us.  Loop bounds and tile numbers of the issuing warps are kept in
 //    uniform registers; from ordinary ones every operand is moved over one by one.
+//  - Rows of out leave by tensor-map stores from a block of 32 x 32 a warp, so the tile
+//    after does not wait for 152 SMs that write at once: 380 -> 367 us (16 k-blocks: 222
+//    -> 205), with one stage of operands less (6 -> 5; 4, and room for two blocks: 375).
+//    kWgrad, whose tiles have few k-blocks, 390 -> 316 us.
 //  - The epilogue is bound by its chain of latencies (wait, load, add), so kMany has 16
 //    warps of 64 columns, 412 -> 386 us; 32 columns of tensor memory in flight,
 //    386 -> 375 us.
@@ -76,7 +80,8 @@ constexpr int kBatchCols = 32;                     // columns of one tensor-memo
 constexpr int kSlotWords = 128 + kPRows;           // scales of columns or rows, then (kWgrad) of rows
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 128;                      // columns of an accumulator
-constexpr int kOutBytes = 64 * 64;                 // a warp's 64 rows x 32 columns of bf16
+constexpr int kOutBytes = 64 * 64;                 // a warp's 64 rows x 32 columns of bf16 (kFew, kWgrad)
+constexpr int kRowsBytes = 32 * 64;                // 32 x 32 (kMany)
 
 template <Kind KIND>
 struct Config {
@@ -90,7 +95,7 @@ struct Config {
   static constexpr int kWarpCols = kAccCols / kSplit;
   static constexpr int kEpilogueWarps = 4 * kAccs * kSplit;
   static constexpr int kThreads = 128 + 32 * kEpilogueWarps;
-  static constexpr int kStages = KIND == kMany ? 6 : KIND == kFew ? 5 : 4;   // what the staging of out leaves room for
+  static constexpr int kStages = KIND == kMany ? 5 : KIND == kFew ? 5 : 4;   // what the staging of out leaves room for
   // Registers a thread: sums, and values of tensor memory.
   static constexpr int kLaunchRegs = KIND == kFew ? 168 : 96;
   static constexpr int kEpilogueRegs = KIND == kFew ? 224 : 104, kOtherRegs = KIND == kFew ? 56 : 64;
@@ -114,7 +119,7 @@ struct Shared {
 template <Kind KIND>
 struct Smem {
   alignas(1024) uint8_t stage[Config<KIND>::kStages][kStageBytes];
-  alignas(1024) uint8_t out[KIND == kMany ? 16 : Config<KIND>::kEpilogueWarps * kOutBytes];
+  alignas(1024) uint8_t out[Config<KIND>::kEpilogueWarps * (KIND == kMany ? kRowsBytes : kOutBytes)];
   Shared s;
 };
 // The dynamic base is only known to be 16-byte aligned: room to align it.
@@ -214,7 +219,7 @@ struct Ring {
 // bounds built on it then stay there.  (From ordinary registers each MMA or TMA
 // operand is moved over one by one, and issuing takes longer than the MMAs.)
 __device__ __forceinline__ int uniform(int v) {
-  return static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(v)));
+  return __reduce_max_sync(0xffffffffu, v);
 }
 
 // The whole warp waits, and leaves together (tcgen05.ld needs all lanes).
@@ -227,34 +232,48 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Rows of out from sums whose thread owns a row (kMany).
-// acc[c][i]: column 32 c + 2 i, +1 after column `col` of the tile.
-__device__ __forceinline__ void store_rows(const GemmParams& p, const Tile& t, int row, int col, const uint64_t (*acc)[16]) {
+// Rows of out from sums whose thread owns a row (kMany): row `quarter` * 32 + lane of
+// the tile, acc[c][i] column 32 c + 2 i, +1 after its column `col`.
+__device__ __forceinline__ void store_rows(const GemmParams& p, const Tile& t, int quarter, int lane, int col, uint8_t* stage,
+                                           const CUtensorMap* map_out, const uint64_t (*acc)[16]) {
   using C = Config<kMany>;
-  const int oc = t.q0 + col;
-  if (row >= t.p_valid || oc >= p.out_cols) return;
-  uint16_t* out = static_cast<uint16_t*>(p.out) + (static_cast<int64_t>(t.p0) + row) * p.out_cols + oc;
-  const int cols = p.out_cols - oc;
-  // 32-byte stores where rows allow: 16-byte ones write each sector in halves
-  const bool wide = p.out_cols % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
+  const int oc = t.q0 + col, row = t.p0 + quarter * 32;
+  const int rows = t.p_valid - quarter * 32, cols = p.out_cols - oc;
+  const bool whole = rows >= 32;   // else a box would reach into the next segment
 #pragma unroll
-  for (int c = 0; c < C::kWarpCols / kBatchCols; ++c)
+  for (int c = 0; c < C::kWarpCols / kBatchCols; ++c) {
+    const int at = c * kBatchCols;
+    uint4 v[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t v[8];
+    for (int h = 0; h < 4; ++h) {
+      uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 f = tc::unpack2(acc[c][8 * h + i]);
-        v[i] = pack_bf16(f.x, f.y);
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = tc::unpack2(acc[c][4 * h + i]);
+        w[i] = pack_bf16(f.x, f.y);
       }
-      const int at = 32 * c + 16 * h;
-      if (wide) {
-        if (at < cols) tc::st_v8(out + at, v);
-      } else {
-        if (at < cols) ptx::st_v4(out + at, make_uint4(v[0], v[1], v[2], v[3]));
-        if (at + 8 < cols) ptx::st_v4(out + at + 8, make_uint4(v[4], v[5], v[6], v[7]));
-      }
+      v[h] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    if (whole) {
+      // A block of 32 x 32, which the next tile's k-blocks do not wait for: 64 bytes a
+      // row, its pieces swapped as the tensor map has them.
+      if (lane == 0) ptx::bulk_wait_read<0>();
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 4; ++h) *reinterpret_cast<uint4*>(stage + lane * 64 + (h ^ lane / 2 % 4) * 16) = v[h];
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (at < cols) tc::store_box(map_out, oc + at, row, 0, ptx::smem_addr(stage));
+        ptx::bulk_commit();
+      }
+    } else if (lane < rows) {
+      uint16_t* out = static_cast<uint16_t*>(p.out) + (static_cast<int64_t>(row) + lane) * p.out_cols + oc;
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        if (at + 8 * h < cols) ptx::st_v4(out + at + 8 * h, v[h]);
+    }
+  }
 }
 
 // Rows of out from sums whose columns are rows of out (kFew, kWgrad).
@@ -357,7 +376,7 @@ __device__ __forceinline__ void zero_gap(const GemmParams& p, const Shared& s, c
 template <Kind KIND>
 __global__ void __launch_bounds__(Config<KIND>::kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-                   const __grid_constant__ CUtensorMap map_c /* kFew: Q in boxes of 16 rows; kWgrad: out */, const GemmParams p) {
+                   const __grid_constant__ CUtensorMap map_c /* kFew: Q in boxes of 16 rows; else out */, const GemmParams p) {
   using C = Config<KIND>;
   constexpr int CTAS = C::kCtas, NBUF = C::kBuffers, ACCS = C::kAccs, kStages = C::kStages, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
@@ -604,7 +623,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of one accumulator.
     tc::reg_inc<C::kEpilogueRegs>();
     constexpr int kBatches = C::kWarpCols / kBatchCols;
-    const int ew = warp - 4, quarter = warp % 4, half = ew / (4 * C::kSplit), part = ew / 4 % C::kSplit;   // half: the accumulator
+    const int uw = uniform(warp);
+    const int ew = uw - 4, quarter = uw % 4, half = ew / (4 * C::kSplit), part = ew / 4 % C::kSplit;   // half: the accumulator
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kAccCols + part * C::kWarpCols;
     uint32_t freed = ptx::smem_addr(&s.acc_empty[half][0]);   // the leader's barriers
     if (CTAS == 2) freed = tc::map_to_rank(freed, 0);
@@ -620,6 +640,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         const Tile tile = get_tile<KIND>(p, s, t, rank, split);
         n = (half == 0 ? tile.n[0] : tile.n[1]) - part * C::kWarpCols;
         kblocks = tile.kblocks;
+        // kWgrad, 8 experts x 1024 rows: 304 -> 280 us (no spills).  kMany is slower so.
+        if (KIND == kWgrad) n = uniform(n), kblocks = uniform(kblocks);
       }
       uint64_t acc[kBatches][16];                             // pairs of sums: see store_rows, store_columns
 #pragma unroll
@@ -743,11 +765,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       if (split > 0) continue;
 
       const Tile tile = get_tile<KIND>(p, s, t, rank, split);
-      if constexpr (KIND == kMany) store_rows(p, tile, quarter * 32 + lane, half * kAccCols + part * C::kWarpCols, acc);
+      if constexpr (KIND == kMany) store_rows(p, tile, quarter, lane, half * kAccCols + part * C::kWarpCols,
+                                                mem.out + ew * kRowsBytes, &map_c, acc);
       else store_columns<KIND>(p, tile, quarter, half, part, lane, mem.out + ew * kOutBytes, &map_c, acc);
       if (KIND != kWgrad && tile.last) zero_gap<KIND>(p, s, tile, rank, ew, lane);
     }
-    if (KIND == kWgrad && lane == 0) ptx::bulk_wait<0>();
+    if (KIND != kFew && lane == 0) ptx::bulk_wait<0>();
   }
 
   if (!ok) set_error(p.err, MOE_ERR_TIMEOUT);
@@ -860,12 +883,13 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream) {
     const int64_t tiles = (min64(a.num_experts, max64(a.pairs, 1)) + a.pairs / 128) * ceil_div64(a.width_out, kPRows);
     while (p.splits < 8 && 2 * p.splits * tiles <= device_sm_count() && 8 * p.splits <= p.kblocks) p.splits *= 2;
   }
-  CUtensorMap rows, rows16, weights;
+  CUtensorMap rows, third, weights;
   cudaError_t e = encode(&rows, a.x, a.width_in, a.capacity, 1, many ? kPRows : 64);
-  if (e == cudaSuccess) e = encode(&rows16, a.x, a.width_in, a.capacity, 1, 16);
+  if (e == cudaSuccess)
+    e = many ? encode(&third, a.out, a.width_out, a.capacity, 1, kBatchCols, 2) : encode(&third, a.x, a.width_in, a.capacity, 1, 16);
   if (e == cudaSuccess) e = encode(&weights, a.w, a.width_in, a.width_out, a.num_experts, many ? 64 : kPRows);
   if (e != cudaSuccess) return e;
-  return many ? launch<kMany>(rows, weights, weights, p, stream) : launch<kFew>(weights, rows, rows16, p, stream);
+  return many ? launch<kMany>(rows, weights, third, p, stream) : launch<kFew>(weights, rows, third, p, stream);
 }
 
 cudaError_t launch_expert_wgrad(const ExpertGemmArgs& a, cudaStream_t stream) {
