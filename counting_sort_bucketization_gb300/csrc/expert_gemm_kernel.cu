@@ -38,7 +38,11 @@
 //  - Rows of out leave by tensor-map stores from a block of 32 x 32 a warp, so the tile
 //    after does not wait for 152 SMs that write at once: 380 -> 367 us (16 k-blocks: 222
 //    -> 205), with one stage of operands less (6 -> 5; 4, and room for two blocks: 375).
-//    kWgrad, whose tiles have few k-blocks, 390 -> 316 us.
+//    kWgrad, whose tiles have few k-blocks, 390 -> 316 us (8 experts of 1024 rows,
+//    4096 x 7168, bf16), and 280 when its loop's bounds stay in uniform registers too.
+//    Rows of dw along lanes would read tensor memory at 1.2 cycles, but came to 295.
+//  - Scales come two k-blocks ahead: 363 us, 425 with one; kWgrad 280, 294 with one, and
+//    302 with three, which spill.
 //  - The epilogue is bound by its chain of latencies (wait, load, add), so kMany has 16
 //    warps of 64 columns, 412 -> 386 us; 32 columns of tensor memory in flight,
 //    386 -> 375 us.
@@ -874,8 +878,8 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream) {
   p.kblocks = static_cast<int>(ceil_div64(a.width_in, kKBlock));
   // kFew's tile holds 128 rows of an expert, kMany's 256.  Up to a mean of 112 rows
   // (nearly all experts in one tile) kFew measured faster, from 128 on kMany: 32 experts,
-  // 7168 -> 4096, 112 rows 187 against 218 us, 128 rows 224 against 217, 256 rows 349
-  // against 283; 2048 -> 7168 the same.
+  // 7168 -> 4096, 64 rows 183 against 203 us, 112 rows 187 against 210, 128 rows 226
+  // against 214; 2048 -> 7168, 112 rows 109 against 115, 128 rows 132 against 119.
   const int64_t mean = a.pairs / a.num_experts;
   const bool many = mean >= 120;
   if (!many) {
