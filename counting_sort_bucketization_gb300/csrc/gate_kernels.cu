@@ -468,6 +468,14 @@ cudaError_t launch_gate(const GateArgs& a, bool backward, cudaStream_t stream) {
                             : run(gate_backward_kernel<V, T, SIGMOID, false>))                      \
                     : (wide ? run(gate_forward_kernel<V, T, SIGMOID, true>)                         \
                             : run(gate_forward_kernel<V, T, SIGMOID, false>));
+  // Up to 64 columns a lane has one or two of its own.
+#define MOE_GATE_NARROW(V)                                               \
+  if (vpl <= V)                                                          \
+    return backward ? run(gate_backward_kernel<V, T, SIGMOID, false>)    \
+                    : run(gate_forward_kernel<V, T, SIGMOID, false>);
+  MOE_GATE_NARROW(1)
+  MOE_GATE_NARROW(2)
+#undef MOE_GATE_NARROW
   MOE_GATE_CASE(4)
   MOE_GATE_CASE(8)
   MOE_GATE_CASE(12)
