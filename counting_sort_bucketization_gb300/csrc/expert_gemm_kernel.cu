@@ -50,11 +50,12 @@
 //    the 16x256-bit one in 2.0; kFew and kWgrad take the latter for its pairs of columns.
 //
 // What it comes to, of twice the bf16 rate that a library product reaches (3781
-// TFLOP/s): 256 experts of 1024 rows, 7168 -> 4096, kMany 6.55 ms (2349 TFLOP/s, 62 %;
-// the epilogue's adds to fp32 sums are what is left, the tensor core waits for them).
-// 16 tokens to top-8 of 256 experts, kFew 0.48 ms (6.3 TB/s of 6.76).  32 experts of
-// 1024 rows, 4096 x 7168, kWgrad 1.59 ms (1207 TFLOP/s: two scales a value and k-block,
-// 1.9 GB of results).
+// TFLOP/s): 16 experts of 1024 rows, 7168 -> 4096, kMany 363 us (2649 TFLOP/s, 70 %; the
+// epilogue's adds to fp32 sums are what is left, the tensor core waits for them); 256
+// experts 5.58 ms after idle (2757), 6.4-6.6 ms one call after the other, when the power
+// cap holds the SMs at 1.47-1.51 GHz of 2.07.  16 tokens to top-8 of 256 experts, kFew
+// 0.47 ms (6.4 TB/s of 6.76).  32 experts of 1024 rows, 4096 x 7168, kWgrad 1.18 ms (1632
+// TFLOP/s: two scales a value and k-block, 1.9 GB of results).
 //
 // One persistent CTA (or pair) per SM walks the tiles of all experts.  All sums
 // are fp32; the result is rounded once.
