@@ -1,5 +1,5 @@
 // tc_ptx.cuh -- inline-PTX wrappers of the fifth-generation tensor core path:
-// tensor memory, tcgen05.mma / commit / ld, tiled TMA loads, clusters, packed
+// tensor memory, tcgen05.mma / commit / ld, tiled TMA loads and stores, clusters, packed
 // fp32 arithmetic and register reallocation.
 #pragma once
 
@@ -235,13 +235,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
                "r"(c), "r"(d)
-               : "memory");
-}
-
-// 32-byte store; p 32-byte aligned.
-__device__ __forceinline__ void st_v8(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 
