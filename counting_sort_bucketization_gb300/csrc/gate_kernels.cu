@@ -26,9 +26,8 @@
 // 131072 x 384 fp32, top-8: forward 108 us (214 MB), backward 70 us (415 MB, 5.9
 // TB/s).  The backward pass is bound by HBM, the forward pass by the issue of its
 // ~675 instructions a token, most of them for the choice.  Listing the candidates
-// took it from 210 us, where each pick was a pass over all keys, to 131 us; the
-// cheaper exponential, rows four values at a time and the next row's loads a token
-// ahead did the rest.  64 x 256, top-8: 7 us, the launch and one reduction.
+// took it from 210 us, where each pick was a pass over all keys, to 131 us; rows four
+// values at a time and the next row's loads a token ahead did the rest.  64 x 256, top-8: 7 us, the launch and one reduction.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -81,15 +80,22 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// e^x as 2^(x log2 e): the product's rounding adds 2^-24 |x| to the result's relative
-// error, which leaves scores good to 2^-18 down to e^-32 of the largest.  Results
-// below 2^-126 are zero.
-__device__ __forceinline__ float exp_fast(float x) {
+// e^x for x <= 0 (-inf too): 2^t with t = x log2 e rounded, times e^(x - t ln 2), whose
+// exponent is at most 2^-24 |x| and enters to first order.  (Without it the product's
+// rounding errs by 2^-24 |x| of the result; expf takes 131072 x 384 from 178 to 193 us in
+// both directions, this to 188.)  ln 2 as one float is good to 2^-28, so what is left is 2^-28 |x|
+// and the approximation's 2^-22.  Results below 2^-126 are zero.
+__device__ __forceinline__ float exp_neg(float x) {
+  x = fmaxf(x, -128.0f);
+  const float t = x * 1.4426950408889634f;
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
-  return r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return fmaf(r, fmaf(-t, 0.6931471805599453f, x), r);
 }
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + exp_fast(-x)); }
+__device__ __forceinline__ float sigmoid(float x) {
+  const float e = exp_neg(-fabsf(x)), r = __fdividef(1.0f, 1.0f + e);
+  return x >= 0.0f ? r : e * r;
+}
 
 // The column of a lane's i-th value.
 template <bool VEC>
@@ -145,8 +151,8 @@ __device__ __forceinline__ float scores(float* l, float m) {
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    // exp(-inf) = 0, and sigmoid(-inf) = 1 / (1 + inf) = 0: closed experts score nothing
-    l[i] = SIGMOID ? sigmoid_fast(l[i]) : exp_fast(l[i] - m);
+    // exp(-inf) = 0, and sigmoid(-inf) = 0 / (1 + 0): closed experts score nothing
+    l[i] = SIGMOID ? sigmoid(l[i]) : exp_neg(l[i] - m);
     s += l[i];
   }
   return fmaxf(warp_sum(s), kTiny);
@@ -280,7 +286,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
       ++routed;
       float s = 0.0f;
       if (mine >= 0) {
-        s = SIGMOID ? sigmoid_fast(picked) : exp_fast(picked - m) * inv;
+        s = SIGMOID ? sigmoid(picked) : exp_neg(picked - m) * inv;
         atomicAdd(&cnt_s[mine], 1);
       }
       const float den = a.normalize ? fmaxf(warp_sum(s), kTiny) : 1.0f;
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
     float s = 0.0f;
     if (mine >= 0) {
       const float lk = load_logit(row + mine);
-      s = SIGMOID ? sigmoid_fast(lk) : exp_fast(lk - m) * inv;
+      s = SIGMOID ? sigmoid(lk) : exp_neg(lk - m) * inv;
     } else {
       dw = 0.0f;
     }
