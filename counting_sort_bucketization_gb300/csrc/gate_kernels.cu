@@ -45,7 +45,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
 constexpr int kGateMaxVpl = 32;              // columns of a lane: MOE_MAX_EXPERTS / 32
-constexpr float kTiny = 1e-30f;              // floor of a sum of scores that divides
+constexpr float kTinySum = 0x1p-30f;         // sums of sigmoids below it are taken of e^(l - max) instead
 constexpr unsigned kKeyNegInf = 0x007fffffu; // sortable keys of -inf and +inf
 constexpr unsigned kKeyInf = 0xff800000u;
 
@@ -82,9 +82,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // e^x for x <= 0 (-inf too): 2^t with t = x log2 e rounded, times e^(x - t ln 2), whose
 // exponent is at most 2^-24 |x| and enters to first order.  (Without it the product's
-// rounding errs by 2^-24 |x| of the result; expf takes 131072 x 384 from 178 to 193 us in
-// both directions, this to 188.)  ln 2 as one float is good to 2^-28, so what is left is 2^-28 |x|
-// and the approximation's 2^-22.  Results below 2^-126 are zero.
+// rounding errs by 2^-24 |x| of the result; expf takes 5 us more on 131072 x 384, both
+// directions.)  ln 2 as one float is good to 2^-28, so what is left is 2^-28 |x| and the
+// approximation's 2^-22.  Results below 2^-126 are zero.
 __device__ __forceinline__ float exp_neg(float x) {
   x = fmaxf(x, -128.0f);
   const float t = x * 1.4426950408889634f;
@@ -144,10 +144,20 @@ __device__ __forceinline__ void store_row(T* row, int lane, int E, const float* 
   }
 }
 
-// Scores of a row in place of its logits; returns their sum (floored).  `m` is
-// the row's largest logit (finite).
-template <int VPL, bool SIGMOID>
-__device__ __forceinline__ float scores(float* l, float m) {
+template <int VPL>
+__device__ __forceinline__ float row_max(const float* l) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+  return unsortable(__reduce_max_sync(kFull, sortable(m)));
+}
+
+// Scores of a routed row in place of its logits, up to a common factor; returns their
+// sum.  `m` is the row's largest logit (softmax).  Sigmoids whose sum is below 2^-30 are
+// e^l to 2^-30 each: e^(l - max) stand in their place, which neither vanish nor lose
+// bits, and `tiny` says so, with the largest logit in `m`.
+template <int VPL, typename T, bool SIGMOID, bool VEC>
+__device__ __forceinline__ float scores(float* l, float& m, bool& tiny, const T* row, int lane, int E) {
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -155,15 +165,32 @@ __device__ __forceinline__ float scores(float* l, float m) {
     l[i] = SIGMOID ? sigmoid(l[i]) : exp_neg(l[i] - m);
     s += l[i];
   }
-  return fmaxf(warp_sum(s), kTiny);
+  s = warp_sum(s);
+  tiny = SIGMOID && s < kTinySum;
+  if (tiny) {
+    load_row<VPL, T, VEC>(row, true, lane, E, l);
+    m = row_max<VPL>(l);
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s += l[i] = exp_neg(l[i] - m);
+    s = warp_sum(s);
+  }
+  return s;
 }
 
-template <int VPL>
-__device__ __forceinline__ float row_max(const float* l) {
-  float m = l[0];
-#pragma unroll
-  for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
-  return unsortable(__reduce_max_sync(kFull, sortable(m)));
+// A pick's share of the picks' scores, of which `top` is the largest's logit (softmax).
+// Each is taken relative to that one's, however small beside the row's; sigmoids only
+// where their sum is tiny.
+template <bool SIGMOID>
+__device__ __forceinline__ float share_of_picks(bool pick, float l, float score, float top) {
+  float v = SIGMOID ? score : pick ? exp_neg(l - top) : 0.0f;
+  float sum = warp_sum(v);
+  if (SIGMOID && sum < kTinySum) {
+    top = unsortable(__reduce_max_sync(kFull, pick ? sortable(l) : 0u));
+    v = pick ? exp_neg(l - top) : 0.0f;
+    sum = warp_sum(v);
+  }
+  return __fdividef(v, sum);
 }
 
 template <int VPL, typename T, bool SIGMOID, bool VEC>
@@ -220,7 +247,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
     float w = 0.0f;
     if (route) {
       // without a bias the largest key is the largest logit
-      const float m = SIGMOID ? 0.0f : !biased ? unsortable(top) : row_max<VPL>(l);
+      float m = SIGMOID ? 0.0f : !biased ? unsortable(top) : row_max<VPL>(l);
 
       // The K-th largest lane maximum (equal ones go together: a lower bound still).
       unsigned floor = top;
@@ -279,18 +306,21 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
         }
       }
       __syncwarp();   // the list is read
-      const float total = scores<VPL, SIGMOID>(l, m);
-      const float inv = __fdividef(1.0f, total);
+      bool tiny;
+      const float inv = __fdividef(1.0f, scores<VPL, T, SIGMOID, VEC>(l, m, tiny, row, lane, E));
 #pragma unroll
       for (int i = 0; i < VPL; ++i) acc[i] += l[i] * inv;
       ++routed;
+      const bool pick = mine >= 0;
+      if (pick) atomicAdd(&cnt_s[mine], 1);
       float s = 0.0f;
-      if (mine >= 0) {
-        s = SIGMOID ? sigmoid(picked) : exp_neg(picked - m) * inv;
-        atomicAdd(&cnt_s[mine], 1);
+      if (pick && (SIGMOID || !a.normalize)) s = SIGMOID ? sigmoid(picked) : exp_neg(picked - m) * inv;
+      if (a.normalize) {
+        // without a bias the largest pick is the largest logit
+        const float top_pick = SIGMOID || !biased ? m : unsortable(__reduce_max_sync(kFull, pick ? sortable(picked) : 0u));
+        s = share_of_picks<SIGMOID>(pick, picked, s, top_pick);
       }
-      const float den = a.normalize ? fmaxf(warp_sum(s), kTiny) : 1.0f;
-      w = __fdividef(a.scale * s, den);
+      w = a.scale * s;
     }
     if (slot < K) {
       a.topk_idx[t * K + slot] = mine;
@@ -363,11 +393,12 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
   }
 }
 
-// Gradient.  With g_e = dloss * coef * E * f_e / routed and A = sum_e q_e g_e,
-// the score's gradient is (g_e - A) / sum(s) plus, for a picked expert,
-// scale / D * (dw_k - sum_j dw_j s_j / D) (without the inner sum if weights are
-// not normalised).  softmax: dl = p (ds - c) with c = sum p ds, of which the
-// balance part is zero; sigmoid: dl = s (1 - s) ds.  The picked columns are
+// Gradient.  With g_e = dloss * coef * E * f_e / routed and A = sum_e q_e g_e, the
+// balance loss gives log s_e the gradient q_e (g_e - A).  The weights give that of a pick
+//   d_k = scale * r_k * (dw_k - sum_j r_j dw_j), r_k = s_k / D   (normalised)
+//   d_k = scale * s_k * dw_k                                     (not),
+// and d log s_e / d l_j is (e == j) - p_j for softmax, where only the second d has a sum
+// c over the picks, and (1 - s_e) on the diagonal for sigmoid.  The picked columns are
 // written by lane k after the row, over the value the row store left there.
 template <int VPL, typename T, bool SIGMOID, bool VEC>
 __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2) gate_backward_kernel(GateArgs a) {
@@ -416,38 +447,41 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
       store_row<VPL, T, VEC>(out, lane, E, zero);
       continue;
     }
-    const float m = SIGMOID ? 0.0f : row_max<VPL>(l);
-    const float total = scores<VPL, SIGMOID>(l, m);
-    const float inv = __fdividef(1.0f, total);
+    float m = SIGMOID ? 0.0f : row_max<VPL>(l);
+    bool tiny;
+    const float inv = __fdividef(1.0f, scores<VPL, T, SIGMOID, VEC>(l, m, tiny, row, lane, E));
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) dot += l[i] * g[i];
     const float A = warp_sum(dot) * inv;
 
-    float s = 0.0f;
-    if (mine >= 0) {
-      const float lk = load_logit(row + mine);
-      s = SIGMOID ? sigmoid(lk) : exp_neg(lk - m) * inv;
-    } else {
-      dw = 0.0f;
+    const bool pick = mine >= 0;
+    const float lk = pick ? load_logit(row + mine) : 0.0f;
+    if (!pick) dw = 0.0f;
+    float q = 0.0f, s = 0.0f;              // the pick's share of the row, and its score
+    if (pick) {
+      if (!SIGMOID || tiny) q = exp_neg(lk - m) * inv;
+      s = SIGMOID ? sigmoid(lk) : q;
+      if (SIGMOID && !tiny) q = s * inv;
     }
-    float ds = a.scale * dw;
+    float d;                               // of the weights, with respect to the logarithm of the pick's score
+    float c = 0.0f;
     if (a.normalize) {
-      const float den = fmaxf(warp_sum(s), kTiny);
-      const float mean = warp_sum(s * dw) / den;
-      ds = a.scale / den * (dw - mean);
+      const float top = SIGMOID ? 0.0f : unsortable(__reduce_max_sync(kFull, pick ? sortable(lk) : 0u));
+      const float share = share_of_picks<SIGMOID>(pick, lk, s, top);
+      d = a.scale * share * (dw - warp_sum(share * dw));
+    } else {
+      d = a.scale * s * dw;
+      if (!SIGMOID) c = warp_sum(d);
     }
-    const float c = SIGMOID ? 0.0f : warp_sum(mine >= 0 ? s * ds : 0.0f);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      // softmax: sum(s) is 1, so (g - A) is the balance part of ds
-      l[i] = SIGMOID ? l[i] * (1.0f - l[i]) * ((g[i] - A) * inv) : l[i] * inv * ((g[i] - A) - c);
+      l[i] = SIGMOID ? l[i] * (tiny ? 1.0f : 1.0f - l[i]) * ((g[i] - A) * inv) : l[i] * inv * ((g[i] - A) - c);
     store_row<VPL, T, VEC>(out, lane, E, l);
     __syncwarp();
-    if (mine >= 0) {
+    if (pick) {
       const float gk = coef * static_cast<float>(a.expert_count[mine]);
-      const float d = SIGMOID ? s * (1.0f - s) * ((gk - A) * inv + ds) : s * ((gk - A) - c + ds);
-      store_logit(out + mine, d);
+      store_logit(out + mine, SIGMOID ? (1.0f - s) * (q * (gk - A) + d) : q * ((gk - A) - c) + d);
     }
   }
 }
