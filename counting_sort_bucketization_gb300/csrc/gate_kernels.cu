@@ -92,9 +92,17 @@ __device__ __forceinline__ float exp_neg(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
   return fmaf(r, fmaf(-t, 0.6931471805599453f, x), r);
 }
+// sigmoid(|x|) and sigmoid(-|x|).  The smaller is not taken as a difference from one, which
+// would have no bits left from 17 on.
+__device__ __forceinline__ void sigmoids(float x, float& large, float& small) {
+  const float e = exp_neg(-fabsf(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(large) : "f"(1.0f + e));   // of 1 to 2: 1 ulp
+  small = e * large;
+}
 __device__ __forceinline__ float sigmoid(float x) {
-  const float e = exp_neg(-fabsf(x)), r = __fdividef(1.0f, 1.0f + e);
-  return x >= 0.0f ? r : e * r;
+  float large, small;
+  sigmoids(x, large, small);
+  return x >= 0.0f ? large : small;
 }
 
 // The column of a lane's i-th value.
@@ -155,26 +163,45 @@ __device__ __forceinline__ float row_max(const float* l) {
 // Scores of a routed row in place of its logits, up to a common factor; returns their
 // sum.  `m` is the row's largest logit (softmax).  Sigmoids whose sum is below 2^-30 are
 // e^l to 2^-30 each: e^(l - max) stand in their place, which neither vanish nor lose
-// bits, and `tiny` says so, with the largest logit in `m`.
+// bits, and `tiny` says so, with the largest logit in `m`.  With `g`, the scores' sum
+// weighted by it goes to `dot`, and a sigmoid's slope s (1 - s) in the score's place.
 template <int VPL, typename T, bool SIGMOID, bool VEC>
-__device__ __forceinline__ float scores(float* l, float& m, bool& tiny, const T* row, int lane, int E) {
-  float s = 0.0f;
+__device__ __forceinline__ float scores(float* l, float& m, bool& tiny, const T* row, int lane, int E,
+                                        const float* g = nullptr, float* dot = nullptr) {
+  float s = 0.0f, d = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     // exp(-inf) = 0, and sigmoid(-inf) = 0 / (1 + 0): closed experts score nothing
-    l[i] = SIGMOID ? sigmoid(l[i]) : exp_neg(l[i] - m);
-    s += l[i];
+    if (SIGMOID && g != nullptr) {
+      float large, small;
+      sigmoids(l[i], large, small);
+      const float score = l[i] >= 0.0f ? large : small;
+      s += score;
+      d += score * g[i];
+      l[i] = large * small;
+    } else {
+      l[i] = SIGMOID ? sigmoid(l[i]) : exp_neg(l[i] - m);
+      s += l[i];
+    }
   }
   s = warp_sum(s);
+  if (!SIGMOID && g != nullptr) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) d += l[i] * g[i];
+  }
   tiny = SIGMOID && s < kTinySum;
   if (tiny) {
     load_row<VPL, T, VEC>(row, true, lane, E, l);
     m = row_max<VPL>(l);
-    s = 0.0f;
+    s = d = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) s += l[i] = exp_neg(l[i] - m);
+    for (int i = 0; i < VPL; ++i) {
+      s += l[i] = exp_neg(l[i] - m);       // its own slope: 1 - s is 1
+      if (g != nullptr) d += l[i] * g[i];
+    }
     s = warp_sum(s);
   }
+  if (g != nullptr) *dot = warp_sum(d);
   return s;
 }
 
@@ -400,8 +427,11 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
 // and d log s_e / d l_j is (e == j) - p_j for softmax, where only the second d has a sum
 // c over the picks, and (1 - s_e) on the diagonal for sigmoid.  The picked columns are
 // written by lane k after the row, over the value the row store left there.
+//
+// Sigmoids take more registers: a CTA an SM fewer than softmax measured faster where more
+// spill (131072 x 256, 53 against 76 us; x 384, 71 against 87; 65536 x 1000, 104 against 113).
 template <int VPL, typename T, bool SIGMOID, bool VEC>
-__global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2) gate_backward_kernel(GateArgs a) {
+__global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? (SIGMOID ? 4 : 5) : VPL <= 12 ? (SIGMOID ? 3 : 4) : VPL <= 16 || !SIGMOID ? 2 : 1) gate_backward_kernel(GateArgs a) {
   const int E = a.num_experts, K = a.topk;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   ptx::grid_dependency_wait();
@@ -449,19 +479,24 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
     }
     float m = SIGMOID ? 0.0f : row_max<VPL>(l);
     bool tiny;
-    const float inv = __fdividef(1.0f, scores<VPL, T, SIGMOID, VEC>(l, m, tiny, row, lane, E));
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) dot += l[i] * g[i];
-    const float A = warp_sum(dot) * inv;
+    float dot;
+    const float inv = __fdividef(1.0f, scores<VPL, T, SIGMOID, VEC>(l, m, tiny, row, lane, E, g, &dot));
+    const float A = dot * inv;
 
     const bool pick = mine >= 0;
     const float lk = pick ? load_logit(row + mine) : 0.0f;
     if (!pick) dw = 0.0f;
-    float q = 0.0f, s = 0.0f;              // the pick's share of the row, and its score
+    float q = 0.0f, s = 0.0f, rest = 1.0f; // the pick's share of the row, its score, and what that lacks to 1
     if (pick) {
       if (!SIGMOID || tiny) q = exp_neg(lk - m) * inv;
-      s = SIGMOID ? sigmoid(lk) : q;
+      if (SIGMOID) {
+        float large, small;
+        sigmoids(lk, large, small);
+        s = lk >= 0.0f ? large : small;
+        rest = lk >= 0.0f ? small : large;
+      } else {
+        s = q;
+      }
       if (SIGMOID && !tiny) q = s * inv;
     }
     float d;                               // of the weights, with respect to the logarithm of the pick's score
@@ -476,12 +511,12 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 5 : VPL <= 12 ? 4 : 2
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      l[i] = SIGMOID ? l[i] * (tiny ? 1.0f : 1.0f - l[i]) * ((g[i] - A) * inv) : l[i] * inv * ((g[i] - A) - c);
+      l[i] = l[i] * inv * ((g[i] - A) - c);
     store_row<VPL, T, VEC>(out, lane, E, l);
     __syncwarp();
     if (pick) {
       const float gk = coef * static_cast<float>(a.expert_count[mine]);
-      store_logit(out + mine, SIGMOID ? (1.0f - s) * (q * (gk - A) + d) : q * ((gk - A) - c) + d);
+      store_logit(out + mine, SIGMOID ? rest * (q * (gk - A) + d) : q * ((gk - A) - c) + d);
     }
   }
 }

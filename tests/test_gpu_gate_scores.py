@@ -1,4 +1,4 @@
-"""Gate scores far from zero: rows whose scores are all tiny, exponents of large magnitude.
+"""Gate scores far from zero: rows whose scores are all tiny, exponents of large magnitude, saturated sigmoids.
 
 The plain side works with logarithms in 64 bits, so no score underflows there.
 
@@ -152,3 +152,13 @@ def test_softmax_scores_of_any_magnitude():
     l = grid(np.random.default_rng(4), 200, 32, lo=-70, hi=0)
     l[:, 7] = 0
     check_forward(l, None, 32, "softmax", False)
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("size", [8.0, 12.0, 16.0, 25.0, 60.0])
+def test_sigmoid_gradient_where_scores_are_close_to_one(size, normalize):
+    """1 - s is kept to full precision: s itself rounds to one from a logit of 17 on."""
+    rng = np.random.default_rng(int(size))
+    l = grid(rng, 21, 24, lo=size - 2, hi=size + 2)
+    l[rng.random(l.shape) < 0.4] *= -1
+    check(l, None, 4, "sigmoid", normalize)
