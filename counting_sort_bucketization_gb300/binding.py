@@ -717,25 +717,27 @@ class Gate:
     ``forward(logits)`` fills ``topk_idx`` [N, K] (int64, ready for ``Layout.build``), ``weights`` [N, K] (for
     ``Layout.combine``), ``expert_count`` [E], ``prob_mean`` [E], ``routed_tokens`` [1] and ``loss`` [1];
     ``backward`` reads them and the same logits.  The buffers are written in place: copy out what must
-    outlive the next call, and do not rebind them."""
+    outlive the next call.  The attributes cannot be rebound."""
 
     def __init__(self, desc, cfg: GateConfig = GateConfig(), device="cuda"):
         N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
         self.desc, self.cfg = desc, cfg
-        self.workspace = new_gate_workspace(desc, device)
-        self.topk_idx = torch.empty((N, K), dtype=torch.int64, device=device)
-        self.weights = torch.empty((N, K), dtype=torch.float32, device=device)
-        self.expert_count = torch.empty(E, dtype=torch.int32, device=device)
-        self.prob_mean = torch.empty(E, dtype=torch.float32, device=device)
-        self.routed_tokens = torch.empty(1, dtype=torch.int32, device=device)
-        self.loss = torch.empty(1, dtype=torch.float32, device=device)
+        # forward() passes the addresses of these tensors, which live as long as the object does
+        self._buffers = (torch.empty((N, K), dtype=torch.int64, device=device),
+                         torch.empty((N, K), dtype=torch.float32, device=device),
+                         torch.empty(E, dtype=torch.int32, device=device),
+                         torch.empty(E, dtype=torch.float32, device=device),
+                         torch.empty(1, dtype=torch.int32, device=device),
+                         torch.empty(1, dtype=torch.float32, device=device), new_gate_workspace(desc, device))
         # What every call passes of this object's own: a serving step's gate is host time.
         self._shape = (N, E)
         self._cdesc = ctypes.byref(_desc(desc))
         self._cgate = {t: ctypes.byref(_gate_desc(cfg, t)) for t in _LOGITS}
-        self._own = tuple(t.data_ptr() for t in (self.topk_idx, self.weights, self.expert_count, self.prob_mean,
-                                                 self.routed_tokens, self.loss, self.workspace))
+        self._own = tuple(t.data_ptr() for t in self._buffers)
         self._ws_bytes = self.workspace.numel()
+
+    topk_idx, weights, expert_count, prob_mean, routed_tokens, loss, workspace = (
+        property(lambda self, i=i: self._buffers[i]) for i in range(7))
 
     def forward(self, logits, bias=None, stream=None) -> "Gate":
         lp, ld = _matrix(logits, "logits", *self._shape, _LOGITS)
