@@ -717,11 +717,12 @@ class Gate:
     ``forward(logits)`` fills ``topk_idx`` [N, K] (int64, ready for ``Layout.build``), ``weights`` [N, K] (for
     ``Layout.combine``), ``expert_count`` [E], ``prob_mean`` [E], ``routed_tokens`` [1] and ``loss`` [1];
     ``backward`` reads them and the same logits.  The buffers are written in place: copy out what must
-    outlive the next call.  The attributes cannot be rebound."""
+    outlive the next call.  The attributes cannot be rebound; ``desc`` and ``cfg`` are taken as they are
+    when the object is made, for both directions (other settings take another object)."""
 
     def __init__(self, desc, cfg: GateConfig = GateConfig(), device="cuda"):
         N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
-        self.desc, self.cfg = desc, cfg
+        self._desc, self._cfg = desc, cfg
         # forward() passes the addresses of these tensors, which live as long as the object does
         self._buffers = (torch.empty((N, K), dtype=torch.int64, device=device),
                          torch.empty((N, K), dtype=torch.float32, device=device),
@@ -730,12 +731,13 @@ class Gate:
                          torch.empty(1, dtype=torch.int32, device=device),
                          torch.empty(1, dtype=torch.float32, device=device), new_gate_workspace(desc, device))
         # What every call passes of this object's own: a serving step's gate is host time.
-        self._shape = (N, E)
+        self._shape, self._topk = (N, E), (N, K)
         self._cdesc = ctypes.byref(_desc(desc))
         self._cgate = {t: ctypes.byref(_gate_desc(cfg, t)) for t in _LOGITS}
         self._own = tuple(t.data_ptr() for t in self._buffers)
         self._ws_bytes = self.workspace.numel()
 
+    desc, cfg = property(lambda self: self._desc), property(lambda self: self._cfg)
     topk_idx, weights, expert_count, prob_mean, routed_tokens, loss, workspace = (
         property(lambda self, i=i: self._buffers[i]) for i in range(7))
 
@@ -748,8 +750,15 @@ class Gate:
         return self
 
     def backward(self, logits, dlogits, dweights=None, dloss=None, stream=None):
-        gate_backward(self.desc, self.cfg, logits, self.topk_idx, self.expert_count, self.routed_tokens, dlogits,
-                      self.workspace, dweights, dloss, stream)
+        N, K = self._topk
+        idx, _, count, _, routed, _, ws = self._own
+        lp, ld = _matrix(logits, "logits", *self._shape, _LOGITS)
+        gp, gld = _matrix(dlogits, "dlogits", *self._shape, (logits.dtype,))
+        _check(load_library().moe_gate_backward(
+            self._cdesc, self._cgate[logits.dtype], lp, ld, idx, count, routed,
+            _dev(dweights, "dweights", torch.float32, N * K, allow_none=True),
+            _dev(dloss, "dloss", torch.float32, 1, allow_none=True), gp, gld, ws, self._ws_bytes, _stream(stream)),
+            "moe_gate_backward")
         return dlogits
 
     def error(self, stream=None) -> int:
