@@ -49,14 +49,9 @@ constexpr float kTinySum = 0x1p-30f;         // sums of sigmoids below it are ta
 constexpr unsigned kKeyNegInf = 0x007fffffu; // sortable keys of -inf and +inf
 constexpr unsigned kKeyInf = 0xff800000u;
 
-template <typename T>
-__device__ __forceinline__ float load_logit(const T* p);
-template <>
-__device__ __forceinline__ float load_logit<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) {
-  return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
-}
+// Ordinary loads: the gradient may be written over the logits.
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
+__device__ __forceinline__ float load_logit(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
 
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) {
@@ -112,11 +107,11 @@ __device__ __forceinline__ int column(int lane, int i) {
 }
 
 __device__ __forceinline__ void load4(const float* p, float* l) {
-  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 v = *reinterpret_cast<const float4*>(p);
   l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
 }
 __device__ __forceinline__ void load4(const uint16_t* p, float* l) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
   l[0] = __uint_as_float(v.x << 16), l[1] = __uint_as_float(v.x & 0xffff0000u);
   l[2] = __uint_as_float(v.y << 16), l[3] = __uint_as_float(v.y & 0xffff0000u);
 }
@@ -512,6 +507,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? (SIGMOID ? 4 : 5) : V
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       l[i] = l[i] * inv * ((g[i] - A) - c);
+    __syncwarp();   // every lane has its pick's logit, which may lie where another stores
     store_row<VPL, T, VEC>(out, lane, E, l);
     __syncwarp();
     if (pick) {

@@ -45,6 +45,18 @@ int gate_args(const moe_layout_desc* desc, const moe_gate_desc* gate, const void
   return MOE_OK;
 }
 
+// Whether the gradient's rows may lie on the logits' in a way that the kernel cannot
+// take: anything but the same rows or none.  (Ranges that interleave with unlike strides
+// count as overlapping.)
+bool rows_clash(const void* x, int64_t x_stride, const void* y, int64_t y_stride, int64_t rows, int64_t width) {
+  if (x == y && (x_stride == y_stride || rows <= 1)) return false;
+  const int64_t a = reinterpret_cast<int64_t>(x), b = reinterpret_cast<int64_t>(y);
+  if (a + (rows - 1) * x_stride + width <= b || b + (rows - 1) * y_stride + width <= a) return false;
+  if (x_stride != y_stride) return true;
+  const int64_t off = ((b - a) % x_stride + x_stride) % x_stride;   // of a row of y in a row of x
+  return off < width || off + width > x_stride;
+}
+
 // Row and column counts of the 8-bit row kernels.
 int check_rows(int64_t rows, int64_t cols, int64_t multiple) {
   if (rows < 0 || cols <= 0 || cols % multiple != 0) return MOE_ERR_INVALID_ARG;
@@ -98,6 +110,10 @@ int moe_gate_backward(const moe_layout_desc* desc, const moe_gate_desc* gate, co
   if (!aligned(topk_idx, 8) || !aligned(dweights, 4) || !aligned(dlogits, gate->logits_bf16 ? 2 : 4))
     return MOE_ERR_INVALID_ARG;
   if (dlogits_stride > MOE_MAX_ROW_BYTES / 4) return MOE_ERR_UNSUPPORTED;
+  const int64_t size = gate->logits_bf16 ? 2 : 4;
+  if (desc->num_tokens > 0 && rows_clash(logits, size * logits_stride, dlogits, size * dlogits_stride, desc->num_tokens,
+                                         size * desc->num_experts))
+    return MOE_ERR_INVALID_ARG;
   a.topk_idx = const_cast<int64_t*>(topk_idx);
   a.expert_count = const_cast<int32_t*>(expert_count);
   a.routed_tokens = const_cast<int32_t*>(routed_tokens);

@@ -407,6 +407,9 @@ MOE_API int moe_gate_forward(const moe_layout_desc* desc, const moe_gate_desc* g
  * dweights [N*K] and dloss [1] are fp32 and may each be NULL (zero).  The counts
  * and the choice of experts carry no gradient; the bias gets none.  dlogits
  * [N, dlogits_stride] has the logits' type; tokens that were not routed get 0.
+ * dlogits may be the logits themselves (same base and stride).  Otherwise no row of
+ * one may touch a row of the other (MOE_ERR_INVALID_ARG; ranges that interleave
+ * need equal strides).
  */
 MOE_API int moe_gate_backward(const moe_layout_desc* desc, const moe_gate_desc* gate, const void* logits,
                               int64_t logits_stride, const int64_t* topk_idx, const int32_t* expert_count,
