@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kColsThreads, 5) quantize_cols_kernel(QuantCol
   __shared__ uint32_t wmax[kColsThreads / 32][kTileCols / 2];
   __shared__ float inv_s[kTileCols];
   __shared__ int valid_s;
+  __shared__ bool off_grid_s;
   ptx::grid_dependency_wait();
   const int64_t chunks = (a.cols + kColTiles * kTileCols - 1) / (kColTiles * kTileCols);
   const int64_t rb = static_cast<int64_t>(blockIdx.x) / chunks;
@@ -187,10 +188,11 @@ __global__ void __launch_bounds__(kColsThreads, 5) quantize_cols_kernel(QuantCol
   load(c_first, next);
   // The expert whose segment holds row r0 says how many of the block's rows are real.
   const int total = a.expert_offset[a.num_experts];
-  if (threadIdx.x == 0) valid_s = 0;
+  if (threadIdx.x == 0) valid_s = 0, off_grid_s = false;
   __syncthreads();
   for (int e = threadIdx.x; e < a.num_experts; e += kColsThreads) {
     const int start = a.expert_offset[e];
+    if (start % kBlock != 0) off_grid_s = true;
     if (start <= r0 && r0 < a.expert_offset[e + 1])
       valid_s = static_cast<int>(max64(0, min64(kBlock, static_cast<int64_t>(start) + a.expert_count[e] - r0)));
   }
@@ -199,6 +201,10 @@ __global__ void __launch_bounds__(kColsThreads, 5) quantize_cols_kernel(QuantCol
     return;
   }
   __syncthreads();
+  if (off_grid_s) {   // a block could lie in two experts
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, MOE_ERR_INVALID_ARG);
+    return;
+  }
   const int valid = valid_s;
   for (int ct = 0; ct < kColTiles; ++ct) {
     const int64_t c0 = c_first + ct * kTileCols;

@@ -70,7 +70,9 @@ enum moe_status {
   MOE_OK = 0,
   MOE_ERR_INVALID_ARG = 1,   /* host check failed: null pointer, bad size or alignment;
                                 device (moe_dispatch_sf_col_major): map entry out of range;
-                                device (moe_gate_forward): a NaN or +inf logit       */
+                                device (moe_gate_forward): a NaN or +inf key;
+                                device (moe_quantize_cols, moe_expert_wgrad_fp8): a
+                                segment that starts inside a block of 128 rows       */
   MOE_ERR_CUDA = 2,          /* a CUDA launch or copy failed                           */
   MOE_ERR_BAD_EXPERT_ID = 3, /* device: some topk_idx entry was >= E                   */
   MOE_ERR_CAPACITY = 4,      /* device: the layout needs more rows than capacity_rows  */
@@ -453,7 +455,9 @@ MOE_API int moe_swiglu_backward(const void* gate_up, const void* dh, int64_t row
  *   ld >= capacity_rows rounded up to 128, a multiple of 128; sf
  *   [ceil(capacity_rows / 128), cols].  Rows in the alignment gaps count as
  *   zeros whatever they hold.  Row blocks past the last segment are not written.
- * desc->alignment must be a multiple of 128 (MOE_ERR_UNSUPPORTED otherwise).
+ * desc->alignment must be a multiple of 128 (MOE_ERR_UNSUPPORTED otherwise).  With a
+ * segment that does not start at a multiple of 128 nothing is written and
+ * MOE_ERR_INVALID_ARG is recorded in the workspace.
  */
 MOE_API int moe_quantize_cols(const moe_layout_desc* desc, const void* x, int64_t capacity_rows, int64_t cols,
                               const int32_t* expert_offset, const int32_t* expert_count, void* q, int64_t ld,
