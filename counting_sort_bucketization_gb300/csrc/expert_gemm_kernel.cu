@@ -431,6 +431,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
       s.seg_start[e] = count > 0 ? start : 0;
       s.seg_count[e] = count;
       tiles = row_tiles<KIND>(p, count) * across;
+      if (KIND == kWgrad && p.accumulate && count == 0) tiles = 0;   // nothing to add (8 experts of 4096 x 7168, half empty: 402 -> 218 us)
     }
     int sum = tiles;
 #pragma unroll

@@ -495,8 +495,9 @@ MOE_API int moe_expert_gemm_fp8(const moe_layout_desc* desc, const void* x, cons
  * them: dy [width_out, ld], dy_sf [ceil(capacity_rows/128), width_out],
  * x [width_in, ld], x_sf [ceil(capacity_rows/128), width_in].
  * dw is [E, width_out, width_in], bf16 (dw_fp32 == 0) or fp32; accumulate != 0
- * adds to what an fp32 dw holds.  width_in a multiple of 8.  desc->alignment
- * must be a multiple of 128.
+ * adds to what an fp32 dw holds, in fp32 (values below 2^-126 in magnitude may
+ * count as zeros there); an expert without rows then keeps its dw as it is.
+ * width_in a multiple of 8.  desc->alignment must be a multiple of 128.
  */
 MOE_API int moe_expert_wgrad_fp8(const moe_layout_desc* desc, const void* dy, const float* dy_sf, const void* x,
                                  const float* x_sf, int64_t ld, int64_t capacity_rows, int64_t width_out,

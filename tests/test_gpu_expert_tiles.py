@@ -62,3 +62,19 @@ def test_weight_gradients_of_many_tiles(counts, wo, wi, kind):
         c["dw"].fill_(5.0)
         assert run_wgrad(c, accumulate=added) == 0
         assert torch.equal(first, c["dw"])
+
+
+def test_an_added_gradient_leaves_experts_without_rows_alone():
+    """Bit for bit: signed zeros, values below the normal range, infinities."""
+    counts = [0, 200, 0, 3, 0]
+    c = wgrad_case(counts, 128, 264, 520, 8)
+    held = torch.randint(-2 ** 31, 2 ** 31 - 1, c["dw"].shape, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV,
+                         dtype=torch.int32)
+    held[0] &= -0x7f800001                                 # all below the normal range
+    held[2, ::2] = -2 ** 31                                # -0.0
+    empty = [0, 2, 4]
+    c["dw"].view(torch.int32)[empty] = held[empty]
+    assert run_wgrad(c, accumulate=True) == 0
+    assert torch.equal(c["dw"].view(torch.int32)[empty], held[empty])
+    c["dw"][empty] = 5.0
+    check_wgrad(c, counts, base=5.0)
