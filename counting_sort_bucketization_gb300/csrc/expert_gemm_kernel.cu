@@ -506,8 +506,16 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
       }
       // Every stage handed back: no copy or remote arrival is left in flight.
-      for (uint32_t i = 0; i < kStages; ++i, ++loads, ring.next())
-        if (loads >= kStages) ok &= wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns);
+#pragma unroll 1
+      for (uint32_t i = 0; ok && i < kStages; ++i, ring.next())
+        if (loads + i >= kStages) ok = wait_warp(&s.empty[ring.i], ring.phase ^ 1, p.wait_ns);
+      // After a wait that ran out the stages will not be handed back, but their copies (the
+      // peer's too, which count on the leader's barriers) are waited for; the cluster's
+      // barrier at the end keeps the peer's shared memory until then.
+      if (!ok && leader)
+#pragma unroll 1
+        for (uint32_t n = loads < kStages ? 0 : loads - kStages; n < loads; ++n)
+          wait_warp(&s.full[n % kStages], n / kStages & 1, p.wait_ns);
     } else if (warp < 3) {
       // ---- MMA: warp 1 + h into accumulator h -----------------------------
       // The barriers of a k-block are asked together: a ready one answers after ~60
