@@ -9,7 +9,8 @@ product -> SwiGLU -> down product -> combine.  Rows travel through the dispatch 
 Training (``MoELayer.step``): the same with bf16 rows dispatched (the weight
 gradients quantise them down the columns too), then every gradient: expert
 weights, router, and the input's share through the experts.  The weighted sum's
-own gradient (a product of rows and a dot product) is plain torch here.
+own gradient (a product of rows and a dot product) and the activation's bf16 rows
+for the second weight gradient are plain torch here.
 """
 from __future__ import annotations
 
@@ -86,7 +87,7 @@ class MoELayer:
         binding.swiglu_quantize(gu, h, h_sf, total_rows=lay.total_rows)
         y = self._empty(cap, H)
         lay.expert_gemm(h, h_sf, self.down, self.down_sf, y)
-        return gu, h, h_sf, y
+        return gu, y
 
     def _rows(self, t, total):
         q, sf = self._empty(*t.shape, dtype=E4M3), binding.new_sf_col_major(-(-t.shape[1] // BLOCK), t.shape[0], device=self.device)
@@ -109,7 +110,7 @@ class MoELayer:
         recv = self._empty(cap, H)
         lay.permute(x, recv)
         xq, xsf = self._rows(recv, lay.total_rows)
-        gu, h, h_sf, y = self._experts(lay, xq, xsf, cap)
+        gu, y = self._experts(lay, xq, xsf, cap)
         out = self._empty(N, H)
         lay.combine(y, gate.weights, out)
 
@@ -132,7 +133,9 @@ class MoELayer:
         dx = self._empty(N, H)
         lay.combine(dx_rows, torch.ones((N, K), device=self.device), dx)
 
-        h_rows = (h.float() * h_sf[:, :cap].t().repeat_interleave(BLOCK, 1)[:, :I]).to(torch.bfloat16)
+        # from gate_up, not from the 8-bit h: the columns are rounded to 8 bits once
+        a, b = gu.float().split(I, 1)
+        h_rows = (torch.nn.functional.silu(a) * b).to(torch.bfloat16)
         d_down = torch.empty((E, H, I), device=self.device)
         lay.expert_wgrad(*self._cols(lay, dy), *self._cols(lay, h_rows), d_down)
         d_gate_up = torch.empty((E, 2 * I, H), device=self.device)
