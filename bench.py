@@ -24,6 +24,7 @@ import hashlib
 import json
 import os
 import platform
+import re
 import statistics
 import subprocess
 import sys
@@ -47,8 +48,8 @@ L2_FLUSH_BYTES = 256 << 20          # > 2x the 129 MB L2
 DEFAULT_WORKLOAD = "roundtrip"      # the largest workload that fits one GPU
 
 # DRAM traffic per launch (ncu dram__bytes_read.sum + dram__bytes_write.sum,
-# one metric pass) of each HBM-bound kernel, by workload, tied to the sources
-# it was measured on: a kernel whose sources changed since reports null.  The
+# one metric pass) of each HBM-bound kernel, by workload, tied to the code it was
+# measured on: a kernel whose sources changed since, but for comments, reports null.  The
 # captures ran `bench.py --profile` at full size, caches flushed before each
 # captured kernel (ncu's default); each figure is the mean of two launches.
 HOW = "ncu, one metric pass (dram__bytes_read.sum + dram__bytes_write.sum), full size, bench.py --profile, caches flushed before the kernel (ncu default); mean of two launches"
@@ -57,22 +58,22 @@ TRAFFIC = {
         "sources": ["counting_sort_bucketization_gb300/csrc/permute_kernel.cu",
                     "counting_sort_bucketization_gb300/csrc/ptx.cuh",
                     "counting_sort_bucketization_gb300/csrc/common.cuh"],
-        "sha256": "1fffee62edae026b5ca95720bf44f6a7005c57c475b74538e2986c35734c6757",
-        "bytes_per_launch": {"roundtrip": {"bytes": 9273815552, "how": HOW}, "decode": {"bytes": 704104576, "how": HOW}, "skewed": {"bytes": 2075054464, "how": HOW}, "prefill_fp8": {"bytes": 2239759872, "how": HOW}, "prefill_fp8/sf-col-major": {"bytes": 2169645440, "how": HOW}, "decode/non-expand": {"bytes": 306171264, "how": HOW}},
+        "sha256": "3e9e6220c2c7017d3bd6739938271fe2641078200321c9fc7c9e5d2fcb58cfa5",
+        "bytes_per_launch": {"roundtrip": {"bytes": 9274186112, "how": HOW}, "decode": {"bytes": 703965184, "how": HOW}, "skewed": {"bytes": 2075211904, "how": HOW}, "prefill_fp8": {"bytes": 2239347200, "how": HOW}, "prefill_fp8/sf-col-major": {"bytes": 2169415680, "how": HOW}, "decode/non-expand": {"bytes": 306337024, "how": HOW}},
     },
     "combine": {   # combine_bulk_kernel (round-trip, skewed) or combine_kernel (decode), by batch size
         "sources": ["counting_sort_bucketization_gb300/csrc/combine_kernel.cu",
                     "counting_sort_bucketization_gb300/csrc/ptx.cuh",
                     "counting_sort_bucketization_gb300/csrc/common.cuh"],
-        "sha256": "088673f399f2a3677b81538aed54aeb2aa922f9fefa85e7585eeec034566d335",
-        "bytes_per_launch": {"roundtrip": {"bytes": 9192338560, "how": HOW}, "skewed": {"bytes": 1876517888, "how": HOW}, "decode": {"bytes": 477036800, "how": HOW}},
+        "sha256": "cecb527fae240dfbbd557397ae93889f125f9da470d0c47c394beb5cfe75faa9",
+        "bytes_per_launch": {"roundtrip": {"bytes": 9192541952, "how": HOW}, "skewed": {"bytes": 1876419968, "how": HOW}, "decode": {"bytes": 477023616, "how": HOW}},
     },
     "sf_col_major_kernel": {
         "sources": ["counting_sort_bucketization_gb300/csrc/sf_layout_kernel.cu",
                     "counting_sort_bucketization_gb300/csrc/ptx.cuh",
                     "counting_sort_bucketization_gb300/csrc/common.cuh"],
-        "sha256": "efff3440144641a56f852de8f68d122acfa0cf96531f3c0882b1463378b547f9",
-        "bytes_per_launch": {"prefill_fp8/sf-col-major": {"bytes": 11648640, "how": HOW}},
+        "sha256": "5b95f1722ccf279cb5eccaec4a68ea5ee4e9545b83d6cc3e1dddc0d02b0df4d6",
+        "bytes_per_launch": {"prefill_fp8/sf-col-major": {"bytes": 11739136, "how": HOW}},
     },
 }
 
@@ -109,10 +110,12 @@ def host_info() -> dict:
 
 
 def sources_sha256(paths) -> str:
+    """Hash of the sources' code: comments and white space do not count."""
     h = hashlib.sha256()
     for p in paths:
-        with open(os.path.join(REPO, p), "rb") as f:
-            h.update(f.read())
+        with open(os.path.join(REPO, p), encoding="utf-8") as f:
+            code = re.sub(r"//[^\n]*|/\*.*?\*/", " ", f.read(), flags=re.S)
+        h.update((" ".join(code.split()) + "\n").encode())
     return h.hexdigest()
 
 
