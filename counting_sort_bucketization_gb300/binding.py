@@ -470,7 +470,9 @@ _LOGITS = (torch.float32, torch.bfloat16)
 
 def gate_forward(desc, cfg, logits, topk_idx, weights, expert_count, prob_mean, routed_tokens, balance_loss,
                  workspace, bias=None, stream=None) -> None:
-    """Top-k ids and weights, per-expert counts and the balance loss of ``logits`` [N, E] (moe_gate_forward)."""
+    """Top-k ids and weights, per-expert counts and the balance loss of ``logits`` [N, E] (moe_gate_forward).
+
+    ``bias`` [E] is added to the logits (not to the scores) for the choice of experts only."""
     N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
     lp, ld = _matrix(logits, "logits", N, E, _LOGITS)
     st = load_library().moe_gate_forward(
@@ -485,7 +487,9 @@ def gate_forward(desc, cfg, logits, topk_idx, weights, expert_count, prob_mean, 
 
 def gate_backward(desc, cfg, logits, topk_idx, expert_count, routed_tokens, dlogits, workspace, dweights=None,
                   dloss=None, stream=None) -> None:
-    """Gradient of the weights and the balance loss with respect to the logits (moe_gate_backward)."""
+    """Gradient of the weights and the balance loss with respect to the logits (moe_gate_backward).
+
+    ``dlogits`` may be ``logits`` itself; rows that touch in another way are refused."""
     N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
     lp, ld = _matrix(logits, "logits", N, E, _LOGITS)
     gp, gld = _matrix(dlogits, "dlogits", N, E, (logits.dtype,))
@@ -713,6 +717,10 @@ class Layout:
 
 class Gate:
     """Output buffers and workspace of the top-k gate for one batch shape.
+
+    Experts are chosen by logit + ``bias``; the weights, the probabilities and the gradient are those of the
+    logits alone.  A correction bias that belongs to the *score* (sigmoid(l) + b, softmax(l) + b) is another
+    choice of experts and not what this argument does.
 
     ``forward(logits)`` fills ``topk_idx`` [N, K] (int64, ready for ``Layout.build``), ``weights`` [N, K] (for
     ``Layout.combine``), ``expert_count`` [E], ``prob_mean`` [E], ``routed_tokens`` [1] and ``loss`` [1];

@@ -27,7 +27,8 @@
 //           memory.
 //   kWgrad  P = x^T, Q = dy^T (so that columns of dw run along lanes); a pair.
 //
-// What shaped it, measured on 16 experts of 1024 rows, 7168 -> 4096:
+// What shaped it, measured on 16 experts of about 1024 rows, 7168 -> 4096 (before and after
+// each step, as the kernel was then):
 //  - From an MMA's issue to a waiting warp it takes ~280 cycles more than the MMA
 //    (512 a k-block), and ~210 for the peer's word that a buffer was read.  Tensor
 //    memory has room for two buffers of 256 columns, so a tile is two accumulators of
@@ -50,12 +51,14 @@
 //    the 16x256-bit one in 2.0; kFew and kWgrad take the latter for its pairs of columns.
 //
 // What it comes to, of twice the bf16 rate that a library product reaches (3781
-// TFLOP/s): 16 experts of 1024 rows, 7168 -> 4096, kMany 363 us (2649 TFLOP/s, 70 %; the
-// epilogue's adds to fp32 sums are what is left, the tensor core waits for them); 256
-// experts 5.58 ms after idle (2757), 6.4-6.6 ms one call after the other, when the power
-// cap holds the SMs at 1.47-1.51 GHz of 2.07.  16 tokens to top-8 of 256 experts, kFew
-// 0.47 ms (6.4 TB/s of 6.76).  32 experts of 1024 rows, 4096 x 7168, kWgrad 1.18 ms (1632
-// TFLOP/s: two scales a value and k-block, 1.9 GB of results).
+// TFLOP/s): 16 experts of about 1024 rows, 7168 -> 4096, kMany 366 us (2630 TFLOP/s, 70 %;
+// the epilogue's adds to fp32 sums are what is left, the tensor core waits for them; 325 us
+// if each has 1024 exactly, so four row tiles, not five); 256 experts 5.7 ms with pauses
+// between calls (2700), 6.5-6.7 ms one call after the other, when the power cap holds the
+// SMs at 1.47-1.51 GHz of 2.07.  16 tokens to top-8 of 256 experts, kFew 0.47 ms (6.4 TB/s
+// of 6.76); one row, 7168 -> 4096, its 29 MB of weights from HBM, 13.5 us.  32 experts of
+// about 1024 rows, 4096 x 7168, kWgrad 1.18 ms in bf16 (1630 TFLOP/s: two scales a value and
+// k-block, 1.9 GB of results), 1.31 in fp32, 1.64 added to fp32.
 //
 // One persistent CTA (or pair) per SM walks the tiles of all experts.  All sums
 // are fp32; the result is rounded once.
@@ -887,9 +890,10 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t stream) {
   p.out_cols = static_cast<int>(a.width_out);
   p.kblocks = static_cast<int>(ceil_div64(a.width_in, kKBlock));
   // kFew's tile holds 128 rows of an expert, kMany's 256.  Up to a mean of 112 rows
-  // (nearly all experts in one tile) kFew measured faster, from 128 on kMany: 32 experts,
-  // 7168 -> 4096, 64 rows 183 against 203 us, 112 rows 187 against 210, 128 rows 226
-  // against 214; 2048 -> 7168, 112 rows 109 against 115, 128 rows 132 against 119.
+  // (nearly all experts in one tile) kFew measures faster, from 128 on kMany.  32 experts,
+  // tokens routed at random, kFew against kMany: 7168 -> 4096, mean of 64 rows 165 to 194 us,
+  // 112 173 to 201, 120 198 to 201, 128 205 to 198, 144 251 to 199; 2048 -> 7168, 112 96
+  // to 107, 120 107 to 107, 128 117 to 108.
   const int64_t mean = a.pairs / a.num_experts;
   const bool many = mean >= 120;
   if (!many) {

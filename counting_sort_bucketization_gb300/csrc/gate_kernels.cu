@@ -11,7 +11,8 @@
 //   counts those before it (larger, or equal with a lower id): its slot.  If more
 //   than 32 reach it, the keys are taken one after the other by redux.max /
 //   redux.min.  A key of -inf is not taken.
-//   s = softmax(l) or sigmoid(l), q = s / sum(s); w_k = scale * s_k / D.
+//   s = softmax(l) or sigmoid(l), q = s / sum(s); w_k = scale * s_k / D, with D the sum of
+//   the picks' s (or 1), each quotient taken relative to its own largest score.
 //   Balance loss: coef * E * sum_e f_e P_e with P_e the mean of q over the
 //   routed tokens and f_e = count_e / (K * routed tokens).
 //
@@ -23,11 +24,14 @@
 // its tokens, then summed over warps, CTAs and last over the CTAs' partials in
 // a fixed order, so results do not change from run to run.
 //
-// 131072 x 384 fp32, top-8: forward 108 us (214 MB), backward 70 us (415 MB, 5.9
+// 131072 x 384 fp32, top-8: forward 112 us (214 MB), backward 72 us (415 MB, 5.8
 // TB/s).  The backward pass is bound by HBM, the forward pass by the issue of its
-// ~675 instructions a token, most of them for the choice.  Listing the candidates
-// took it from 210 us, where each pick was a pass over all keys, to 131 us; rows four
-// values at a time and the next row's loads a token ahead did the rest.  64 x 256, top-8: 7 us, the launch and one reduction.
+// ~720 instructions a token, most of them for the choice (bf16 logits, half the
+// bytes, take 124 us).  Listing the candidates took it from 210 us, where each pick was
+// a pass over all keys, to 131 us; rows four values at a time and the next row's loads a
+// token ahead did the rest.  64 x 256, top-8: 7 us, the launch and one reduction.
+// From 513 experts on a lane's 32 columns and the next token's do not fit its registers
+// (up to 420 bytes of spills a thread): 65536 x 1000, 171 us forward, 85 backward.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -17,8 +17,8 @@
 //
 // All of them move a few bytes an element once and are bound by HBM (a copy
 // reaches 6.76 TB/s): rows of 32768 x 7168 in 113 us (6.3 TB/s), SwiGLU of
-// 34816 x (2 x 2048) in 57.5 us (6.2), its gradient on 10007 x (2 x 1936) in
-// 29.9 us (6.5), the columns of 32768 receive rows x 4096 in 72 us (5.8; the
+// 34816 x (2 x 2048) in 57 us (6.3), its gradient on 10007 x (2 x 1936) in
+// 29.8 us (6.5), the columns of 32768 receive rows x 4096 in 72 us (5.8; the
 // barriers between the steps of a tile are what is left).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -61,7 +61,9 @@ __device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float 
   return cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);
 }
 
-// 1 / (1 + 2^(-g log2 e)); the exponent's rounding adds 2^-24 |g| where e^-g counts.
+// 1 / (1 + 2^(-g log2 e)).  The product's rounding adds 2^-24 |g| to the relative error where e^-g
+// counts, 2^-18 at -64, and results below 2^-126 are zero: every use is rounded to 16 or 8
+// bits (2^-9, 2^-4) right after.
 __device__ __forceinline__ float sigmoid(float g) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
@@ -79,7 +81,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // A half-warp owns one block of 128 columns (16 bytes of bf16 a lane); a CTA
 // of 8 warps covers 16 rows x 4 blocks.  Each half-warp takes the four blocks
 // of its row in turn with all loads issued first, so a lane has 4 (SWIGLU: 8)
-// 16-byte loads in flight (with 2 and 4 the same rows took 138 us, not 117), and
+// 16-byte loads in flight (with 2 and 4 the same rows take 133 us, SwiGLU 60), and
 // the 16 rows of a CTA make 64-byte runs of a column-major scale column.
 constexpr int kRowsThreads = 256;
 constexpr int kRowsPerCta = kRowsThreads / 16;
@@ -147,8 +149,8 @@ __global__ void __launch_bounds__(kRowsThreads, SWIGLU ? 4 : 6) quantize_rows_ke
 // side by side with the next tile's rows on their way.  A thread holds 4
 // consecutive rows x 8 columns, so its codes of a column make one 32-bit word
 // of the transposed tile; words go through shared memory at a pitch of 33 and
-// leave as 128-byte runs of a transposed row.  (Five CTAs an SM: 76 us where four
-// take 83 and three 87.  A warp a tile of 16 columns, without barriers, took 115: its
+// leave as 128-byte runs of a transposed row.  (Five CTAs an SM: 72 us where four
+// take 76 and three 82.  A warp a tile of 16 columns, without barriers, took 115: its
 // 32-byte pieces of rows cost more than the barriers.)
 constexpr int kColsThreads = 256;
 constexpr int kTileCols = 64;

@@ -385,6 +385,8 @@ MOE_API int moe_gate_workspace_bytes(const moe_layout_desc* desc, size_t* bytes)
  *   key_e = l_e + bias_e in fp32 (bias may be NULL: 0); the K largest keys, in
  *     descending order, equal keys by ascending id; a key of -inf is never
  *     taken, so l_e = -inf closes expert e for the token;
+ *   the bias counts for this choice alone.  It is not a bias of the score: gates that
+ *     choose by sigmoid(l_e) + b_e or softmax(l)_e + b_e choose other experts;
  *   s = softmax(l) or sigmoid(l) (without the bias), q = s / sum_e s;
  *   topk_idx[t*K+k] = id (int64), weights[t*K+k] = scale * s_id / D with
  *     D = the sum of the token's picked s if normalize, else 1; slots without
@@ -395,7 +397,8 @@ MOE_API int moe_gate_workspace_bytes(const moe_layout_desc* desc, size_t* bytes)
  *   expert_count[E], routed_tokens[1] = T,
  *   prob_mean[E] = (1/T) sum_t q, balance_loss[1] =
  *     balance_coef * E * sum_e (expert_count[e] / (K*T)) * prob_mean[e]
- * (zeros if T = 0).  Everything is fp32 and does not change from run to run.
+ * (zeros if T = 0).  Everything is fp32 and does not change from run to run; what is
+ * below 2^-126 may come out as zero.
  * alignment and num_ranks of desc are not used.
  */
 MOE_API int moe_gate_forward(const moe_layout_desc* desc, const moe_gate_desc* gate, const void* logits,
