@@ -1,7 +1,9 @@
 """Where the gate's gradient may lie in relation to the logits: the host checks, without a GPU.
 
 A call that passes its checks reaches a launch, which no GPU answers with MOE_ERR_CUDA (2); on a machine with a GPU only the
-refusals are tried, since the addresses are not real."""
+refusals are tried, since the addresses are not real.  Such calls are made in a thread of their own, which keeps the CUDA
+error they leave."""
+import concurrent.futures
 import ctypes
 
 import pytest
@@ -48,4 +50,5 @@ def test_the_same_rows_and_separate_rows_are_taken(call, bf16, size):
                                    (16, at + 64 * 16 * size, 99), (40, at + 16 * size, 40), (40, at + 24 * size, 40),
                                    (40, at - 16 * size, 40), (32, at + (32 * 9 + 16) * size, 32),
                                    (40, at + (63 * 40 + 16) * size, 41)]:
-        assert call(at, stride, other, dstride, bf16) == 2, (stride, other - at, dstride)
+        with concurrent.futures.ThreadPoolExecutor(1) as thread:
+            assert thread.submit(call, at, stride, other, dstride, bf16).result() == 2, (stride, other - at, dstride)
