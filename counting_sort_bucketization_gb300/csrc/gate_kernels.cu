@@ -104,6 +104,10 @@ __device__ __forceinline__ float sigmoid(float x) {
   return x >= 0.0f ? large : small;
 }
 
+// A share of a sum of scores.  The sum is zero only where a caller's own ids are of closed
+// experts alone.
+__device__ __forceinline__ float share(float v, float sum) { return sum > 0.0f ? __fdividef(v, sum) : 0.0f; }
+
 // The column of a lane's i-th value.
 template <bool VEC>
 __device__ __forceinline__ int column(int lane, int i) {
@@ -216,7 +220,7 @@ __device__ __forceinline__ float share_of_picks(bool pick, float l, float score,
     v = pick ? exp_neg(l - top) : 0.0f;
     sum = warp_sum(v);
   }
-  return __fdividef(v, sum);
+  return share(v, sum);
 }
 
 template <int VPL, typename T, bool SIGMOID, bool VEC>
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? (SIGMOID ? 4 : 5) : V
     float m = SIGMOID ? 0.0f : row_max<VPL>(l);
     bool tiny;
     float dot;
-    const float inv = __fdividef(1.0f, scores<VPL, T, SIGMOID, VEC>(l, m, tiny, row, lane, E, g, &dot));
+    const float inv = share(1.0f, scores<VPL, T, SIGMOID, VEC>(l, m, tiny, row, lane, E, g, &dot));
     const float A = dot * inv;
 
     const bool pick = mine >= 0;
@@ -502,8 +506,8 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? (SIGMOID ? 4 : 5) : V
     float c = 0.0f;
     if (a.normalize) {
       const float top = SIGMOID ? 0.0f : unsortable(__reduce_max_sync(kFull, pick ? sortable(lk) : 0u));
-      const float share = share_of_picks<SIGMOID>(pick, lk, s, top);
-      d = a.scale * share * (dw - warp_sum(share * dw));
+      const float r = share_of_picks<SIGMOID>(pick, lk, s, top);
+      d = a.scale * r * (dw - warp_sum(r * dw));
     } else {
       d = a.scale * s * dw;
       if (!SIGMOID) c = warp_sum(d);
