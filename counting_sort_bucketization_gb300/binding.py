@@ -60,11 +60,24 @@ class GateConfig:
     normalize: bool = True         # a token's weights sum to ``scale``
     scale: float = 1.0
     balance_coef: float = 0.0      # factor of the balance loss
+    bias_on: str = "logit"         # experts are chosen by logit + bias, or by "score" + bias
+    num_groups: int = 1            # with bias_on="score": groups of experts side by side,
+    topk_groups: int = 1           #   how many of them a token's experts come from,
+    group_sum: int = 1             #   and of how many of its largest keys a group's score is the sum (1 or 2)
 
 
 class _CGateDesc(ctypes.Structure):
     _fields_ = [("logits_bf16", ctypes.c_int32), ("sigmoid", ctypes.c_int32), ("normalize", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("balance_coef", ctypes.c_float)]
+
+
+class _CGateGroups(ctypes.Structure):
+    _fields_ = [("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32), ("group_sum", ctypes.c_int32)]
+
+
+class _CNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("stream_fp32", ctypes.c_int32), ("weight_fp32", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -108,6 +121,12 @@ def load_library() -> ctypes.CDLL:
         lib.moe_gate_workspace_bytes.argtypes = [dp, ctypes.POINTER(ctypes.c_size_t)]
         lib.moe_gate_forward.argtypes = [dp, gp, p, i64, p, p, p, p, p, p, p, p, sz, p]
         lib.moe_gate_backward.argtypes = [dp, gp, p, i64, p, p, p, p, p, p, i64, p, sz, p]
+        rp, np_ = ctypes.POINTER(_CGateGroups), ctypes.POINTER(_CNormDesc)
+        lib.moe_gate_forward_grouped.argtypes = [dp, gp, rp, p, i64, p, p, p, p, p, p, p, p, sz, p]
+        lib.moe_combine_backward.argtypes = [dp, p, i64, p, p, p, p, i64, p, p, p, ci, p, sz, p]
+        lib.moe_rms_norm.argtypes = [np_, p, p, p, p, p, p, p, p, i64, p, p]
+        lib.moe_rms_norm_workspace_bytes.argtypes = [np_, ctypes.POINTER(ctypes.c_size_t)]
+        lib.moe_rms_norm_backward.argtypes = [np_, p, p, p, p, p, p, p, p, p, ci, p, sz, p]
         lib.moe_quantize_rows.argtypes = [p, i64, i64, p, p, p, i64, p]
         lib.moe_swiglu_quantize.argtypes = [p, i64, i64, p, p, p, i64, p]
         lib.moe_swiglu_backward.argtypes = [p, p, i64, i64, p, p, p]
@@ -130,7 +149,8 @@ def load_library() -> ctypes.CDLL:
                      "moe_dispatch_permute", "moe_combine_unpermute", "moe_layout_get_error",
                      "moe_dispatch_sf_col_major", "moe_gate_workspace_bytes", "moe_gate_forward",
                      "moe_gate_backward", "moe_quantize_rows", "moe_swiglu_quantize", "moe_swiglu_backward",
-                     "moe_quantize_cols", "moe_expert_gemm_fp8", "moe_expert_wgrad_fp8"):
+                     "moe_quantize_cols", "moe_expert_gemm_fp8", "moe_expert_wgrad_fp8", "moe_gate_forward_grouped",
+                     "moe_combine_backward", "moe_rms_norm", "moe_rms_norm_workspace_bytes", "moe_rms_norm_backward"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -359,6 +379,32 @@ def accumulate_stats(desc, expert_count, cumulative, stream=None) -> None:
     _check(st, "moe_layout_accumulate_stats")
 
 
+def combine_backward(desc, dout, dst_slot, weights, dy, workspace, expert_out=None, dweights=None, expert_offset=None,
+                     expert_count=None, zero_pad=True, stream=None) -> None:
+    """Gradient of the combine: dy[dst_slot[t,k]] = bf16(w[t,k] * dout[t]) and, with ``expert_out``,
+    dweights[t,k] = <dout[t], expert_out[dst_slot[t,k]]> (0 where masked).
+
+    ``dout`` [N, H], ``dy`` and ``expert_out`` [capacity, H], all bf16; ``dy`` may be ``expert_out`` itself.
+    ``zero_pad`` zeroes the alignment-gap rows of ``dy`` and needs the layout's offsets and counts."""
+    N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
+    if dy.dim() != 2 or tuple(dout.shape) != (N, dy.shape[1]):
+        raise ValueError(f"dy must be [capacity, H] and dout [{N}, H]")
+    cap, H = dy.shape
+    if dweights is not None and expert_out is None:
+        raise ValueError("dweights needs expert_out")
+    if expert_out is not None and expert_out.shape != dy.shape:
+        raise ValueError(f"expert_out must be [{cap}, {H}]")
+    st = load_library().moe_combine_backward(
+        ctypes.byref(_desc(desc)), _dev(dout, "dout", torch.bfloat16), H, _dev(dst_slot, "dst_slot", torch.int32, N * K),
+        _dev(weights, "weights", torch.float32, N * K),
+        _dev(expert_out, "expert_out", torch.bfloat16, allow_none=True), _dev(dy, "dy", torch.bfloat16), cap,
+        _dev(dweights, "dweights", torch.float32, N * K, allow_none=True),
+        _dev(expert_offset, "expert_offset", torch.int32, E + 1, allow_none=not zero_pad),
+        _dev(expert_count, "expert_count", torch.int32, E, allow_none=not zero_pad), 1 if zero_pad else 0,
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check(st, "moe_combine_backward")
+
+
 def _host(t: torch.Tensor | None, name: str, allow_none=False, nbytes=None):
     if t is None:
         if allow_none:
@@ -447,6 +493,17 @@ def _gate_desc(cfg, dtype) -> _CGateDesc:
                       float(cfg.scale), float(cfg.balance_coef))
 
 
+def _gate_groups(cfg) -> _CGateGroups | None:
+    """The groups of a gate that chooses by score, None for one that chooses by logit."""
+    if cfg.bias_on not in ("logit", "score"):
+        raise ValueError(f"unknown bias_on {cfg.bias_on!r}")
+    if cfg.bias_on == "score":
+        return _CGateGroups(int(cfg.num_groups), int(cfg.topk_groups), int(cfg.group_sum))
+    if (cfg.num_groups, cfg.topk_groups, cfg.group_sum) != (1, 1, 1):
+        raise ValueError('groups of experts need bias_on="score"')
+    return None
+
+
 def _matrix(t, name, rows, cols, dtypes):
     """A [rows, cols] device matrix with contiguous columns; returns (pointer, row stride in elements)."""
     if t is None or not t.is_cuda:
@@ -470,19 +527,22 @@ _LOGITS = (torch.float32, torch.bfloat16)
 
 def gate_forward(desc, cfg, logits, topk_idx, weights, expert_count, prob_mean, routed_tokens, balance_loss,
                  workspace, bias=None, stream=None) -> None:
-    """Top-k ids and weights, per-expert counts and the balance loss of ``logits`` [N, E] (moe_gate_forward).
+    """Top-k ids and weights, per-expert counts and the balance loss of ``logits`` [N, E] (moe_gate_forward, or
+    moe_gate_forward_grouped for a ``cfg`` with bias_on="score").
 
-    ``bias`` [E] is added to the logits (not to the scores) for the choice of experts only."""
+    ``bias`` [E] is added to the logits (to the scores) for the choice of experts only."""
     N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
     lp, ld = _matrix(logits, "logits", N, E, _LOGITS)
-    st = load_library().moe_gate_forward(
-        ctypes.byref(_desc(desc)), ctypes.byref(_gate_desc(cfg, logits.dtype)), lp, ld,
+    lib, groups = load_library(), _gate_groups(cfg)
+    fn, more = (lib.moe_gate_forward, ()) if groups is None else (lib.moe_gate_forward_grouped, (ctypes.byref(groups),))
+    st = fn(
+        ctypes.byref(_desc(desc)), ctypes.byref(_gate_desc(cfg, logits.dtype)), *more, lp, ld,
         _dev(bias, "bias", torch.float32, E, allow_none=True), _dev(topk_idx, "topk_idx", torch.int64, N * K),
         _dev(weights, "weights", torch.float32, N * K), _dev(expert_count, "expert_count", torch.int32, E),
         _dev(prob_mean, "prob_mean", torch.float32, E), _dev(routed_tokens, "routed_tokens", torch.int32, 1),
         _dev(balance_loss, "balance_loss", torch.float32, 1), _dev(workspace, "workspace", torch.uint8),
         workspace.numel(), _stream(stream))
-    _check(st, "moe_gate_forward")
+    _check(st, fn.__name__)
 
 
 def gate_backward(desc, cfg, logits, topk_idx, expert_count, routed_tokens, dlogits, workspace, dweights=None,
@@ -573,6 +633,83 @@ def quantize_cols(desc, x, expert_offset, expert_count, q, sf, workspace, stream
         _dev(q, "q", torch.float8_e4m3fn), q.shape[1], _dev(sf, "sf", torch.float32),
         _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     _check(st, "moe_quantize_cols")
+
+
+# ---------------------------------------------------------------- norm
+def _norm_desc(rows, cols, eps, stream, weight) -> _CNormDesc:
+    if stream not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"the residual stream must be bfloat16 or float32, got {stream}")
+    if weight.dtype not in (torch.bfloat16, torch.float32) or weight.numel() != cols:
+        raise ValueError(f"weight must be [{cols}] in bfloat16 or float32")
+    return _CNormDesc(int(rows), int(cols), float(eps), int(stream == torch.float32), int(weight.dtype == torch.float32))
+
+
+def _like(t, shape, name, dtype):
+    """Pointer of a contiguous device tensor of exactly this shape, or None."""
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _dev(t, name, dtype, allow_none=True)
+
+
+def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, residual_out=None, rstd=None, eps=1e-6, total_rows=None,
+             col_major=False, stream=None) -> None:
+    """z = x + residual (kept in ``residual_out``, which may be ``residual``), normed by its root mean square and
+    scaled by ``weight``: into ``y`` (bf16), into ``q`` (e4m3) with block scales ``sf`` as ``quantize_rows`` makes
+    them, or both.  ``rstd`` [rows] (fp32) is what ``rms_norm_backward`` needs.
+
+    ``x`` bf16 [rows, cols]; ``residual`` bf16 or fp32, or None: x is normed as it is.  Rows from ``total_rows``
+    (device int32) on are left alone."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    rows, cols = x.shape
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out go together")
+    if (q is None) != (sf is None):
+        raise ValueError("q and sf go together")
+    kind = torch.bfloat16 if residual is None else residual.dtype
+    d = _norm_desc(rows, cols, eps, kind, weight)
+    ld = 0
+    if q is not None:
+        if col_major:
+            ld = _sf_ld(sf, rows, _blocks(cols))
+        elif tuple(sf.shape) != (rows, _blocks(cols)):
+            raise ValueError(f"sf must be [{rows}, {_blocks(cols)}], got {tuple(sf.shape)}")
+    st = load_library().moe_rms_norm(
+        ctypes.byref(d), _dev(x, "x", torch.bfloat16), _like(residual, x.shape, "residual", kind), _dev(weight, "weight"),
+        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True),
+        _like(residual_out, x.shape, "residual_out", kind), _like(y, x.shape, "y", torch.bfloat16),
+        _like(q, x.shape, "q", torch.float8_e4m3fn), _dev(sf, "sf", torch.float32, allow_none=True), ld,
+        _like(rstd, (rows,), "rstd", torch.float32), _stream(stream))
+    _check(st, "moe_rms_norm")
+
+
+def new_norm_workspace(cols, device="cuda") -> torch.Tensor:
+    """Workspace of ``rms_norm_backward`` for rows of ``cols`` values."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_rms_norm_workspace_bytes(ctypes.byref(_CNormDesc(0, int(cols), 1.0, 0, 0)), ctypes.byref(n)),
+           "moe_rms_norm_workspace_bytes")
+    return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+
+
+def rms_norm_backward(dy, z, rstd, weight, dz, dresidual=None, dx=None, dweight=None, workspace=None, accumulate=False,
+                      total_rows=None, stream=None) -> None:
+    """Gradient of ``rms_norm`` from its kept ``z`` (the residual_out, or x) and ``rstd``: ``dz`` (the stream's type)
+    is the gradient of x and of the residual, with ``dresidual`` added; ``dx`` the same in bf16.  ``dweight`` [cols]
+    (fp32) needs a ``workspace`` (``new_norm_workspace``); ``accumulate`` adds to it."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be [rows, cols]")
+    rows, cols = dy.shape
+    d = _norm_desc(rows, cols, 1.0, z.dtype, weight)
+    if dweight is not None and workspace is None:
+        raise ValueError("dweight needs a workspace")
+    st = load_library().moe_rms_norm_backward(
+        ctypes.byref(d), _dev(dy, "dy", torch.bfloat16), _like(z, dy.shape, "z", z.dtype),
+        _like(rstd, (rows,), "rstd", torch.float32), _dev(weight, "weight"), _like(dresidual, dy.shape, "dresidual", z.dtype),
+        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True), _like(dz, dy.shape, "dz", z.dtype),
+        _like(dx, dy.shape, "dx", torch.bfloat16), _like(dweight, (cols,), "dweight", torch.float32), int(bool(accumulate)),
+        _dev(workspace, "workspace", torch.uint8, allow_none=True), 0 if workspace is None else workspace.numel(),
+        _stream(stream))
+    _check(st, "moe_rms_norm_backward")
 
 
 # ---------------------------------------------------------------- expert products
@@ -698,6 +835,11 @@ class Layout:
     def combine(self, expert_out, weights, out, stream=None):
         combine_unpermute(self.desc, expert_out, self.dst_slot, weights, out, self.workspace, stream)
 
+    def combine_backward(self, dout, weights, dy, expert_out=None, dweights=None, zero_pad=True, stream=None):
+        """Gradient of ``combine``: rows ``dy`` [capacity, H] and, from ``expert_out``, ``dweights`` [N, K]."""
+        combine_backward(self.desc, dout, self.dst_slot, weights, dy, self.workspace, expert_out, dweights,
+                         self.expert_offset, self.expert_count, zero_pad, stream)
+
     def expert_gemm(self, x, x_sf, w, w_sf, out, stream=None):
         """Expert product of 8-bit receive rows (column-major scales ``x_sf``) with weights [E, out, in]."""
         expert_gemm(self.desc, x, x_sf, w, w_sf, self.expert_offset, self.expert_count, out, self.workspace, stream)
@@ -720,7 +862,8 @@ class Gate:
 
     Experts are chosen by logit + ``bias``; the weights, the probabilities and the gradient are those of the
     logits alone.  A correction bias that belongs to the *score* (sigmoid(l) + b, softmax(l) + b) is another
-    choice of experts and not what this argument does.
+    choice of experts: ``GateConfig(bias_on="score")`` makes it, also limited to a token's best groups of experts
+    (``num_groups``, ``topk_groups``, ``group_sum``).
 
     ``forward(logits)`` fills ``topk_idx`` [N, K] (int64, ready for ``Layout.build``), ``weights`` [N, K] (for
     ``Layout.combine``), ``expert_count`` [E], ``prob_mean`` [E], ``routed_tokens`` [1] and ``loss`` [1];
@@ -742,6 +885,8 @@ class Gate:
         self._shape, self._topk = (N, E), (N, K)
         self._cdesc = ctypes.byref(_desc(desc))
         self._cgate = {t: ctypes.byref(_gate_desc(cfg, t)) for t in _LOGITS}
+        groups = _gate_groups(cfg)
+        self._groups = () if groups is None else (ctypes.byref(groups),)
         self._own = tuple(t.data_ptr() for t in self._buffers)
         self._ws_bytes = self.workspace.numel()
 
@@ -751,10 +896,12 @@ class Gate:
 
     def forward(self, logits, bias=None, stream=None) -> "Gate":
         lp, ld = _matrix(logits, "logits", *self._shape, _LOGITS)
-        _check(load_library().moe_gate_forward(
-            self._cdesc, self._cgate[logits.dtype], lp, ld,
+        lib = load_library()
+        fn = lib.moe_gate_forward_grouped if self._groups else lib.moe_gate_forward
+        _check(fn(
+            self._cdesc, self._cgate[logits.dtype], *self._groups, lp, ld,
             _dev(bias, "bias", torch.float32, self._shape[1], allow_none=True), *self._own, self._ws_bytes,
-            _stream(stream)), "moe_gate_forward")
+            _stream(stream)), "moe_gate_forward_grouped" if self._groups else "moe_gate_forward")
         return self
 
     def backward(self, logits, dlogits, dweights=None, dloss=None, stream=None):

@@ -132,6 +132,9 @@ struct GateArgs {
   float balance_coef;
   int64_t* topk_idx;             // written forward, read backward
   float* weights;
+  int num_groups;                // routing by scores: groups of experts, how many stay,
+  int topk_groups;               //   and of how many keys a group's score is the sum
+  int group_sum;
   int32_t* expert_count;         // written forward, read backward
   float* prob_mean;
   int32_t* routed_tokens;        // written forward, read backward
@@ -147,6 +150,58 @@ struct GateArgs {
 };
 
 cudaError_t launch_gate(const GateArgs& a, bool backward, cudaStream_t stream);
+// The forward pass with experts chosen by score + bias and by groups (route_kernels.cu).
+cudaError_t launch_route(const GateArgs& a, cudaStream_t stream);
+
+// ------------------------------------------------ norm (norm_kernels.cu)
+constexpr int kNormMaxCtas = 608;      // partial sums of the weight's gradient at most
+
+struct NormArgs {
+  const uint16_t* x;             // bf16 bits [rows, cols]; backward: dy
+  const void* residual;          // residual stream, or null; backward: z
+  const void* weight;            // [cols]
+  const int32_t* total_rows;     // rows in use, or null: all
+  int64_t rows;
+  int64_t cols;
+  float eps;
+  bool stream_fp32;
+  bool weight_fp32;
+  void* residual_out;            // with a residual; backward: dz
+  uint16_t* y;                   // bf16 bits, or null; backward: dx or null
+  uint8_t* q;                    // e4m3, or null
+  float* sf;                     // scale of (row, block) at row * sf_row_stride + block * sf_block_stride
+  int64_t sf_row_stride;
+  int64_t sf_block_stride;
+  float* rstd;                   // [rows], or null; read backward
+  const void* dresidual;         // backward, or null
+  float* dweight;                // backward, or null
+  float* partial;                // backward: [kNormMaxCtas, cols]
+  bool accumulate;
+};
+
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream);
+
+// ------------------------------------------------ combine's gradient (combine_backward_kernel.cu)
+struct CombineBackwardArgs {
+  const uint16_t* dout;          // bf16 bits [N, hidden]
+  int64_t hidden;
+  const int32_t* dst_slot;
+  const float* weights;
+  const uint16_t* expert_out;    // bf16 bits [capacity, hidden]; with dweights
+  uint16_t* dy;                  // bf16 bits [capacity, hidden]
+  int64_t capacity;
+  float* dweights;               // [N * K], or null
+  const int32_t* expert_offset;  // with zero_pad
+  const int32_t* expert_count;
+  bool zero_pad;
+  int64_t num_tokens;
+  int topk;
+  int num_experts;
+  int* err;
+};
+
+cudaError_t launch_combine_backward(const CombineBackwardArgs& a, cudaStream_t stream);
 
 // ------------------------------------------------ 8-bit rows (quantize_kernels.cu)
 struct QuantRowsArgs {

@@ -28,38 +28,10 @@
 #include "common.cuh"
 #include "launch.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int kBlock = 128;            // values that share a scale
-constexpr float kE4m3Max = 448.0f;
-constexpr float kAmaxFloor = 1e-30f;
-
-__device__ __forceinline__ void unpack8(uint4 v, float* f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Two floats to two e4m3 codes (lo in the low byte), round to nearest even.
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float d) {
-  return cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);
-}
 
 // 1 / (1 + 2^(-g log2 e)).  The product's rounding adds 2^-24 |g| to the relative error where e^-g
 // counts, 2^-18 at -64, and results below 2^-126 are zero: every use is rounded to 16 or 8
@@ -68,13 +40,6 @@ __device__ __forceinline__ float sigmoid(float g) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
   return __fdividef(1.0f, 1.0f + e);
-}
-
-// The larger of two magnitudes; a NaN on either side stays (fmaxf would drop it).
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
 }
 
 // ---------------------------------------------------------------- rows

@@ -38,8 +38,8 @@
  *    them start reading their inputs topk_idx, x and sf before the kernel in
  *    front of them on the stream has finished: the dispatch permutes prefetch
  *    token rows, the rank kernels stage ids.  This is safe after copies, after
- *    this library's own kernels (the gate and the quantisers, which write those
- *    inputs, do not release their dependents early) and after any other
+ *    this library's own kernels (the gate, the norm and the quantisers, which write
+ *    those inputs, do not release their dependents early) and after any other
  *    kernel that does not release its dependents early.  The kernel
  *    launched on the stream directly before one of these calls must not write
  *    the call's topk_idx, x or sf and also release its dependents before it
@@ -70,7 +70,8 @@ enum moe_status {
   MOE_OK = 0,
   MOE_ERR_INVALID_ARG = 1,   /* host check failed: null pointer, bad size or alignment;
                                 device (moe_dispatch_sf_col_major): map entry out of range;
-                                device (moe_gate_forward): a NaN or +inf key;
+                                device (moe_gate_forward, moe_gate_forward_grouped): a NaN
+                                or +inf key;
                                 device (moe_quantize_cols, moe_expert_wgrad_fp8): a
                                 segment that starts inside a block of 128 rows       */
   MOE_ERR_CUDA = 2,          /* a CUDA launch or copy failed                           */
@@ -420,6 +421,106 @@ MOE_API int moe_gate_backward(const moe_layout_desc* desc, const moe_gate_desc* 
                               int64_t logits_stride, const int64_t* topk_idx, const int32_t* expert_count,
                               const int32_t* routed_tokens, const float* dweights, const float* dloss,
                               void* dlogits, int64_t dlogits_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Groups of experts: E / num_groups side by side.  Plain values, copied by every call. */
+typedef struct moe_gate_groups {
+  int32_t num_groups;    /* G, 1 <= G <= MOE_MAX_GROUPS, divides E                         */
+  int32_t topk_groups;   /* groups a token's experts come from, 1 .. G                     */
+  int32_t group_sum;     /* a group's score: the sum of its 1 or 2 largest keys            */
+} moe_gate_groups;
+#define MOE_MAX_GROUPS 32
+
+/*
+ * moe_gate_forward with experts chosen by score and limited to the best groups
+ * (same arguments, outputs, workspace and errors otherwise; the gradient is
+ * moe_gate_backward):
+ *   key_e = s_e + bias_e, s = softmax(l) or sigmoid(l) (bias may be NULL: 0); an expert
+ *     with l_e or bias_e = -inf is closed: its key is -inf and never taken;
+ *   a group's score is the sum of its group_sum largest keys above -inf (of one, if it
+ *     has no other); the topk_groups groups of the largest scores stay, equal scores by
+ *     ascending group; a group whose experts are all closed never does;
+ *   the K largest keys of those groups, in descending order, equal keys by ascending id;
+ *   ids, weights (of s, without the bias), counts and balance loss as in moe_gate_forward.
+ * Keys are compared as numbers, not as what 32 bits make of them: what fp32 leaves open is
+ * settled in 64 bits.  Where all biases are equal the order of the keys is that of the
+ * logits.
+ * Tokens with a NaN or +inf among their logits or keys are not routed and record
+ * MOE_ERR_INVALID_ARG.
+ */
+MOE_API int moe_gate_forward_grouped(const moe_layout_desc* desc, const moe_gate_desc* gate,
+                                     const moe_gate_groups* groups, const void* logits, int64_t logits_stride,
+                                     const float* bias, int64_t* topk_idx, float* weights, int32_t* expert_count,
+                                     float* prob_mean, int32_t* routed_tokens, float* balance_loss,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of moe_combine_unpermute's sum: for every valid (t, k)
+ *   dy[dst_slot[t*K+k], h] = bf16(weights[t*K+k] * float(dout[t, h]))
+ *   dweights[t*K+k] = sum_h float(dout[t, h]) * float(expert_out[dst_slot[t*K+k], h])
+ * in fp32, in an order that does not change from run to run; dweights of a masked
+ * slot is 0.  dweights may be NULL, and expert_out with it.  With zero_pad != 0 the
+ * alignment-gap rows of dy are set to zero (expert_offset and expert_count as written by
+ * the layout; NULL allowed otherwise); rows past the last segment are not written.
+ *   dout bf16 [N, hidden], expert_out and dy bf16 [capacity_rows, hidden]; hidden a
+ *   positive multiple of 8; 16-byte aligned.  dy may be expert_out itself (written in
+ *   place); other overlaps are refused.  Slots >= capacity_rows are skipped (their
+ *   dweights are 0) and record MOE_ERR_CAPACITY.
+ */
+MOE_API int moe_combine_backward(const moe_layout_desc* desc, const void* dout, int64_t hidden,
+                                 const int32_t* dst_slot, const float* weights, const void* expert_out,
+                                 void* dy, int64_t capacity_rows, float* dweights, const int32_t* expert_offset,
+                                 const int32_t* expert_count, int zero_pad, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Norm settings.  Plain values, copied by every call. */
+typedef struct moe_norm_desc {
+  int64_t rows;          /* rows >= 0                                                      */
+  int64_t cols;          /* a positive multiple of 16, at most MOE_MAX_NORM_COLS           */
+  float eps;             /* > 0                                                            */
+  int32_t stream_fp32;   /* residual stream (residual, residual_out, z, dz): 0 bf16, 1 fp32 */
+  int32_t weight_fp32;   /* weight: 0 bf16, 1 fp32                                         */
+} moe_norm_desc;
+#define MOE_MAX_NORM_COLS 32768
+
+/*
+ * Residual addition and root-mean-square norm, with the normed rows in bf16, in 8 bits
+ * or both.  For every row:
+ *   z = x + residual, rounded to the stream's type and written to residual_out
+ *       (residual and residual_out both NULL: z = x, and the stream must be bf16);
+ *   r = 1 / sqrt(mean_j z_j^2 + eps);  v_j = z_j * r * weight_j, in fp32;
+ *   y = bf16(v);
+ *   q, sf = v quantised as by moe_quantize_rows (sf_ld as there: 0 row-major for
+ *       moe_dispatch_permute, > 0 column-major for moe_expert_gemm_fp8);
+ *   rstd[row] = r, for moe_rms_norm_backward.
+ *   x bf16 [rows, cols]; y, q (with sf) and rstd may each be NULL, but not both y and q.
+ *   16-byte aligned bases (rstd, sf: 4).  residual_out may be residual itself, and any
+ *   bf16 output any bf16 input; other overlaps are refused.
+ * total_rows (device int32, may be NULL): rows in use; later rows are neither read nor
+ * written.
+ */
+MOE_API int moe_rms_norm(const moe_norm_desc* norm, const void* x, const void* residual, const void* weight,
+                         const int32_t* total_rows, void* residual_out, void* y, void* q, float* sf,
+                         int64_t sf_ld, float* rstd, void* stream);
+
+/* Bytes of the gradient's workspace (16-byte aligned; it need not be zero-filled; one
+ * stream at a time). */
+MOE_API int moe_rms_norm_workspace_bytes(const moe_norm_desc* norm, size_t* bytes);
+
+/*
+ * Gradient of moe_rms_norm.  z is the call's residual_out (its x, without a residual),
+ * rstd its rstd, dy bf16 the gradient of v, dresidual that of residual_out from elsewhere
+ * (the stream's type; may be NULL).  With g = dy * weight and h = z * rstd:
+ *   dz = rstd * (g - h * mean_j(g_j h_j)) + dresidual: the gradient of x and of residual,
+ *       in the stream's type;  dx: the same in bf16 (may be NULL);
+ *   dweight[j] = sum over the rows of dy_j h_j in fp32 (may be NULL); accumulate != 0 adds
+ *       to what it holds.  The order of the sum does not change from run to run.
+ * dz may be dresidual, z or (bf16) dy, and dx dy; other overlaps are refused.  eps is not
+ * used.  workspace may be NULL without dweight.
+ */
+MOE_API int moe_rms_norm_backward(const moe_norm_desc* norm, const void* dy, const void* z, const float* rstd,
+                                  const void* weight, const void* dresidual, const int32_t* total_rows,
+                                  void* dz, void* dx, float* dweight, int accumulate, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * bf16 rows to e4m3 with one fp32 scale for each 1x128 block (the last block of
