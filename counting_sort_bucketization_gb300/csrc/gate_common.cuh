@@ -194,26 +194,28 @@ __device__ __forceinline__ float share_of_picks(bool pick, float l, float score,
   return share(v, sum);
 }
 
-// What a CTA's warps have summed over their tokens (acc: a lane's columns of the scores'
-// shares; cnt_s: picks of each expert; `routed` tokens of the warp) to the results over
-// the batch.  All threads of every CTA of the grid call it.
-template <int VPL, bool VEC>
-__device__ __forceinline__ void finish_sums(const GateArgs& a, const float* acc, int routed, float* sum_s, int* cnt_s,
-                                            float* red_s, bool& last_s) {
-  const int E = a.num_experts, K = a.topk;
+// Adds the warps' sums over their tokens (acc: the scores' shares of a lane's columns) to the
+// CTA's, one warp after the other, so the order is fixed.
+template <int VPL, typename F>
+__device__ __forceinline__ void add_columns(const float* acc, int E, float* sum_s, F column_of) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  // The CTA's sums: warps one after the other, so the order is fixed.
-  if (lane == 0 && routed > 0) atomicAdd(&cnt_s[E], routed);
   for (int w = 0; w < kGateWarps; ++w) {
     if (w == warp) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const int col = column<VEC>(lane, i);
+        const int col = column_of(lane, i);
         if (col < E) sum_s[col] += acc[i];
       }
     }
     __syncthreads();
   }
+}
+
+// The CTAs' sums (sum_s: [E]; cnt_s: [E + 1], picks of each expert and routed tokens) to the
+// results over the batch.  All threads of every CTA of the grid call it after a barrier.
+__device__ __forceinline__ void finish_sums(const GateArgs& a, float* sum_s, int* cnt_s, float* red_s, bool& last_s) {
+  const int E = a.num_experts, K = a.topk;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   // Partials of CTAs, then of groups of CTAs: whoever finishes last in a group (and the
   // last group) adds them in their order.
   const int groups = (static_cast<int>(gridDim.x) + kGateGroup - 1) / kGateGroup;

@@ -172,7 +172,9 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
     }
   }
 
-  finish_sums<VPL, VEC>(a, acc, routed, sum_s, cnt_s, red_s, last_s);
+  if (lane == 0 && routed > 0) atomicAdd(&cnt_s[E], routed);
+  add_columns<VPL>(acc, E, sum_s, [](int l, int i) { return column<VEC>(l, i); });
+  finish_sums(a, sum_s, cnt_s, red_s, last_s);
 }
 
 // Gradient.  With g_e = dloss * coef * E * f_e / routed and A = sum_e q_e g_e, the

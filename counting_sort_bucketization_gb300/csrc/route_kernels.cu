@@ -9,13 +9,16 @@
 //
 // Keys are numbers, not their approximations in 32 bits: two of them may lie closer than
 // those err (their order then hangs on how a sigmoid was computed).  So a warp compares in
-// 32 bits with the errors' bound in hand, and where a decision lies within it, the token
-// is done again in 64 bits (choose_exact).  Equal logits with equal biases tie exactly, and
-// where no bias differs from another the order of the logits is that of the keys; neither
-// needs 64 bits.
+// 32 bits with the errors' bound in hand, and where a decision lies within it, that token's
+// is done again with keys of two floats (exact_picks), after the loop over the tokens: calls
+// within it cost all tokens registers (131072 x 384 in 16 groups 194 us, 168 without them).
+// Equal logits with equal biases tie exactly, and where no bias differs from another the
+// order of the logits is that of the keys; neither is left open.
 //
 // One warp a token, as in the gate (gate_kernels.cu, whose list of candidates this is).
 // The groups' two largest keys: 32 / G lanes a group walk its keys in shared memory.
+#include <cfloat>
+
 #include "gate_common.cuh"
 
 namespace moe {
@@ -28,324 +31,549 @@ namespace {
 constexpr float kErrSigmoid = 0x1p-20f;
 constexpr float kErrSoftmax = 0x1p-18f;
 
-struct Pick64 {
-  double key;
-  int id;
+// Numbers as sums of two floats, good to about 2^-46: hi is the sum rounded, lo the rest.
+// (The 64-bit unit does 2 multiply-adds a cycle and SM; a token redone with it took 40 us.)
+// Intrinsics, so that no addition is fused with a product.
+struct Two {
+  float hi, lo;
 };
-__device__ __forceinline__ Pick64 warp_best(Pick64 p) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double k = __shfl_xor_sync(kFull, p.key, o);
-    const int id = __shfl_xor_sync(kFull, p.id, o);
-    if (k > p.key || (k == p.key && id < p.id)) p.key = k, p.id = id;
-  }
-  return p;
+__device__ __forceinline__ Two quick_sum(float a, float b) {   // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two exact_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const Two s = exact_sum(a.hi, b.hi);
+  return quick_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  const float e = __fmaf_rn(a.hi, b.hi, -p);
+  return quick_sum(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, e)));
+}
+__device__ __forceinline__ Two reciprocal(Two d) {
+  const float q = __frcp_rn(d.hi);
+  const float rest = __fmaf_rn(-q, d.lo, __fmaf_rn(-q, d.hi, 1.0f));
+  return quick_sum(q, __fmul_rn(rest, q));
+}
+// e^x, x <= 0: x = n ln 2 + r, the Taylor series of e^r (its terms from r^7 on need one float),
+// times 2^n.  ln 2 comes in three parts, of which n times the first two is exact.  Below
+// 2^-125 zero.
+__device__ __forceinline__ Two two_exp(Two x) {
+  if (!(x.hi > -86.0f)) return {0.0f, 0.0f};
+  const float n = rintf(x.hi * 1.4426950408889634f);
+  const Two a = exact_sum(__fmaf_rn(-n, 0x1.62e4p-1f, x.hi), __fmul_rn(-n, 0x1.7f7cp-20f));
+  const Two r = quick_sum(a.hi, __fadd_rn(a.lo, __fmaf_rn(-n, 0x1.1cf79ap-36f, x.lo)));
+  float q = 1.0f / 479001600.0f;
+  q = fmaf(q, r.hi, 1.0f / 39916800.0f);
+  q = fmaf(q, r.hi, 1.0f / 3628800.0f);
+  q = fmaf(q, r.hi, 1.0f / 362880.0f);
+  q = fmaf(q, r.hi, 1.0f / 40320.0f);
+  q = fmaf(q, r.hi, 1.0f / 5040.0f);
+  Two p = add(mul(r, {q, 0.0f}), {0x1.6c16c2p-10f, -0x1.27d27ep-35f});   // 1/720
+  p = add(mul(r, p), {0x1.111112p-7f, -0x1.dddddep-32f});                // 1/120
+  p = add(mul(r, p), {0x1.555556p-5f, -0x1.555556p-30f});                // 1/24
+  p = add(mul(r, p), {0x1.555556p-3f, -0x1.555556p-28f});                // 1/6
+  p = add(mul(r, p), {0.5f, 0.0f});
+  p = add(mul(r, p), {1.0f, 0.0f});
+  p = add(mul(r, p), {1.0f, 0.0f});
+  const float scale = __uint_as_float(static_cast<unsigned>(static_cast<int>(n) + 127) << 23);
+  return {p.hi * scale, p.lo * scale};
+}
+__device__ __forceinline__ Two two_sigmoid(float l) {
+  const Two e = two_exp({-fabsf(l), 0.0f});
+  const Two s = reciprocal(add({1.0f, 0.0f}, e));
+  return l >= 0.0f ? s : mul(e, s);
 }
 
-// The token's picks in 64 bits: lane k < K gets pick k's id, or -1.  `key` is the warp's.
+// Keys of two floats as integers in their order; 0 is none.
+__device__ __forceinline__ uint64_t ordered(Two k) {
+  return static_cast<uint64_t>(sortable(k.hi + 0.0f)) << 32 | sortable(k.lo + 0.0f);
+}
+__device__ __forceinline__ Two number(uint64_t u) {
+  return {unsortable(static_cast<unsigned>(u >> 32)), unsortable(static_cast<unsigned>(u))};
+}
+__device__ __forceinline__ Two plus_bias(Two s, float b) {
+  const Two k = exact_sum(s.hi, b);
+  return quick_sum(k.hi, __fadd_rn(k.lo, s.lo));
+}
+// The largest of the lanes' keys.
+__device__ __forceinline__ uint64_t warp_best(uint64_t key) {
+  const unsigned hi = __reduce_max_sync(kFull, static_cast<unsigned>(key >> 32));
+  const unsigned lo = __reduce_max_sync(kFull, static_cast<unsigned>(key >> 32) == hi ? static_cast<unsigned>(key) : 0u);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// One over the softmax's sum (sigmoid: 1).
 template <typename T, bool SIGMOID>
-__device__ __noinline__ int choose_exact(const T* row, float m, const float* bias, double* key, int E, int K, int G,
-                                         int topk_groups, int group_sum, bool biased) {
-  const int lane = threadIdx.x % 32;
-  const double none = -INFINITY;
-  double sum = 0.0;
-  for (int e = lane; e < E; e += 32) {
-    const double l = static_cast<double>(load_logit(row + e));
-    const double s = SIGMOID ? 1.0 / (1.0 + exp(-l)) : exp(l - static_cast<double>(m));
-    sum += s;
-    key[e] = s;
-  }
-  if (!SIGMOID) {
+__device__ __forceinline__ Two exact_scale(const T* row, float m, int E) {
+  if (SIGMOID) return {1.0f, 0.0f};
+  Two sum{0.0f, 0.0f};
+#pragma unroll 2
+  for (int e = threadIdx.x % 32; e < E; e += 32) sum = add(sum, two_exp(exact_sum(load_logit(row + e), -m)));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  for (int o = 16; o > 0; o >>= 1) sum = add(sum, {__shfl_xor_sync(kFull, sum.hi, o), __shfl_xor_sync(kFull, sum.lo, o)});
+  return reciprocal(sum);
+}
+template <typename T, bool SIGMOID>
+__device__ __forceinline__ uint64_t exact_key(const T* row, float m, Two scale, const float* bias, int e) {
+  const float l = load_logit(row + e), b = bias[e];
+  const Two s = SIGMOID ? two_sigmoid(l) : mul(two_exp(exact_sum(l, -m)), scale);
+  return l > -INFINITY && b > -INFINITY ? ordered(plus_bias(s, b)) : 0;
+}
+
+// How many of `found` <= 32 candidates, a lane each, come before the lane's.
+template <typename T, bool SIGMOID>
+__device__ __noinline__ int exact_rank(const T* row, float m, const float* bias, int E, int id, int found) {
+  const Two scale = exact_scale<T, SIGMOID>(row, m, E);
+  const uint64_t own = threadIdx.x % 32 < found ? exact_key<T, SIGMOID>(row, m, scale, bias, id) : 0;
+  int before = 0;
+  for (int j = 0; j < found; ++j) {
+    const uint64_t k = __shfl_sync(kFull, own, j);
+    const int other = __shfl_sync(kFull, id, j);
+    before += k > own || (k == own && other < id);
   }
-  for (int e = lane; e < E; e += 32) {
-    const double s = SIGMOID ? key[e] : key[e] / sum;
-    key[e] = load_logit(row + e) > -INFINITY ? s + static_cast<double>(bias[e]) : none;
-  }
+  return before;
+}
+
+// A token's picks from such keys: lane k < K gets pick k's id, or -1.  `key` is the warp's,
+// [E]; `m` the row's largest logit.
+template <typename T, bool SIGMOID>
+__device__ __noinline__ int exact_picks(const GateArgs& a, const T* row, float m, const float* bias, bool biased, uint64_t* key) {
+  const int lane = threadIdx.x % 32;
+  const int E = a.num_experts, per = E / a.num_groups;
+  const Two scale = exact_scale<T, SIGMOID>(row, m, E);
+#pragma unroll 2
+  for (int e = lane; e < E; e += 32) key[e] = exact_key<T, SIGMOID>(row, m, scale, bias, e);
   __syncwarp();
-  unsigned kept = kFull;
-  const int per = E / G;
-  if (topk_groups < G) {
-    Pick64 own{none, lane};
-    if (lane < G) {
-      double hi = none, lo = none;
-      for (int e = lane * per; e < (lane + 1) * per; ++e) {
-        const double k = key[e];
-        if (k > hi) lo = hi, hi = k;
-        else if (k > lo) lo = k;
+  if (a.topk_groups < a.num_groups) {
+    uint64_t score = 0;                  // of group `lane`
+    if (lane < a.num_groups) {
+      uint64_t hi = 0, lo = 0;
+#pragma unroll 4
+      for (int j = 0; j < per; ++j) {
+        const uint64_t k = key[lane * per + j];
+        lo = max(lo, min(hi, k));
+        hi = max(hi, k);
       }
-      own.key = group_sum == 2 && lo > none ? hi + lo : hi;
+      score = a.group_sum == 2 && lo > 0 ? ordered(add(number(hi), number(lo))) : hi;
     }
-    kept = 0;
-    for (int j = 0; j < topk_groups; ++j) {
-      const Pick64 best = warp_best(own);
-      if (!(best.key > none)) break;
-      kept |= 1u << best.id;
-      if (lane == best.id) own.key = none;
+    unsigned kept = 0;
+    for (int j = 0; j < a.topk_groups; ++j) {
+      const uint64_t best = warp_best(score);
+      if (best == 0) break;
+      const int g = __ffs(__ballot_sync(kFull, score == best)) - 1;
+      kept |= 1u << g;
+      if (lane == g) score = 0;
     }
-  }
-  if (!biased) {
     __syncwarp();
-    for (int e = lane; e < E; e += 32) key[e] = static_cast<double>(load_logit(row + e));
-    __syncwarp();
+    for (int e = lane; e < E; e += 32) {
+      if (!(kept >> (e / per) & 1)) key[e] = 0;
+      else if (!biased && key[e] > 0) key[e] = static_cast<uint64_t>(sortable(load_logit(row + e) + 0.0f)) << 32;
+    }
   }
   int mine = -1;
-  for (int k = 0; k < K; ++k) {
-    Pick64 own{none, E};
+  for (int k = 0; k < a.topk; ++k) {
+    __syncwarp();
+    uint64_t own = 0;
+    unsigned id = kFull;
+#pragma unroll 4
     for (int e = lane; e < E; e += 32)
-      if (key[e] > own.key && (kept >> (e / per) & 1)) own.key = key[e], own.id = e;
-    const Pick64 best = warp_best(own);
-    if (!(best.key > none)) break;
-    if (lane == k) mine = best.id;
-    __syncwarp();
-    if (lane == 0) key[best.id] = none;
-    __syncwarp();
+      if (key[e] > own) own = key[e], id = e;
+    const uint64_t best = warp_best(own);
+    if (best == 0) break;
+    id = __reduce_min_sync(kFull, own == best ? id : kFull);
+    if (lane == k) mine = static_cast<int>(id);
+    if (id % 32 == lane) key[id] = 0;
   }
   __syncwarp();
   return mine;
 }
 
-template <int VPL, typename T, bool SIGMOID, bool VEC>
-__global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2) route_forward_kernel(GateArgs a) {
+// The column of a lane's i-th value: V side by side (BLOCKED), or 32 apart.
+template <int V, bool BLOCKED>
+__device__ __forceinline__ int route_column(int lane, int i) {
+  return BLOCKED ? lane * V + i : lane + 32 * i;
+}
+template <int V, typename T, bool BLOCKED>
+__device__ __forceinline__ void load_route_row(const T* row, bool live, int lane, int E, float* l) {
+  constexpr int kStep = BLOCKED && V % 4 == 0 ? 4 : 1;
+#pragma unroll
+  for (int i = 0; i < V; i += kStep) {
+    const int col = route_column<V, BLOCKED>(lane, i);
+#pragma unroll
+    for (int j = 0; j < kStep; ++j) l[i + j] = -INFINITY;
+    if (live && col < E) {
+      if constexpr (kStep == 4) load4(row + col, l + i);
+      else l[i] = load_logit(row + col);
+    }
+  }
+}
+
+__device__ __forceinline__ void add_best(float& hi, float& lo, float k) {
+  lo = fmaxf(lo, fminf(hi, k));
+  hi = fmaxf(hi, k);
+}
+// The two largest of a lane's and another's two largest.
+__device__ __forceinline__ void merge_best(float& hi, float& lo, float h2, float l2) {
+  lo = fmaxf(fmaxf(lo, l2), fminf(hi, h2));
+  hi = fmaxf(hi, h2);
+}
+
+template <int V, typename T, bool SIGMOID, bool BLOCKED>
+__global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) route_forward_kernel(GateArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int E = a.num_experts, K = a.topk, G = a.num_groups, per = E / G;
+  constexpr bool kAhead = V <= 16;       // the next token's row is loaded a token ahead
   __shared__ bool last_s;
   __shared__ uint64_t list_s[kGateWarps][32];
-  __shared__ float list_l_s[kGateWarps][32];
   __shared__ float red_s[kGateWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   uint64_t* list = list_s[warp];
-  float* list_l = list_l_s[warp];
-  // a warp's keys: 32 bits each for the groups, 64 where they are done again
-  double* key64 = reinterpret_cast<double*>(smem) + static_cast<size_t>(warp) * (32 * VPL);
-  float* key_s = reinterpret_cast<float*>(key64);
-  float* sum_s = reinterpret_cast<float*>(reinterpret_cast<double*>(smem) + kGateWarps * 32 * VPL);   // [E]
-  int* cnt_s = reinterpret_cast<int*>(sum_s) + E;   // [E + 1]: picks of each expert, routed tokens
-  float* bias_s = sum_s + 2 * E + 1;                // [32 * VPL]
+  uint64_t* key64 = reinterpret_cast<uint64_t*>(smem) + static_cast<size_t>(warp) * (32 * V);   // for exact_picks
+  float* key_s = reinterpret_cast<float*>(key64);                                                // for groups not BLOCKED
+  float* sum_s = reinterpret_cast<float*>(reinterpret_cast<uint64_t*>(smem) + kGateWarps * 32 * V);   // [E]
+  float* bias_s = sum_s + 32 * V;                   // [32 * V]
+  int* cnt_s = reinterpret_cast<int*>(bias_s + 32 * V);   // [E + 1]: picks of each expert, routed tokens
   for (int e = threadIdx.x; e < E; e += kGateThreads) sum_s[e] = 0.0f;
   for (int e = threadIdx.x; e <= E; e += kGateThreads) cnt_s[e] = 0;
   ptx::grid_dependency_wait();
-  // biases that are all the same number change no order
-  bool differ = false;
-  for (int e = threadIdx.x; e < 32 * VPL; e += kGateThreads) {
+  // Biases that are all the same number change no order.  Others than numbers close experts
+  // (-inf) or spoil the tokens that have them open (NaN, +inf).
+  bool differ = false, odd = false;
+  for (int e = threadIdx.x; e < 32 * V; e += kGateThreads) {
     const float b = a.bias != nullptr && e < E ? a.bias[e] : 0.0f;
     bias_s[e] = b;
-    differ |= a.bias != nullptr && e < E && (!(b == a.bias[0]) || !(fabsf(b) < INFINITY));
+    if (a.bias != nullptr && e < E) {
+      differ |= b != a.bias[0];
+      odd |= !(fabsf(b) < INFINITY);
+    }
   }
-  const bool biased = __syncthreads_or(differ);
+  const bool check_keys = __syncthreads_or(odd), biased = __syncthreads_or(differ) || check_keys;
 
-  // lanes of a group, and where each starts in it: apart, so that groups meet no bank together
   const bool limited = a.topk_groups < G;
-  int lanes = 32;
-  while (lanes * G > 32) lanes /= 2;
+  const bool by_logit = !biased && a.group_sum == 1;   // a group's score is in the order of its best logit
+  // Lanes of a group (BLOCKED: those that hold it), the lane's group, its place there.
+  int lanes = BLOCKED ? max(1, per / V) : 32;
+  if (!BLOCKED)
+    while (lanes * G > 32) lanes /= 2;
   const int group = lane / lanes, sub = lane % lanes;
-  const int turn = limited ? (group * lanes) % per : 0;
+  const int turn = limited && !BLOCKED ? (group * lanes) % per : 0;   // groups start apart, so that they meet no bank together
   const unsigned inverse = (0x400000u + per - 1) / per;   // e / per = e * inverse >> 22 for e < 1024
 
-  float acc[VPL];
+  // Where a token's choice is left open, its first id says so until the loop is over.
+  // One token's whose candidates are listed waits in registers instead.
+  constexpr int64_t kOpen = -2;
+  bool any_open = false;
+  int64_t late = 0;
+  int late_found = 0;
+  float late_m = 0.0f;
+  int* late_ids = reinterpret_cast<int*>(key64) + 32 * V;   // past the groups' keys
+  // Keys from `guess` on are candidates, if between K and 32 reach it: a little below the
+  // K-th best key of the token before.
+  float guess = INFINITY, slack = 0.0f;
+
+  float acc[V];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
   const T* logits = static_cast<const T*>(a.logits);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
   int routed = 0;
-  float next[VPL];
-  load_row<VPL, T, VEC>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
+  float next[V];
+  if (kAhead) load_route_row<V, T, BLOCKED>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
   for (; t < a.num_tokens; t += stride) {
     const T* row = logits + t * a.logits_stride;
-    float l[VPL];
-    unsigned u[VPL];
+    float key[V], s[V];                  // key: first the logit
+    if (kAhead) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) l[i] = next[i];
-    load_row<VPL, T, VEC>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
-
-    // The addition turns -0 into +0 and any NaN into the one that sorts above +inf.
-    unsigned best = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      u[i] = sortable(l[i] + 0.0f);
-      best = max(best, u[i]);
+      for (int i = 0; i < V; ++i) key[i] = next[i];
+      load_route_row<V, T, BLOCKED>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
+    } else {
+      load_route_row<V, T, BLOCKED>(row, true, lane, E, key);
     }
-    unsigned top = __reduce_max_sync(kFull, best);
-    bool bad = top >= kKeyInf;
-    bool route = !bad && top > kKeyNegInf;
-    int mine = -1, slot = lane;            // this lane's pick and its place among the K
+    float m = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = fmaxf(m, key[i]);
+    m = unsortable(__reduce_max_sync(kFull, sortable(m + 0.0f)));
+
+    // Scores; a NaN among the logits shows in their sum.  (What they err by is no matter for
+    // the means, and the picks' weights come from better ones.)
+    float sum = 0.0f;
+    const float finite = fmaxf(m, -FLT_MAX);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float x = (SIGMOID ? -key[i] : key[i] - finite) * 1.4426950408889634f;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s[i]) : "f"(x));
+      if (SIGMOID) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[i]) : "f"(1.0f + s[i]));
+      sum += s[i];
+    }
+    sum = warp_sum(sum);
+    bool bad = !(m < INFINITY) || !(sum < INFINITY);
+    bool route = !bad && m > -INFINITY;
+    int64_t mine = -1;                   // this lane's pick
+    int slot = lane;                     // and its place among the K
     float w = 0.0f;
     if (route) {
-      float m = unsortable(top);
-      const float m0 = m;
-      bool tiny;
-      const float inv = __fdividef(1.0f, scores<VPL, T, SIGMOID, VEC>(l, m, tiny, row, lane, E));
-      const float factor = SIGMOID ? (tiny ? exp_neg(m0) : 1.0f) : inv;   // to the score itself
-      const float most = SIGMOID ? sigmoid(m0) : inv;
-      const float err = (SIGMOID ? kErrSigmoid * fminf(most, 0.5f) : kErrSoftmax * most) + 0x1p-120f;
-      bool exact = false;                  // some decision lies within the errors
+      float factor = SIGMOID ? 1.0f : __fdividef(1.0f, sum);       // of s to the score
+      if (SIGMOID && sum < kTinySum) {   // sigmoids that are e^l to 2^-30: e^(l - m) in their place
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += s[i] = exp_neg(key[i] - m);
+        sum = warp_sum(sum);
+        factor = exp_neg(m);
+      }
+      const float inv = __fdividef(1.0f, sum);
+      float b[V];
+      if (biased || limited) {
+        if constexpr (BLOCKED && V % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < V; i += 4) load4(bias_s + lane * V + i, b + i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) b[i] = bias_s[route_column<V, BLOCKED>(lane, i)];
+        }
+      }
+      if (check_keys) {
+        bool open = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (key[i] > -INFINITY) open |= b[i] != -INFINITY, bad |= !(b[i] < INFINITY);
+        bad = __any_sync(kFull, bad);
+        route = __any_sync(kFull, open) && !bad;
+      }
+      if (route)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += s[i] * inv;
 
-      if (biased) {
-        best = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const float key = fmaf(l[i], factor, bias_s[column<VEC>(lane, i)]);
-          u[i] = u[i] > kKeyNegInf ? sortable(key + 0.0f) : kKeyNegInf;
-          best = max(best, u[i]);
-        }
-        top = __reduce_max_sync(kFull, best);
-        bad = top >= kKeyInf;
-        route = !bad && top > kKeyNegInf;
-      }
-      if (route && limited) {
-        const bool by_logit = !biased && a.group_sum == 1;   // the best key is the best logit's
-#pragma unroll
-        for (int i = 0; i < VPL; i += VEC ? 4 : 1) {
-          float k[4];
-#pragma unroll
-          for (int j = 0; j < (VEC ? 4 : 1); ++j)
-            k[j] = u[i + j] <= kKeyNegInf ? -INFINITY
-                   : biased || by_logit   ? unsortable(u[i + j])
-                                          : fmaf(l[i + j], factor, bias_s[column<VEC>(lane, i + j)]);
-          if constexpr (VEC) store4(key_s + column<VEC>(lane, i), k);
-          else key_s[column<VEC>(lane, i)] = k[0];
-        }
-        __syncwarp();
-        float hi = -INFINITY, lo = -INFINITY;
-        if (group < G)
-          for (int j = sub; j < per; j += lanes) {
-            int at = j + turn;
-            if (at >= per) at -= per;
-            const float k = key_s[group * per + at];
-            lo = fmaxf(lo, fminf(hi, k));
-            hi = fmaxf(hi, k);
-          }
-        for (int o = lanes / 2; o > 0; o /= 2) {
-          const float h2 = __shfl_xor_sync(kFull, hi, o), l2 = __shfl_xor_sync(kFull, lo, o);
-          lo = fmaxf(fmaxf(lo, l2), fminf(hi, h2));
-          hi = fmaxf(hi, h2);
-        }
-        const float score = a.group_sum == 2 && lo > -INFINITY ? hi + lo : hi;
-        const float off = 2.0f * err + 0x1p-23f * (fabsf(hi) + (lo > -INFINITY ? fabsf(lo) : 0.0f));
-        unsigned rest = group < G ? sortable(score + 0.0f) : kKeyNegInf, kept = 0;
-        unsigned last = 0;
-        float worst = 0.0f;                // of the bounds
-        for (int j = 0; j < a.topk_groups; ++j) {
-          const unsigned b = __reduce_max_sync(kFull, rest);
-          if (b <= kKeyNegInf) break;
-          const int g = (__ffs(__ballot_sync(kFull, rest == b)) - 1) / lanes;
-          kept |= 1u << g;
-          last = b;
-          if (group == g) rest = kKeyNegInf, worst = off;
-        }
-        const unsigned out = __reduce_max_sync(kFull, rest);
-        if (out > kKeyNegInf && !by_logit) {
-          if (rest == out) worst = fmaxf(worst, off);
-          worst = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(worst)));
-          exact = unsortable(last) - unsortable(out) <= 2.0f * worst;
-        }
-        best = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const unsigned g = static_cast<unsigned>(column<VEC>(lane, i)) * inverse >> 22;
-          if (!(kept >> (g & 31) & 1)) u[i] = min(u[i], kKeyNegInf);
-          best = max(best, u[i]);
-        }
-        top = __reduce_max_sync(kFull, best);
-        __syncwarp();                      // the keys are read
-      }
-      // Two keys closer than this may be in either order.
+      // What a key may err by, but for its own rounding.
+      const float most = SIGMOID ? sigmoid(m) : factor;
+      const float err = (SIGMOID ? kErrSigmoid * fminf(most, 0.25f) : kErrSoftmax * most) + 0x1p-120f;
       const auto near = [&](float x, float y) {
         return biased && fabsf(x - y) <= 2.0f * err + 0x1p-23f * fmaxf(fabsf(x), fabsf(y));
       };
-      float picked = 0.0f;                 // the pick's logit
-      if (route && !exact) {
-        // The K-th largest lane maximum (equal ones go together: a lower bound still).
-        unsigned floor = top;
-        {
-          unsigned rest = best;
-          for (int k = 1; k < K && floor > kKeyNegInf; ++k) {
-            if (rest == floor) rest = 0;
-            floor = __reduce_max_sync(kFull, rest);
-          }
-          if (biased && floor > kKeyNegInf) {
-            const float f = unsortable(floor);
-            floor = sortable(f - (2.0f * err + 0x1p-22f * fabsf(f)));
-          }
-          floor = max(floor, kKeyNegInf + 1);
-        }
-        int found = 0;
+      bool exact = false;                  // the choice is left open
+      float hi = -INFINITY, lo = -INFINITY;   // the lane's largest keys
+      if (limited && !by_logit) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const unsigned who = __ballot_sync(kFull, u[i] >= floor);
-          if (who == 0) continue;
-          if (u[i] >= floor) {
-            const int at = found + __popc(who & ptx::lanemask_lt());
-            if (at < 32) list[at] = static_cast<uint64_t>(u[i]) << 32 | ~static_cast<unsigned>(column<VEC>(lane, i));
-          }
-          found += __popc(who);
+        for (int i = 0; i < V; ++i) {
+          const float k = key[i] > -INFINITY ? fmaf(s[i], factor, b[i]) : -INFINITY;
+          if (BLOCKED) add_best(hi, lo, k);
+          else key_s[route_column<V, BLOCKED>(lane, i)] = k;
+          if (biased) key[i] = k;
         }
-        __syncwarp();
-        if (found <= 32) {
-          const uint64_t own = lane < found ? list[lane] : 0;
-          const int id = static_cast<int>(~static_cast<unsigned>(own));
-          picked = lane < found ? (biased ? load_logit(row + id) : unsortable(static_cast<unsigned>(own >> 32))) : 0.0f;
-          int before = 0;
-#pragma unroll 4
-          for (int j = 0; j < found; ++j) before += list[j] > own;
-          if (lane < found) {
-            if (before < K) mine = id;
-            slot = before;
-          }
-          if (biased) {
-            __syncwarp();                  // the list is read
-            if (lane < found) list[before] = own, list_l[before] = picked;
-            __syncwarp();
-            if (mine >= 0 && before + 1 < found) {
-              const uint64_t follow = list[before + 1];
-              const int other = static_cast<int>(~static_cast<unsigned>(follow));
-              if (near(unsortable(static_cast<unsigned>(own >> 32)), unsortable(static_cast<unsigned>(follow >> 32))))
-                exact = picked != list_l[before + 1] || bias_s[id] != bias_s[other];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (biased) key[i] = key[i] > -INFINITY ? fmaf(s[i], factor, b[i]) : -INFINITY;
+          if (limited && !BLOCKED) key_s[route_column<V, BLOCKED>(lane, i)] = key[i];
+          hi = fmaxf(hi, key[i]);
+        }
+      }
+      float own_hi = hi, own_lo = lo;      // of the lane's keys, for the choice
+      bool held = true;                  // the lane's experts (BLOCKED) are of a kept group
+      unsigned kept = kFull;
+      if (limited) {
+        if (BLOCKED) {
+          if ((lanes & (lanes - 1)) == 0) {
+            for (int o = lanes / 2; o > 0; o /= 2)
+              merge_best(hi, lo, __shfl_xor_sync(kFull, hi, o), __shfl_xor_sync(kFull, lo, o));
+          } else {
+            const float h1 = hi, l1 = lo;
+            for (int j = 1; j < lanes; ++j) {
+              const int from = group * lanes + (sub + j >= lanes ? sub + j - lanes : sub + j);
+              merge_best(hi, lo, __shfl_sync(kFull, h1, from & 31), __shfl_sync(kFull, l1, from & 31));
             }
           }
         } else {
-          float last_key = INFINITY, last_l = 0.0f, last_b = 0.0f;
-          for (int k = 0; k <= K && top > kKeyNegInf; ++k) {
-            unsigned lowest = kFull;
-#pragma unroll
-            for (int i = VPL - 1; i >= 0; --i)
-              if (u[i] == top) lowest = static_cast<unsigned>(column<VEC>(lane, i));
-            const unsigned id = __reduce_min_sync(kFull, lowest);
-            const float lk = load_logit(row + id), bk = bias_s[id], key = unsortable(top);
-            if (near(last_key, key) && (lk != last_l || bk != last_b)) exact = true;
-            last_key = key, last_l = lk, last_b = bk;
-            if (lane == k && k < K) mine = static_cast<int>(id), picked = lk;
-            best = 0;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-              if (column<VEC>(lane, i) == static_cast<int>(id)) u[i] = 0;
-              best = max(best, u[i]);
+          __syncwarp();
+          hi = lo = -INFINITY;
+          if (group < G)
+            for (int j = sub; j < per; j += lanes) {
+              int at = j + turn;
+              if (at >= per) at -= per;
+              add_best(hi, lo, key_s[group * per + at]);
             }
-            top = __reduce_max_sync(kFull, best);
+          for (int o = lanes / 2; o > 0; o /= 2)
+            merge_best(hi, lo, __shfl_xor_sync(kFull, hi, o), __shfl_xor_sync(kFull, lo, o));
+          __syncwarp();                  // the keys are read
+        }
+        const float score = group < G ? (a.group_sum == 2 && lo > -INFINITY ? hi + lo : hi) : -INFINITY;
+        const float off = by_logit ? 0.0f : 2.0f * err + 0x1p-23f * (fabsf(hi) + (lo > -INFINITY ? fabsf(lo) : 0.0f));
+        unsigned rest = sortable(score + 0.0f);
+        kept = 0;
+        held = false;
+        for (int j = 0; j < a.topk_groups; ++j) {
+          const unsigned best = __reduce_max_sync(kFull, rest);
+          if (best <= kKeyNegInf) break;
+          const int g = (__ffs(__ballot_sync(kFull, rest == best)) - 1) / lanes;
+          kept |= 1u << g;
+          if (group == g) rest = kKeyNegInf, held = true;
+        }
+        if (!by_logit) {
+          // What a group left may reach, and the least that a kept one may be.
+          const bool there = score > -INFINITY;
+          const unsigned reach = __reduce_max_sync(kFull, there && !held ? sortable(score + off) : 0u);
+          const unsigned least = __reduce_min_sync(kFull, held ? sortable(score - off) : kFull);
+          exact = reach >= least;
+        }
+        if (!BLOCKED)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const unsigned g = static_cast<unsigned>(route_column<V, BLOCKED>(lane, i)) * inverse >> 22;
+            if (!(kept >> (g & 31) & 1)) key[i] = -INFINITY;
+          }
+        else if (!held)
+          own_hi = own_lo = -INFINITY;
+      }
+      // Few lanes have keys left, or many picks are wanted: a lane's second counts too.
+      if ((limited && !(BLOCKED && biased && !by_logit)) || (!limited && K > 8)) {
+        own_hi = own_lo = -INFINITY;
+        if (!BLOCKED || held)
+#pragma unroll
+          for (int i = 0; i < V; ++i) add_best(own_hi, own_lo, key[i]);
+      }
+      if (route && !exact) {
+        const auto mark = [&](float least) {
+          unsigned bits = 0;
+          if (!BLOCKED || held)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (key[i] >= least) bits |= 1u << i;
+          return bits;
+        };
+        // How many are marked in all and by the lanes before this one.
+        int found, at;
+        const auto count = [&](unsigned bits) {
+          const int c = __popc(bits);
+          found = at = 0;
+#pragma unroll
+          for (int j = 0; (1 << j) <= V; ++j) {
+            const unsigned who = __ballot_sync(kFull, c >> j & 1);
+            found += __popc(who) << j;
+            at += __popc(who & ptx::lanemask_lt()) << j;
+          }
+        };
+        unsigned bits = mark(guess);
+        count(bits);
+        unsigned top = 0;
+        float edge = guess;              // what is not marked lies below it
+        const bool few = found < K, many = found > 32;
+        if (few || many) {
+          // The K-th largest of the lanes' largest (equal ones of two lanes go together: a
+          // lower bound still), less what it may err by.
+          unsigned rest = sortable(own_hi + 0.0f), second = sortable(own_lo + 0.0f);
+          top = __reduce_max_sync(kFull, rest);
+          unsigned floor = top;
+          for (int k = 1; k < K && floor > kKeyNegInf; ++k) {
+            if (rest == floor) rest = second, second = 0;
+            floor = __reduce_max_sync(kFull, rest);
+          }
+          float least = -FLT_MAX;
+          if (floor > kKeyNegInf) {
+            least = unsortable(floor);
+            if (biased) least -= 2.0f * err + 0x1p-22f * fabsf(least);
+          }
+          bits = mark(least);
+          count(bits);
+          edge = -FLT_MAX;               // further below
+        }
+        float picked = 0.0f;             // the pick's logit
+        int candidate = 0;
+        if (found <= 32) {
+          int* ids = reinterpret_cast<int*>(list);
+          for (; bits != 0; bits &= bits - 1) ids[at++] = route_column<V, BLOCKED>(lane, __ffs(bits) - 1);
+          __syncwarp();
+          const int id = lane < found ? ids[lane] : 0;
+          const float l = lane < found ? load_logit(row + id) : 0.0f;
+          const float bias = bias_s[id];
+          __syncwarp();
+          const float k = !biased ? l : (SIGMOID ? sigmoid(l) : exp_neg(l - m) * factor) + bias;
+          const uint64_t own = lane < found ? static_cast<uint64_t>(sortable(k + 0.0f)) << 32 | ~static_cast<unsigned>(id) : 0;
+          list[lane] = own;
+          __syncwarp();
+          int before = 0;
+#pragma unroll 4
+          for (int j = 0; j < found; ++j) before += list[j] > own;
+          float* sorted = reinterpret_cast<float*>(list);        // keys in order, and their ids
+          int* sorted_id = reinterpret_cast<int*>(list) + 32;
+          __syncwarp();
+          if (lane < found) sorted[before] = k, sorted_id[before] = id;
+          __syncwarp();
+          if (biased && lane < found && before < K) {
+            if (before + 1 == found) {
+              exact = near(k, edge);
+            } else if (near(k, sorted[before + 1])) {
+              const int other = sorted_id[before + 1];
+              exact = load_logit(row + other) != l || bias_s[other] != bias;
+            }
+          }
+          if (found >= K) {
+            const float last = sorted[K - 1];
+            if (few) slack = fmaxf(2.0f * slack, 0x1p-4f * (sorted[0] - last) + 0x1p-8f * fabsf(last));
+            else if (many) slack *= 0.5f;
+            else if (found > 20) slack *= 0.75f;
+            guess = last - slack;
+          }
+          candidate = id;
+          if (lane < found) {
+            if (before < K) mine = id, picked = l;
+            slot = before;
+          }
+        } else {
+          float last_key = INFINITY, last_l = 0.0f, last_b = 0.0f;
+          float h;
+          for (int k = 0; k <= K && top > kKeyNegInf; ++k) {
+            const float want = unsortable(top);
+            unsigned lowest = kFull;
+            if (!BLOCKED || held)
+#pragma unroll
+              for (int i = V - 1; i >= 0; --i)
+                if (key[i] == want) lowest = static_cast<unsigned>(route_column<V, BLOCKED>(lane, i));
+            const unsigned id = __reduce_min_sync(kFull, lowest);
+            const float lk = load_logit(row + id), bk = bias_s[id];
+            if (near(last_key, want) && (lk != last_l || bk != last_b)) exact = true;
+            last_key = want, last_l = lk, last_b = bk;
+            if (lane == k && k < K) mine = id, picked = lk;
+            h = -INFINITY;
+            if (!BLOCKED || held)
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                if (route_column<V, BLOCKED>(lane, i) == static_cast<int>(id)) key[i] = -INFINITY;
+                h = fmaxf(h, key[i]);
+              }
+            top = __reduce_max_sync(kFull, sortable(h + 0.0f));
           }
         }
-        __syncwarp();                      // the list is read
-      }
-      if (route && __any_sync(kFull, exact)) {
-        mine = choose_exact<T, SIGMOID>(row, m0, bias_s, key64, E, K, G, a.topk_groups, a.group_sum, biased);
-        picked = mine >= 0 ? load_logit(row + mine) : 0.0f;
-        slot = lane;
-      }
-      if (route) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] += l[i] * inv;
-        ++routed;
+        __syncwarp();                    // the list is read
+        exact = __any_sync(kFull, exact);
+        if (exact) {
+          mine = -1;
+          if (found <= 32 && late_found == 0) {
+            late = t, late_found = found, late_m = m;
+            if (lane < found) late_ids[slot] = candidate;
+            exact = false;
+            slot = 32;                   // nothing is written yet
+          }
+        }
         const bool pick = mine >= 0;
         if (pick) atomicAdd(&cnt_s[mine], 1);
-        float s = 0.0f;
-        if (pick && (SIGMOID || !a.normalize)) s = SIGMOID ? sigmoid(picked) : exp_neg(picked - m) * inv;
+        float p = 0.0f;
+        if (pick && (SIGMOID || !a.normalize)) p = SIGMOID ? sigmoid(picked) : exp_neg(picked - m) * inv;
         if (a.normalize) {
           const float top_pick = SIGMOID ? m : unsortable(__reduce_max_sync(kFull, pick ? sortable(picked) : 0u));
-          s = share_of_picks<SIGMOID>(pick, picked, s, top_pick);
+          p = share_of_picks<SIGMOID>(pick, picked, p, top_pick);
         }
-        w = a.scale * s;
+        w = a.scale * p;
+      }
+      if (route) ++routed;
+      if (exact) {
+        any_open = true;
+        slot = lane;
+        if (lane == 0) mine = kOpen;
       }
     }
     if (bad && lane == 0) set_error(a.err, MOE_ERR_INVALID_ARG);
@@ -354,27 +582,71 @@ __global__ void __launch_bounds__(kGateThreads, VPL <= 8 ? 4 : VPL <= 12 ? 3 : 2
       a.weights[t * K + slot] = w;
     }
   }
-  finish_sums<VPL, VEC>(a, acc, routed, sum_s, cnt_s, red_s, last_s);
+  __syncwarp();
+  // Choices left open, from exact keys.
+  const auto settle = [&](int64_t tok, float m, int mine, int slot) {
+    const T* row = logits + tok * a.logits_stride;
+    const bool pick = mine >= 0;
+    const float picked = pick ? load_logit(row + mine) : 0.0f;
+    float p = 0.0f;
+    if (pick) atomicAdd(&cnt_s[mine], 1);
+    if (SIGMOID) {
+      if (pick) p = sigmoid(picked);
+    } else if (!a.normalize) {
+      float sum = 0.0f;
+      for (int e = lane; e < E; e += 32) sum += exp_neg(load_logit(row + e) - m);
+      p = share(pick ? exp_neg(picked - m) : 0.0f, warp_sum(sum));
+    }
+    if (a.normalize)
+      p = share_of_picks<SIGMOID>(pick, picked, p, unsortable(__reduce_max_sync(kFull, pick ? sortable(picked) : 0u)));
+    if (slot < K) {
+      a.topk_idx[tok * K + slot] = mine;
+      a.weights[tok * K + slot] = a.scale * p;
+    }
+  };
+  if (late_found > 0) {
+    const int id = lane < late_found ? late_ids[lane] : 0;
+    const int before = exact_rank<T, SIGMOID>(logits + late * a.logits_stride, late_m, bias_s, E, id, late_found);
+    settle(late, late_m, lane < late_found && before < K ? id : -1, lane < late_found ? before : lane);
+    __syncwarp();
+  }
+  if (any_open)
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp; first < a.num_tokens; first += 32 * stride) {
+      const int64_t own = first + lane * stride;
+      unsigned open = __ballot_sync(kFull, own < a.num_tokens && a.topk_idx[own * K] == kOpen);
+      for (; open != 0; open &= open - 1) {
+        const int64_t tok = first + (__ffs(open) - 1) * stride;
+        const T* row = logits + tok * a.logits_stride;
+        float m = -INFINITY;
+        for (int e = lane; e < E; e += 32) m = fmaxf(m, load_logit(row + e));
+        m = unsortable(__reduce_max_sync(kFull, sortable(m + 0.0f)));
+        settle(tok, m, exact_picks<T, SIGMOID>(a, row, m, bias_s, biased, key64), lane);
+      }
+    }
+  if (lane == 0 && routed > 0) atomicAdd(&cnt_s[E], routed);
+  add_columns<V>(acc, E, sum_s, [](int l, int i) { return route_column<V, BLOCKED>(l, i); });
+  finish_sums(a, sum_s, cnt_s, red_s, last_s);
 }
 
 template <typename T, bool SIGMOID>
 cudaError_t launch_typed(const GateArgs& a, cudaStream_t stream) {
-  const int vpl = (a.num_experts + 31) / 32;
+  const int v = (a.num_experts + 31) / 32, per = a.num_experts / a.num_groups;
+  // Columns side by side where a lane's are of one group, and (from 4 a lane on) every row
+  // starts on a vector's boundary.
   const bool wide = a.num_experts % 4 == 0 && a.logits_stride % 4 == 0 && aligned(a.logits, 4 * sizeof(T));
+  const auto blocked = [&](int V) { return (V < 4 || wide) && (a.topk_groups == a.num_groups || per % V == 0); };
   count_launch();
   // One wave of CTAs walks the tokens.
-  const auto run = [&](auto kernel, int v) {
-    const size_t smem = 8 * static_cast<size_t>(kGateWarps) * 32 * v + 4 * (static_cast<size_t>(2 * a.num_experts + 1) + 32 * v);
+  const auto run = [&](auto kernel, int V) {
+    const size_t smem = 8 * static_cast<size_t>(kGateWarps) * 32 * V + 4 * (2 * 32 * static_cast<size_t>(V) + a.num_experts + 1);
     if (cudaError_t e = ensure_smem_limit(kernel, smem)) return e;
     const int ctas = cached_occupancy(kernel, kGateThreads, smem);
     const int64_t most = min64(static_cast<int64_t>(ctas > 0 ? ctas : 1) * device_sm_count(), kGateMaxCtas);
     const int64_t grid = max64(1, min64(ceil_div64(a.num_tokens, kGateWarps), most));
     return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kGateThreads, smem, stream, a);
   };
-  // Up to 64 columns a lane has one or two of its own; four at a time where every row starts
-  // on a vector's boundary.
 #define MOE_ROUTE_CASE(V) \
-  if (vpl <= V) return wide && V >= 4 ? run(route_forward_kernel<V, T, SIGMOID, (V >= 4)>, V) : run(route_forward_kernel<V, T, SIGMOID, false>, V);
+  if (v <= V) return blocked(V) ? run(route_forward_kernel<V, T, SIGMOID, true>, V) : run(route_forward_kernel<V, T, SIGMOID, false>, V);
   MOE_ROUTE_CASE(1)
   MOE_ROUTE_CASE(2)
   MOE_ROUTE_CASE(4)
