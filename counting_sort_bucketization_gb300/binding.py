@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 import threading
 
@@ -387,17 +388,16 @@ def combine_backward(desc, dout, dst_slot, weights, dy, workspace, expert_out=No
     ``dout`` [N, H], ``dy`` and ``expert_out`` [capacity, H], all bf16; ``dy`` may be ``expert_out`` itself.
     ``zero_pad`` zeroes the alignment-gap rows of ``dy`` and needs the layout's offsets and counts."""
     N, K, E = int(desc.num_tokens), int(desc.topk), int(desc.num_experts)
-    if dy.dim() != 2 or tuple(dout.shape) != (N, dy.shape[1]):
-        raise ValueError(f"dy must be [capacity, H] and dout [{N}, H]")
-    cap, H = dy.shape
+    shape = dy.shape
+    if len(shape) != 2:
+        raise ValueError("dy must be [capacity, H]")
+    cap, H = shape
     if dweights is not None and expert_out is None:
         raise ValueError("dweights needs expert_out")
-    if expert_out is not None and expert_out.shape != dy.shape:
-        raise ValueError(f"expert_out must be [{cap}, {H}]")
     st = load_library().moe_combine_backward(
-        ctypes.byref(_desc(desc)), _dev(dout, "dout", torch.bfloat16), H, _dev(dst_slot, "dst_slot", torch.int32, N * K),
-        _dev(weights, "weights", torch.float32, N * K),
-        _dev(expert_out, "expert_out", torch.bfloat16, allow_none=True), _dev(dy, "dy", torch.bfloat16), cap,
+        ctypes.byref(_desc(desc)), _like(dout, (N, H), "dout", torch.bfloat16), H,
+        _dev(dst_slot, "dst_slot", torch.int32, N * K), _dev(weights, "weights", torch.float32, N * K),
+        _like(expert_out, shape, "expert_out", torch.bfloat16), _like(dy, shape, "dy", torch.bfloat16), cap,
         _dev(dweights, "dweights", torch.float32, N * K, allow_none=True),
         _dev(expert_offset, "expert_offset", torch.int32, E + 1, allow_none=not zero_pad),
         _dev(expert_count, "expert_count", torch.int32, E, allow_none=not zero_pad), 1 if zero_pad else 0,
@@ -636,19 +636,33 @@ def quantize_cols(desc, x, expert_offset, expert_count, q, sf, workspace, stream
 
 
 # ---------------------------------------------------------------- norm
-def _norm_desc(rows, cols, eps, stream, weight) -> _CNormDesc:
-    if stream not in (torch.bfloat16, torch.float32):
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+# A serving step's norm is host time: descriptions of the shapes in use are kept, and each
+# tensor is looked at once.
+@functools.lru_cache(maxsize=256)
+def _norm_desc(rows, cols, eps, stream_fp32, weight_fp32):
+    return ctypes.byref(_CNormDesc(int(rows), int(cols), float(eps), int(stream_fp32), int(weight_fp32)))
+
+
+def _norm_types(stream, weight, cols):
+    if stream not in _FLOATS:
         raise ValueError(f"the residual stream must be bfloat16 or float32, got {stream}")
-    if weight.dtype not in (torch.bfloat16, torch.float32) or weight.numel() != cols:
+    if weight.dtype not in _FLOATS or weight.numel() != cols:
         raise ValueError(f"weight must be [{cols}] in bfloat16 or float32")
-    return _CNormDesc(int(rows), int(cols), float(eps), int(stream == torch.float32), int(weight.dtype == torch.float32))
+    return stream is torch.float32, weight.dtype is torch.float32
 
 
 def _like(t, shape, name, dtype):
-    """Pointer of a contiguous device tensor of exactly this shape, or None."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+    """Pointer of a contiguous device tensor of exactly this shape and type, or None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return _dev(t, name, dtype, allow_none=True)
+    return _dev(t, name, dtype)
 
 
 def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, residual_out=None, rstd=None, eps=1e-6, total_rows=None,
@@ -659,28 +673,31 @@ def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, residual_out=Non
 
     ``x`` bf16 [rows, cols]; ``residual`` bf16 or fp32, or None: x is normed as it is.  Rows from ``total_rows``
     (device int32) on are left alone."""
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [rows, cols]")
-    rows, cols = x.shape
+    rows, cols = shape
     if (residual is None) != (residual_out is None):
         raise ValueError("residual and residual_out go together")
     if (q is None) != (sf is None):
         raise ValueError("q and sf go together")
     kind = torch.bfloat16 if residual is None else residual.dtype
-    d = _norm_desc(rows, cols, eps, kind, weight)
-    ld = 0
+    fp32, weight_fp32 = _norm_types(kind, weight, cols)
+    ld, scales = 0, None
     if q is not None:
+        scales = (rows, _blocks(cols))
         if col_major:
-            ld = _sf_ld(sf, rows, _blocks(cols))
-        elif tuple(sf.shape) != (rows, _blocks(cols)):
-            raise ValueError(f"sf must be [{rows}, {_blocks(cols)}], got {tuple(sf.shape)}")
+            ld = _sf_ld(sf, rows, scales[1])
+            scales = (scales[1], ld)
     st = load_library().moe_rms_norm(
-        ctypes.byref(d), _dev(x, "x", torch.bfloat16), _like(residual, x.shape, "residual", kind), _dev(weight, "weight"),
+        _norm_desc(rows, cols, eps, fp32, weight_fp32), _like(x, shape, "x", torch.bfloat16),
+        _like(residual, shape, "residual", kind), _like(weight, weight.shape, "weight", weight.dtype),
         _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True),
-        _like(residual_out, x.shape, "residual_out", kind), _like(y, x.shape, "y", torch.bfloat16),
-        _like(q, x.shape, "q", torch.float8_e4m3fn), _dev(sf, "sf", torch.float32, allow_none=True), ld,
+        _like(residual_out, shape, "residual_out", kind), _like(y, shape, "y", torch.bfloat16),
+        _like(q, shape, "q", torch.float8_e4m3fn), _like(sf, scales, "sf", torch.float32), ld,
         _like(rstd, (rows,), "rstd", torch.float32), _stream(stream))
-    _check(st, "moe_rms_norm")
+    if st:
+        _check(st, "moe_rms_norm")
 
 
 def new_norm_workspace(cols, device="cuda") -> torch.Tensor:
@@ -696,17 +713,19 @@ def rms_norm_backward(dy, z, rstd, weight, dz, dresidual=None, dx=None, dweight=
     """Gradient of ``rms_norm`` from its kept ``z`` (the residual_out, or x) and ``rstd``: ``dz`` (the stream's type)
     is the gradient of x and of the residual, with ``dresidual`` added; ``dx`` the same in bf16.  ``dweight`` [cols]
     (fp32) needs a ``workspace`` (``new_norm_workspace``); ``accumulate`` adds to it."""
-    if dy.dim() != 2:
+    shape, kind = dy.shape, z.dtype
+    if len(shape) != 2:
         raise ValueError("dy must be [rows, cols]")
-    rows, cols = dy.shape
-    d = _norm_desc(rows, cols, 1.0, z.dtype, weight)
+    rows, cols = shape
+    fp32, weight_fp32 = _norm_types(kind, weight, cols)
     if dweight is not None and workspace is None:
         raise ValueError("dweight needs a workspace")
     st = load_library().moe_rms_norm_backward(
-        ctypes.byref(d), _dev(dy, "dy", torch.bfloat16), _like(z, dy.shape, "z", z.dtype),
-        _like(rstd, (rows,), "rstd", torch.float32), _dev(weight, "weight"), _like(dresidual, dy.shape, "dresidual", z.dtype),
-        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True), _like(dz, dy.shape, "dz", z.dtype),
-        _like(dx, dy.shape, "dx", torch.bfloat16), _like(dweight, (cols,), "dweight", torch.float32), int(bool(accumulate)),
+        _norm_desc(rows, cols, 1.0, fp32, weight_fp32), _like(dy, shape, "dy", torch.bfloat16), _like(z, shape, "z", kind),
+        _like(rstd, (rows,), "rstd", torch.float32), _like(weight, weight.shape, "weight", weight.dtype),
+        _like(dresidual, shape, "dresidual", kind),
+        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True), _like(dz, shape, "dz", kind),
+        _like(dx, shape, "dx", torch.bfloat16), _like(dweight, (cols,), "dweight", torch.float32), int(bool(accumulate)),
         _dev(workspace, "workspace", torch.uint8, allow_none=True), 0 if workspace is None else workspace.numel(),
         _stream(stream))
     _check(st, "moe_rms_norm_backward")

@@ -154,7 +154,8 @@ cudaError_t launch_gate(const GateArgs& a, bool backward, cudaStream_t stream);
 cudaError_t launch_route(const GateArgs& a, cudaStream_t stream);
 
 // ------------------------------------------------ norm (norm_kernels.cu)
-constexpr int kNormMaxCtas = 608;      // partial sums of the weight's gradient at most
+// Partial sums of the weight's gradient, one a CTA, at most: what 160 SMs hold at 64 registers.
+int64_t norm_parts(int64_t cols);
 
 struct NormArgs {
   const uint16_t* x;             // bf16 bits [rows, cols]; backward: dy
@@ -175,7 +176,7 @@ struct NormArgs {
   float* rstd;                   // [rows], or null; read backward
   const void* dresidual;         // backward, or null
   float* dweight;                // backward, or null
-  float* partial;                // backward: [kNormMaxCtas, cols]
+  float* partial;                // backward: [norm_parts, cols]
   bool accumulate;
 };
 

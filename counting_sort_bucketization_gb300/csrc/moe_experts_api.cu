@@ -198,7 +198,7 @@ int moe_combine_backward(const moe_layout_desc* desc, const void* dout, int64_t 
   a.dweights = dweights;
   a.expert_offset = expert_offset;
   a.expert_count = expert_count;
-  a.zero_pad = zero_pad != 0;
+  a.zero_pad = zero_pad != 0 && desc->alignment > 1;   // else there are no gaps
   a.num_tokens = desc->num_tokens;
   a.topk = desc->topk;
   a.num_experts = desc->num_experts;
@@ -255,7 +255,7 @@ int moe_rms_norm(const moe_norm_desc* norm, const void* x, const void* residual,
 int moe_rms_norm_workspace_bytes(const moe_norm_desc* norm, size_t* bytes) {
   if (int st = check_norm(norm)) return st;
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-  *bytes = 4 * static_cast<size_t>(kNormMaxCtas) * static_cast<size_t>(norm->cols);
+  *bytes = 4 * static_cast<size_t>(norm_parts(norm->cols)) * static_cast<size_t>(norm->cols);
   return MOE_OK;
 }
 
@@ -267,7 +267,7 @@ int moe_rms_norm_backward(const moe_norm_desc* norm, const void* dy, const void*
   const bool wide = norm->stream_fp32 != 0;
   if (weight == nullptr || (rows > 0 && (dy == nullptr || z == nullptr || rstd == nullptr || dz == nullptr)))
     return MOE_ERR_INVALID_ARG;
-  const int64_t need = 4 * kNormMaxCtas * cols;
+  const int64_t need = 4 * norm_parts(cols) * cols;
   if (dweight != nullptr && (workspace == nullptr || static_cast<int64_t>(workspace_bytes) < need)) return MOE_ERR_INVALID_ARG;
   if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(rstd, 4) || !aligned(weight, 16) || !aligned(dresidual, 16) ||
       !aligned(dz, 16) || !aligned(dx, 16) || !aligned(dweight, 4) || !aligned(workspace, 16) || !aligned(total_rows, 4))

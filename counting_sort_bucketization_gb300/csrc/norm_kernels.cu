@@ -42,6 +42,23 @@ struct Raw8 {
       v[0] = load_v4(static_cast<const uint16_t*>(base) + at);
     }
   }
+  // Rounds to the stream's type.
+  __device__ __forceinline__ void set(const float* f) {
+    if constexpr (FP32) {
+      v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+      v[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+    } else {
+      v[0] = pack8(f);
+    }
+  }
+  __device__ __forceinline__ void store(void* base, int64_t at) const {
+    if constexpr (FP32) {
+      ptx::st_v4(static_cast<float*>(base) + at, v[0]);
+      ptx::st_v4(static_cast<float*>(base) + at + 4, v[1]);
+    } else {
+      ptx::st_v4(static_cast<uint16_t*>(base) + at, v[0]);
+    }
+  }
   __device__ __forceinline__ void get(float* f) const {
     if constexpr (FP32) {
       f[0] = __uint_as_float(v[0].x), f[1] = __uint_as_float(v[0].y), f[2] = __uint_as_float(v[0].z), f[3] = __uint_as_float(v[0].w);
@@ -82,8 +99,13 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
-template <int NV, bool CTA_ROW, bool FP32>
-__global__ void __launch_bounds__(CTA_ROW ? kMaxRowThreads : kShortThreads) norm_kernel(NormArgs a) {
+// MAXT: threads of a row at most; 32: each warp of a CTA has a row.  A CTA a row (or eight):
+// a wave of CTAs that walk the rows, with the next row's copies under way, took 183 us in
+// place of 182 on 32768 x 4096, 330 in place of 254 with the stream in fp32: SMs are not
+// equally fast, and the block scheduler evens that out.
+template <int NV, int MAXT, bool FP32>
+__global__ void __launch_bounds__(MAXT == 32 ? kShortThreads : MAXT, NV <= 4 ? 4 : 1) norm_kernel(NormArgs a) {
+  constexpr bool CTA_ROW = MAXT > 32;
   __shared__ float part[kMaxRowThreads / 32];
   ptx::grid_dependency_wait();
   const int threads = CTA_ROW ? static_cast<int>(blockDim.x) : 32;
@@ -94,87 +116,93 @@ __global__ void __launch_bounds__(CTA_ROW ? kMaxRowThreads : kShortThreads) norm
                               : static_cast<int64_t>(blockIdx.x) * (kShortThreads / 32) + threadIdx.x / 32;
   if (row >= rows) return;               // a whole CTA, or a whole warp
   const int64_t base = row * a.cols;
+  const int cols = static_cast<int>(a.cols);
   Raw8<false> x[NV];
-  Raw8<FP32> res[NV];
+  Raw8<FP32> z[NV];                      // the residual, then z
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = 8 * static_cast<int64_t>(j * threads + tid);
-    if (c < a.cols) {
+    const int c = 8 * (j * threads + tid);
+    if (c < cols) {
       x[j].load(a.x, base + c);
-      if (a.residual != nullptr) res[j].load(a.residual, base + c);
+      if (a.residual != nullptr) z[j].load(a.residual, base + c);
     }
   }
-  float z[NV][8];
   float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = 8 * static_cast<int64_t>(j * threads + tid);
-    if (c < a.cols) {
-      x[j].get(z[j]);
-      if (a.residual != nullptr) {
-        float f[8];
-        res[j].get(f);
+    const int c = 8 * (j * threads + tid);
+    if (c >= cols) break;
+    float f[8];
+    x[j].get(f);
+    if (a.residual != nullptr) {
+      float g[8];
+      z[j].get(g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[j][i] += f[i];
-        if constexpr (FP32) {
-          store_fp32(static_cast<float*>(a.residual_out) + base + c, z[j]);
-        } else {
-          const uint4 v = pack8(z[j]);
-          ptx::st_v4(static_cast<uint16_t*>(a.residual_out) + base + c, v);
-          unpack8(v, z[j]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[j][i] = 0.0f;
+      for (int i = 0; i < 8; ++i) f[i] += g[i];
     }
+    z[j].set(f);
+    if (a.residual != nullptr) z[j].store(a.residual_out, base + c);
+    z[j].get(f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(z[j][i], z[j][i], sum);
+    for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
   }
   sum = row_sum<CTA_ROW>(sum, part);
-  float r = 1.0f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
+  float r = 1.0f / sqrtf(sum / static_cast<float>(cols) + a.eps);
   if (!(sum < INFINITY)) {               // squares beyond fp32: eps is nothing beside them
     sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      if (8 * (j * threads + tid) >= cols) break;
+      float f[8];
+      z[j].get(f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = z[j][i] * 0x1p-80f;
-        sum = fmaf(v, v, sum);
-      }
+      for (int i = 0; i < 8; ++i) sum = fmaf(f[i] * 0x1p-80f, f[i] * 0x1p-80f, sum);
+    }
     sum = row_sum<CTA_ROW>(sum, part);
-    r = 0x1p-80f / sqrtf(sum / static_cast<float>(a.cols));
+    r = 0x1p-80f / sqrtf(sum / static_cast<float>(cols));
   }
   if (a.rstd != nullptr && tid == 0) a.rstd[row] = r;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = 8 * static_cast<int64_t>(j * threads + tid);
-    const bool in = c < a.cols;
-    float w[8] = {};
-    if (in) load_weight(a, c, w);
+    const int c = 8 * (j * threads + tid);
+    const bool in = c < cols;
+    float f[8] = {};
+    if (in) {
+      float w[8];
+      load_weight(a, c, w);
+      z[j].get(f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[j][i] = z[j][i] * r * w[i];
-    if (a.y != nullptr && in) ptx::st_v4(a.y + base + c, pack8(z[j]));
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+      if (a.y != nullptr) ptx::st_v4(a.y + base + c, pack8(f));
+    }
     if (a.q != nullptr) {
       float m = kAmaxFloor;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(z[j][i]));
+      for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
       const float sf = __fdiv_rn(m, kE4m3Max);
       const float inv = __fdiv_rn(1.0f, sf);
       if (in) {
-        *reinterpret_cast<uint2*>(a.q + base + c) = quantize8(z[j], inv);
+        *reinterpret_cast<uint2*>(a.q + base + c) = quantize8(f, inv);
         if (tid % 16 == 0) a.sf[row * a.sf_row_stride + c / kBlock * a.sf_block_stride] = sf;
       }
     }
   }
 }
 
-// One wave of CTAs walks the rows; a thread keeps its columns' part of the weight's
-// gradient over all of them, and the CTAs' parts are added by the kernel below.
-template <int NV, bool CTA_ROW, bool FP32>
-__global__ void __launch_bounds__(CTA_ROW ? kMaxRowThreads : kShortThreads) norm_backward_kernel(NormArgs a) {
+// A CTA walks a share of the rows; a thread keeps its columns' part of the weight's gradient
+// over them, and the CTAs' parts are added by the kernel below.  Shares are fixed, so the
+// sums are.  (32768 x 4096: 184 us; two shares for each CTA that fits, so that SMs that are
+// ahead take more, 191, four 203: their parts cost more than they even out.)
+//
+// CTAs an SM: what is in flight counts, so many with few registers: 32768 x 4096 with four
+// 184 us, three 190, two 221; the stream in fp32 spills with four (383, 342 with three).
+template <int NV, int MAXT, bool FP32>
+__global__ void __launch_bounds__(MAXT == 32 ? kShortThreads : MAXT,
+                                  NV == 1 ? 4 : NV == 2 ? (MAXT == 256 && !FP32 ? 4 : 3) : MAXT <= 256 ? 2 : 1)
+norm_backward_kernel(NormArgs a) {
+  constexpr bool CTA_ROW = MAXT > 32;
   __shared__ float part[kMaxRowThreads / 32];
   extern __shared__ float sum_s[];       // [cols], where warps have a row each
   ptx::grid_dependency_wait();
@@ -184,56 +212,54 @@ __global__ void __launch_bounds__(CTA_ROW ? kMaxRowThreads : kShortThreads) norm
   const int mine = CTA_ROW ? 0 : static_cast<int>(threadIdx.x) / 32;
   int64_t rows = a.rows;
   if (a.total_rows != nullptr) rows = min64(rows, *a.total_rows);
-  const float inv_cols = 1.0f / static_cast<float>(a.cols);
+  const int cols = static_cast<int>(a.cols);
+  const float inv_cols = 1.0f / static_cast<float>(cols);
   float dw[NV][8] = {};
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + mine; row < rows; row += static_cast<int64_t>(gridDim.x) * kRows) {
     const int64_t base = row * a.cols;
-    const float r = a.rstd[row];
     Raw8<false> dy[NV];
     Raw8<FP32> z[NV], dres[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = 8 * static_cast<int64_t>(j * threads + tid);
-      if (c < a.cols) {
+      const int c = 8 * (j * threads + tid);
+      if (c < cols) {
         dy[j].load(a.x, base + c);
         z[j].load(a.residual, base + c);
         if (a.dresidual != nullptr) dres[j].load(a.dresidual, base + c);
       }
     }
-    float g[NV][8], h[NV][8];
+    const float r = a.rstd[row];
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = 8 * static_cast<int64_t>(j * threads + tid);
-      if (c < a.cols) {
-        float w[8];
-        load_weight(a, c, w);
-        dy[j].get(g[j]);
-        z[j].get(h[j]);
+      const int c = 8 * (j * threads + tid);
+      if (c >= cols) break;
+      float g[8], h[8], w[8];
+      load_weight(a, c, w);
+      dy[j].get(g);
+      z[j].get(h);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[j][i] *= r;
-          dw[j][i] = fmaf(g[j][i], h[j][i], dw[j][i]);
-          g[j][i] *= w[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[j][i] = h[j][i] = 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        h[i] *= r;
+        dw[j][i] = fmaf(g[i], h[i], dw[j][i]);
+        sum = fmaf(g[i] * w[i], h[i], sum);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(g[j][i], h[j][i], sum);
     }
     const float mean = row_sum<CTA_ROW>(sum, part) * inv_cols;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = 8 * static_cast<int64_t>(j * threads + tid);
-      if (c >= a.cols) continue;
-      float d[8] = {};
+      const int c = 8 * (j * threads + tid);
+      if (c >= cols) break;
+      float g[8], h[8], w[8], d[8] = {};
+      load_weight(a, c, w);
+      dy[j].get(g);
+      z[j].get(h);
       if (a.dresidual != nullptr) dres[j].get(d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = fmaf(r, fmaf(-h[j][i], mean, g[j][i]), d[i]);
-      if constexpr (FP32) store_fp32(static_cast<float*>(a.residual_out) + base + c, d);
-      else ptx::st_v4(static_cast<uint16_t*>(a.residual_out) + base + c, pack8(d));
+      for (int i = 0; i < 8; ++i) d[i] = fmaf(r, fmaf(-h[i] * r, mean, g[i] * w[i]), d[i]);
+      Raw8<FP32> out;
+      out.set(d);
+      out.store(a.residual_out, base + c);
       if (a.y != nullptr) ptx::st_v4(a.y + base + c, pack8(d));
     }
   }
@@ -242,29 +268,29 @@ __global__ void __launch_bounds__(CTA_ROW ? kMaxRowThreads : kShortThreads) norm
   if constexpr (CTA_ROW) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = 8 * static_cast<int64_t>(j * threads + tid);
-      if (c < a.cols) store_fp32(out + c, dw[j]);
+      const int c = 8 * (j * threads + tid);
+      if (c < cols) store_fp32(out + c, dw[j]);
     }
   } else {
     for (int w = 0; w < kRows; ++w) {    // one after the other: a fixed order
       if (w == mine) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          const int64_t c = 8 * static_cast<int64_t>(j * threads + tid);
-          if (c >= a.cols) continue;
+          const int c = 8 * (j * threads + tid);
+          if (c >= cols) break;
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum_s[c + i] = w == 0 ? dw[j][i] : sum_s[c + i] + dw[j][i];
         }
       }
       __syncthreads();
     }
-    for (int c = threadIdx.x; c < a.cols; c += kShortThreads) out[c] = sum_s[c];
+    for (int c = threadIdx.x; c < cols; c += kShortThreads) out[c] = sum_s[c];
   }
 }
 
 // The weight's gradient from the CTAs' parts: a warp's lanes have 32 columns, its CTA's
-// eight warps every eighth part, added in their order.
-constexpr int kSumThreads = 256;
+// 32 warps every 32nd part, added in their order.
+constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads) norm_weight_kernel(const float* partial, int parts, int64_t cols, float* dweight,
                                                                   bool accumulate) {
   __shared__ float sum_s[kSumThreads / 32][32];
@@ -283,30 +309,34 @@ __global__ void __launch_bounds__(kSumThreads) norm_weight_kernel(const float* p
   }
 }
 
-// Threads of a row and vectors of a thread.  A warp has up to 1024 columns, a CTA two
-// vectors a thread up to 8192, then four and eight.
+// Vectors of a thread and threads of a row.  A warp has up to 1024 columns, a CTA two
+// vectors a thread up to 4096, four up to 8192, then eight; the gradient, which holds more,
+// four and twice the threads up to 16384 (385 us in place of 559 on 16384 x 16384).
 struct Shape {
   int nv;
+  int max_threads;
   int threads;
-  bool cta_row;
 };
-Shape shape_of(int64_t cols) {
+Shape shape_of(int64_t cols, bool backward) {
   const int64_t vecs = ceil_div64(cols, 8);
-  if (vecs <= 128) return {vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4, kShortThreads, false};
-  const int nv = vecs <= 2 * kMaxRowThreads ? 2 : vecs <= 4 * kMaxRowThreads ? 4 : 8;
-  return {nv, static_cast<int>(ceil_div64(ceil_div64(vecs, nv), 32) * 32), true};
+  if (vecs <= 128) return {vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4, 32, kShortThreads};
+  const int nv = vecs <= 512 ? 2 : vecs <= (backward ? 2048 : 1024) ? 4 : 8;
+  const int threads = static_cast<int>(ceil_div64(ceil_div64(vecs, nv), 32) * 32);
+  return {nv, threads <= 256 ? 256 : 512, threads};
 }
 
 template <typename F>
 cudaError_t with_shape(const Shape& s, bool fp32, F run) {
-#define MOE_NORM_CASE(NV, CTA) \
-  if (s.nv == NV && s.cta_row == CTA) return fp32 ? run.template operator()<NV, CTA, true>() : run.template operator()<NV, CTA, false>();
-  MOE_NORM_CASE(1, false)
-  MOE_NORM_CASE(2, false)
-  MOE_NORM_CASE(4, false)
-  MOE_NORM_CASE(2, true)
-  MOE_NORM_CASE(4, true)
-  MOE_NORM_CASE(8, true)
+#define MOE_NORM_CASE(NV, MAXT) \
+  if (s.nv == NV && s.max_threads == MAXT) return fp32 ? run.template operator()<NV, MAXT, true>() : run.template operator()<NV, MAXT, false>();
+  MOE_NORM_CASE(1, 32)
+  MOE_NORM_CASE(2, 32)
+  MOE_NORM_CASE(4, 32)
+  MOE_NORM_CASE(2, 256)
+  MOE_NORM_CASE(4, 256)
+  MOE_NORM_CASE(4, 512)
+  MOE_NORM_CASE(8, 256)
+  MOE_NORM_CASE(8, 512)
 #undef MOE_NORM_CASE
   return cudaErrorInvalidValue;
 }
@@ -315,10 +345,10 @@ struct Forward {
   const NormArgs& a;
   const Shape& s;
   cudaStream_t stream;
-  template <int NV, bool CTA_ROW, bool FP32>
+  template <int NV, int MAXT, bool FP32>
   cudaError_t operator()() const {
-    const int64_t grid = CTA_ROW ? a.rows : ceil_div64(a.rows, kShortThreads / 32);
-    return launch_pdl(norm_kernel<NV, CTA_ROW, FP32>, dim3(static_cast<unsigned>(grid)), s.threads, 0, stream, a);
+    const int64_t grid = MAXT > 32 ? a.rows : ceil_div64(a.rows, kShortThreads / 32);
+    return launch_pdl(norm_kernel<NV, MAXT, FP32>, dim3(static_cast<unsigned>(grid)), s.threads, 0, stream, a);
   }
 };
 
@@ -326,13 +356,13 @@ struct Backward {
   const NormArgs& a;
   const Shape& s;
   cudaStream_t stream;
-  template <int NV, bool CTA_ROW, bool FP32>
+  template <int NV, int MAXT, bool FP32>
   cudaError_t operator()() const {
-    const auto kernel = norm_backward_kernel<NV, CTA_ROW, FP32>;
-    const size_t smem = CTA_ROW ? 0 : 4 * static_cast<size_t>(a.cols);
+    const auto kernel = norm_backward_kernel<NV, MAXT, FP32>;
+    const size_t smem = MAXT > 32 ? 0 : 4 * static_cast<size_t>(a.cols);
     const int ctas = cached_occupancy(kernel, s.threads, smem);
-    const int64_t most = min64(static_cast<int64_t>(ctas > 0 ? ctas : 1) * device_sm_count(), kNormMaxCtas);
-    const int64_t units = CTA_ROW ? a.rows : ceil_div64(a.rows, kShortThreads / 32);
+    const int64_t most = min64(static_cast<int64_t>(ctas > 0 ? ctas : 1) * device_sm_count(), norm_parts(a.cols));
+    const int64_t units = MAXT > 32 ? a.rows : ceil_div64(a.rows, kShortThreads / 32);
     const int64_t grid = max64(1, min64(units, most));
     count_launch();
     cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), s.threads, smem, stream, a);
@@ -349,15 +379,17 @@ struct Backward {
 // griddepcontrol.wait, so it never releases its dependents early.
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
-  const Shape s = shape_of(a.cols);
+  const Shape s = shape_of(a.cols, false);
   count_launch();
   return with_shape(s, a.stream_fp32, Forward{a, s, stream});
 }
 
+int64_t norm_parts(int64_t cols) { return 160 * max64(1, 1024 / shape_of(cols, true).threads); }
+
 // Without rows the gradient of the weight is still written.
 cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream) {
   if (a.rows == 0 && a.dweight == nullptr) return cudaSuccess;
-  const Shape s = shape_of(a.cols);
+  const Shape s = shape_of(a.cols, true);
   return with_shape(s, a.stream_fp32, Backward{a, s, stream});
 }
 
