@@ -24,11 +24,12 @@
 namespace moe {
 namespace {
 
-// Bounds of what a 32-bit score errs by, of the row's largest score.  Sigmoid: e^-x 2^-21.4,
-// the sum and the reciprocal 2^-22 (of itself), so 2^-20 of a small one and 2^-21 at 1/2 and
-// above.  Softmax: two exponentials, a sum of up to 37 additions one after the other, a
-// quotient.
-constexpr float kErrSigmoid = 0x1p-20f;
+// Bounds of what a 32-bit score errs by, of the row's largest score (a sigmoid counts as 1/8
+// at most).  e^x as 2^(x log2 e) errs by 1.5 * 2^-24 |x| + 2^-22 of itself.  Sigmoid: |x| <= 21
+// unless all are tiny (then they are e^(x - max)), and two roundings and a reciprocal's 2^-23:
+// 2^-18.7 of a small one; near 1 what e^-x errs by counts s (1 - s), 2^-21.9 in all.  Softmax: a
+// sum of up to 37 additions one after the other, and a quotient: 2^-18.6.
+constexpr float kErrSigmoid = 0x1p-18f;
 constexpr float kErrSoftmax = 0x1p-18f;
 
 // Numbers as sums of two floats, good to about 2^-46: hi is the sum rounded, lo the rest.
@@ -193,6 +194,99 @@ __device__ __noinline__ int exact_picks(const GateArgs& a, const T* row, float m
   return mine;
 }
 
+// Where a token's choice is left open, its first id says so until the loop over the tokens is
+// over; one token whose candidates are listed is kept by its warp instead.
+constexpr int64_t kOpen = -2;
+struct Late {
+  int64_t token = 0;
+  int found = 0;                         // candidates
+  float m = 0.0f;                        // the row's largest logit
+  int* ids;                              // shared memory, [32]
+};
+
+// Ids and weights of a token from its picks: a lane's pick (or -1) and its place.
+template <typename T, bool SIGMOID>
+__device__ __forceinline__ void settle(const GateArgs& a, int* cnt_s, int64_t token, float m, int mine, int slot) {
+  const T* row = static_cast<const T*>(a.logits) + token * a.logits_stride;
+  const bool pick = mine >= 0;
+  const float picked = pick ? load_logit(row + mine) : 0.0f;
+  float p = 0.0f;
+  if (pick) atomicAdd(&cnt_s[mine], 1);
+  if (SIGMOID) {
+    if (pick) p = sigmoid(picked);
+  } else if (!a.normalize) {
+    float sum = 0.0f;
+    for (int e = threadIdx.x % 32; e < a.num_experts; e += 32) sum += exp_neg(load_logit(row + e) - m);
+    p = share(pick ? exp_neg(picked - m) : 0.0f, warp_sum(sum));
+  }
+  if (a.normalize)
+    p = share_of_picks<SIGMOID>(pick, picked, p, unsortable(__reduce_max_sync(kFull, pick ? sortable(picked) : 0u)));
+  if (slot < a.topk) {
+    a.topk_idx[token * a.topk + slot] = mine;
+    a.weights[token * a.topk + slot] = a.scale * p;
+  }
+}
+
+// The warp's choices left open, from exact keys.  Its i-th token is first + i * stride.
+template <typename T, bool SIGMOID>
+__device__ __noinline__ void settle_open(const GateArgs& a, const float* bias_s, bool biased, uint64_t* key64, int* cnt_s,
+                                         const Late& late, bool any_open, int64_t first, int64_t stride) {
+  const int lane = threadIdx.x % 32, E = a.num_experts, K = a.topk;
+  const T* logits = static_cast<const T*>(a.logits);
+  if (late.found > 0) {
+    const int id = lane < late.found ? late.ids[lane] : 0;
+    const int before = exact_rank<T, SIGMOID>(logits + late.token * a.logits_stride, late.m, bias_s, E, id, late.found);
+    settle<T, SIGMOID>(a, cnt_s, late.token, late.m, lane < late.found && before < K ? id : -1, lane < late.found ? before : lane);
+    __syncwarp();
+  }
+  if (!any_open) return;
+  for (int64_t base = first; base < a.num_tokens; base += 32 * stride) {
+    const int64_t own = base + lane * stride;
+    unsigned open = __ballot_sync(kFull, own < a.num_tokens && a.topk_idx[own * K] == kOpen);
+    for (; open != 0; open &= open - 1) {
+      const int64_t tok = base + (__ffs(open) - 1) * stride;
+      const T* row = logits + tok * a.logits_stride;
+      float m = -INFINITY;
+      for (int e = lane; e < E; e += 32) m = fmaxf(m, load_logit(row + e));
+      m = unsortable(__reduce_max_sync(kFull, sortable(m + 0.0f)));
+      settle<T, SIGMOID>(a, cnt_s, tok, m, exact_picks<T, SIGMOID>(a, row, m, bias_s, biased, key64), lane);
+    }
+  }
+}
+
+__device__ __forceinline__ void add_best(float& hi, float& lo, float k) {
+  lo = fmaxf(lo, fminf(hi, k));
+  hi = fmaxf(hi, k);
+}
+// The two largest of a lane's and another's two largest.
+__device__ __forceinline__ void merge_best(float& hi, float& lo, float h2, float l2) {
+  lo = fmaxf(fmaxf(lo, l2), fminf(hi, h2));
+  hi = fmaxf(hi, h2);
+}
+
+// Biases to shared memory ([padded], zeros past E), and what is to be known of them.
+// Biases that are all the same number change no order.  Others than numbers close experts
+// (-inf) or spoil the tokens that have them open (NaN, +inf).  All threads of the CTA.
+struct Biases {
+  bool differ;
+  bool odd;
+};
+__device__ __forceinline__ Biases load_biases(const GateArgs& a, float* bias_s, int padded) {
+  bool differ = false, odd = false;
+  for (int e = threadIdx.x; e < padded; e += kGateThreads) {
+    const float b = a.bias != nullptr && e < a.num_experts ? a.bias[e] : 0.0f;
+    bias_s[e] = b;
+    if (a.bias != nullptr && e < a.num_experts) {
+      differ |= b != a.bias[0];
+      odd |= !(fabsf(b) < INFINITY);
+    }
+  }
+  Biases r;
+  r.odd = __syncthreads_or(odd);
+  r.differ = __syncthreads_or(differ) || r.odd;
+  return r;
+}
+
 // The column of a lane's i-th value: V side by side (BLOCKED), or 32 apart.
 template <int V, bool BLOCKED>
 __device__ __forceinline__ int route_column(int lane, int i) {
@@ -213,26 +307,17 @@ __device__ __forceinline__ void load_route_row(const T* row, bool live, int lane
   }
 }
 
-__device__ __forceinline__ void add_best(float& hi, float& lo, float k) {
-  lo = fmaxf(lo, fminf(hi, k));
-  hi = fmaxf(hi, k);
-}
-// The two largest of a lane's and another's two largest.
-__device__ __forceinline__ void merge_best(float& hi, float& lo, float h2, float l2) {
-  lo = fmaxf(fmaxf(lo, l2), fminf(hi, h2));
-  hi = fmaxf(hi, h2);
-}
-
 template <int V, typename T, bool SIGMOID, bool BLOCKED>
-__global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) route_forward_kernel(GateArgs a) {
+__global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) route_forward_kernel(GateArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int E = a.num_experts, K = a.topk, G = a.num_groups, per = E / G;
-  constexpr bool kAhead = V <= 16;       // the next token's row is loaded a token ahead
   __shared__ bool last_s;
-  __shared__ uint64_t list_s[kGateWarps][32];
+  __shared__ __align__(16) float list_k_s[kGateWarps][32];
+  __shared__ int list_id_s[kGateWarps][32];
   __shared__ float red_s[kGateWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  uint64_t* list = list_s[warp];
+  float* list_k = list_k_s[warp];
+  int* list_id = list_id_s[warp];
   uint64_t* key64 = reinterpret_cast<uint64_t*>(smem) + static_cast<size_t>(warp) * (32 * V);   // for exact_picks
   float* key_s = reinterpret_cast<float*>(key64);                                                // for groups not BLOCKED
   float* sum_s = reinterpret_cast<float*>(reinterpret_cast<uint64_t*>(smem) + kGateWarps * 32 * V);   // [E]
@@ -241,19 +326,10 @@ __global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) ro
   for (int e = threadIdx.x; e < E; e += kGateThreads) sum_s[e] = 0.0f;
   for (int e = threadIdx.x; e <= E; e += kGateThreads) cnt_s[e] = 0;
   ptx::grid_dependency_wait();
-  // Biases that are all the same number change no order.  Others than numbers close experts
-  // (-inf) or spoil the tokens that have them open (NaN, +inf).
-  bool differ = false, odd = false;
-  for (int e = threadIdx.x; e < 32 * V; e += kGateThreads) {
-    const float b = a.bias != nullptr && e < E ? a.bias[e] : 0.0f;
-    bias_s[e] = b;
-    if (a.bias != nullptr && e < E) {
-      differ |= b != a.bias[0];
-      odd |= !(fabsf(b) < INFINITY);
-    }
-  }
-  const bool check_keys = __syncthreads_or(odd), biased = __syncthreads_or(differ) || check_keys;
+  const Biases biases = load_biases(a, bias_s, 32 * V);
+  const bool biased = biases.differ, check_keys = biases.odd;
 
+  constexpr int kLine = 128 / static_cast<int>(sizeof(T));   // values
   const bool limited = a.topk_groups < G;
   const bool by_logit = !biased && a.group_sum == 1;   // a group's score is in the order of its best logit
   // Lanes of a group (BLOCKED: those that hold it), the lane's group, its place there.
@@ -264,14 +340,9 @@ __global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) ro
   const int turn = limited && !BLOCKED ? (group * lanes) % per : 0;   // groups start apart, so that they meet no bank together
   const unsigned inverse = (0x400000u + per - 1) / per;   // e / per = e * inverse >> 22 for e < 1024
 
-  // Where a token's choice is left open, its first id says so until the loop is over.
-  // One token's whose candidates are listed waits in registers instead.
-  constexpr int64_t kOpen = -2;
   bool any_open = false;
-  int64_t late = 0;
-  int late_found = 0;
-  float late_m = 0.0f;
-  int* late_ids = reinterpret_cast<int*>(key64) + 32 * V;   // past the groups' keys
+  Late late;
+  late.ids = reinterpret_cast<int*>(key64) + 32 * V;        // past the groups' keys
   // Keys from `guess` on are candidates, if between K and 32 reach it: a little below the
   // K-th best key of the token before.
   float guess = INFINITY, slack = 0.0f;
@@ -283,18 +354,15 @@ __global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) ro
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
   int routed = 0;
-  float next[V];
-  if (kAhead) load_route_row<V, T, BLOCKED>(logits + t * a.logits_stride, t < a.num_tokens, lane, E, next);
   for (; t < a.num_tokens; t += stride) {
     const T* row = logits + t * a.logits_stride;
     float key[V], s[V];                  // key: first the logit
-    if (kAhead) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = next[i];
-      load_route_row<V, T, BLOCKED>(row + stride * a.logits_stride, t + stride < a.num_tokens, lane, E, next);
-    } else {
-      load_route_row<V, T, BLOCKED>(row, true, lane, E, key);
-    }
+    load_route_row<V, T, BLOCKED>(row, true, lane, E, key);
+    // The next token's row on its way to the L2 (in registers it costs spills: 131072 x 384 147
+    // us in place of 139).
+    if (t + stride < a.num_tokens)
+      for (int c = lane * kLine; c < E; c += 32 * kLine)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row + stride * a.logits_stride + c));
     float m = key[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, key[i]);
@@ -350,8 +418,10 @@ __global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) ro
         for (int i = 0; i < V; ++i) acc[i] += s[i] * inv;
 
       // What a key may err by, but for its own rounding.
-      const float most = SIGMOID ? sigmoid(m) : factor;
-      const float err = (SIGMOID ? kErrSigmoid * fminf(most, 0.25f) : kErrSoftmax * most) + 0x1p-120f;
+      // (a sigmoid is below e^m)
+      float most = factor;
+      if (SIGMOID) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(most) : "f"(m * 1.4426950408889634f));
+      const float err = (SIGMOID ? 1.01f * kErrSigmoid * fminf(most, 0.125f) : kErrSoftmax * most) + 0x1p-120f;
       const auto near = [&](float x, float y) {
         return biased && fabsf(x - y) <= 2.0f * err + 0x1p-23f * fmaxf(fabsf(x), fabsf(y));
       };
@@ -409,7 +479,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) ro
         for (int j = 0; j < a.topk_groups; ++j) {
           const unsigned best = __reduce_max_sync(kFull, rest);
           if (best <= kKeyNegInf) break;
-          const int g = (__ffs(__ballot_sync(kFull, rest == best)) - 1) / lanes;
+          const int g = __shfl_sync(kFull, group, __ffs(__ballot_sync(kFull, rest == best)) - 1);
           kept |= 1u << g;
           if (group == g) rest = kKeyNegInf, held = true;
         }
@@ -481,39 +551,53 @@ __global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) ro
           count(bits);
           edge = -FLT_MAX;               // further below
         }
-        float picked = 0.0f;             // the pick's logit
+        float picked = 0.0f, score = 0.0f;   // the pick's logit and score
         int candidate = 0;
+        bool beyond = false;             // what is not listed may belong to the picks
         if (found <= 32) {
-          int* ids = reinterpret_cast<int*>(list);
-          for (; bits != 0; bits &= bits - 1) ids[at++] = route_column<V, BLOCKED>(lane, __ffs(bits) - 1);
+          // Ids, keys; then both in the keys' order.
+          for (; bits != 0; bits &= bits - 1) list_id[at++] = route_column<V, BLOCKED>(lane, __ffs(bits) - 1);
           __syncwarp();
-          const int id = lane < found ? ids[lane] : 0;
+          const int id = lane < found ? list_id[lane] : 0;
           const float l = lane < found ? load_logit(row + id) : 0.0f;
           const float bias = bias_s[id];
-          __syncwarp();
-          const float k = !biased ? l : (SIGMOID ? sigmoid(l) : exp_neg(l - m) * factor) + bias;
-          const uint64_t own = lane < found ? static_cast<uint64_t>(sortable(k + 0.0f)) << 32 | ~static_cast<unsigned>(id) : 0;
-          list[lane] = own;
+          score = SIGMOID ? sigmoid(l) : exp_neg(fminf(l - m, 0.0f)) * inv;
+          const float k = lane >= found ? -INFINITY : biased ? score + bias : l;
+          list_k[lane] = k;
           __syncwarp();
           int before = 0;
-#pragma unroll 4
-          for (int j = 0; j < found; ++j) before += list[j] > own;
-          float* sorted = reinterpret_cast<float*>(list);        // keys in order, and their ids
-          int* sorted_id = reinterpret_cast<int*>(list) + 32;
+          for (int j = 0; j < found; j += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(list_k + j);
+            before += (o.x > k) + (o.y > k) + (o.z > k) + (o.w > k);
+          }
+          // Equal keys: the lower id first, which is the lower lane where a lane's columns are
+          // side by side.
+          unsigned same = __match_any_sync(kFull, lane < found ? before : 32 + lane);
+          if (BLOCKED) {
+            before += __popc(same & ptx::lanemask_lt());
+          } else {
+            const int mates = __reduce_max_sync(kFull, __popc(same));
+            int earlier = 0;
+            if (mates > 1)
+              for (int j = 0; j < found; ++j) {
+                const int other = __shfl_sync(kFull, id, j);
+                earlier += (same >> j & 1) != 0 && other < id;
+              }
+            before += earlier;
+          }
           __syncwarp();
-          if (lane < found) sorted[before] = k, sorted_id[before] = id;
+          if (lane < found) list_k[before] = k, list_id[before] = id;
           __syncwarp();
           if (biased && lane < found && before < K) {
-            if (before + 1 == found) {
-              exact = near(k, edge);
-            } else if (near(k, sorted[before + 1])) {
-              const int other = sorted_id[before + 1];
-              exact = load_logit(row + other) != l || bias_s[other] != bias;
+            if (before == K - 1) exact = beyond = near(k, edge);
+            if (before + 1 < found && near(k, list_k[before + 1])) {
+              const int other = list_id[before + 1];
+              exact |= load_logit(row + other) != l || bias_s[other] != bias;
             }
           }
           if (found >= K) {
-            const float last = sorted[K - 1];
-            if (few) slack = fmaxf(2.0f * slack, 0x1p-4f * (sorted[0] - last) + 0x1p-8f * fabsf(last));
+            const float last = list_k[K - 1];
+            if (few) slack = fmaxf(2.0f * slack, 0x1p-4f * (list_k[0] - last) + 0x1p-8f * fabsf(last));
             else if (many) slack *= 0.5f;
             else if (found > 20) slack *= 0.75f;
             guess = last - slack;
@@ -537,7 +621,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) ro
             const float lk = load_logit(row + id), bk = bias_s[id];
             if (near(last_key, want) && (lk != last_l || bk != last_b)) exact = true;
             last_key = want, last_l = lk, last_b = bk;
-            if (lane == k && k < K) mine = id, picked = lk;
+            if (lane == k && k < K) mine = id, picked = lk, score = SIGMOID ? sigmoid(lk) : exp_neg(lk - m) * inv;
             h = -INFINITY;
             if (!BLOCKED || held)
 #pragma unroll
@@ -552,17 +636,16 @@ __global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) ro
         exact = __any_sync(kFull, exact);
         if (exact) {
           mine = -1;
-          if (found <= 32 && late_found == 0) {
-            late = t, late_found = found, late_m = m;
-            if (lane < found) late_ids[slot] = candidate;
+          if (found <= 32 && late.found == 0 && !__any_sync(kFull, beyond)) {
+            late.token = t, late.found = found, late.m = m;
+            if (lane < found) late.ids[slot] = candidate;
             exact = false;
             slot = 32;                   // nothing is written yet
           }
         }
         const bool pick = mine >= 0;
         if (pick) atomicAdd(&cnt_s[mine], 1);
-        float p = 0.0f;
-        if (pick && (SIGMOID || !a.normalize)) p = SIGMOID ? sigmoid(picked) : exp_neg(picked - m) * inv;
+        float p = pick ? score : 0.0f;
         if (a.normalize) {
           const float top_pick = SIGMOID ? m : unsortable(__reduce_max_sync(kFull, pick ? sortable(picked) : 0u));
           p = share_of_picks<SIGMOID>(pick, picked, p, top_pick);
@@ -583,46 +666,9 @@ __global__ void __launch_bounds__(kGateThreads, V <= 8 ? 4 : V <= 12 ? 3 : 2) ro
     }
   }
   __syncwarp();
-  // Choices left open, from exact keys.
-  const auto settle = [&](int64_t tok, float m, int mine, int slot) {
-    const T* row = logits + tok * a.logits_stride;
-    const bool pick = mine >= 0;
-    const float picked = pick ? load_logit(row + mine) : 0.0f;
-    float p = 0.0f;
-    if (pick) atomicAdd(&cnt_s[mine], 1);
-    if (SIGMOID) {
-      if (pick) p = sigmoid(picked);
-    } else if (!a.normalize) {
-      float sum = 0.0f;
-      for (int e = lane; e < E; e += 32) sum += exp_neg(load_logit(row + e) - m);
-      p = share(pick ? exp_neg(picked - m) : 0.0f, warp_sum(sum));
-    }
-    if (a.normalize)
-      p = share_of_picks<SIGMOID>(pick, picked, p, unsortable(__reduce_max_sync(kFull, pick ? sortable(picked) : 0u)));
-    if (slot < K) {
-      a.topk_idx[tok * K + slot] = mine;
-      a.weights[tok * K + slot] = a.scale * p;
-    }
-  };
-  if (late_found > 0) {
-    const int id = lane < late_found ? late_ids[lane] : 0;
-    const int before = exact_rank<T, SIGMOID>(logits + late * a.logits_stride, late_m, bias_s, E, id, late_found);
-    settle(late, late_m, lane < late_found && before < K ? id : -1, lane < late_found ? before : lane);
-    __syncwarp();
-  }
-  if (any_open)
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp; first < a.num_tokens; first += 32 * stride) {
-      const int64_t own = first + lane * stride;
-      unsigned open = __ballot_sync(kFull, own < a.num_tokens && a.topk_idx[own * K] == kOpen);
-      for (; open != 0; open &= open - 1) {
-        const int64_t tok = first + (__ffs(open) - 1) * stride;
-        const T* row = logits + tok * a.logits_stride;
-        float m = -INFINITY;
-        for (int e = lane; e < E; e += 32) m = fmaxf(m, load_logit(row + e));
-        m = unsortable(__reduce_max_sync(kFull, sortable(m + 0.0f)));
-        settle(tok, m, exact_picks<T, SIGMOID>(a, row, m, bias_s, biased, key64), lane);
-      }
-    }
+  if (late.found > 0 || any_open)
+    settle_open<T, SIGMOID>(a, bias_s, biased, key64, cnt_s, late, any_open,
+                               static_cast<int64_t>(blockIdx.x) * kGateWarps + warp, stride);
   if (lane == 0 && routed > 0) atomicAdd(&cnt_s[E], routed);
   add_columns<V>(acc, E, sum_s, [](int l, int i) { return route_column<V, BLOCKED>(l, i); });
   finish_sums(a, sum_s, cnt_s, red_s, last_s);
