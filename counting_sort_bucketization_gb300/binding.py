@@ -176,6 +176,12 @@ def _desc(d) -> _CDesc:
     return _CDesc(int(d.num_tokens), int(d.topk), int(d.num_experts), int(d.num_ranks), int(d.alignment))
 
 
+@functools.lru_cache(maxsize=256)
+def _desc_ref(N, K, E, R, A):
+    """A description that calls may share: the library copies it."""
+    return ctypes.byref(_CDesc(N, K, E, R, A))
+
+
 def _check(status: int, what: str) -> None:
     if status != 0:
         raise LayoutError(what, status)
@@ -214,6 +220,23 @@ def _dev(t: torch.Tensor | None, name: str, dtype=None, numel=None, allow_none=F
     if nbytes is not None and _nbytes(t) < nbytes:
         raise ValueError(f"{name} needs at least {nbytes} bytes, has {_nbytes(t)}")
     return t.data_ptr()
+
+
+def _like(t, shape, name, dtype):
+    """Pointer of a contiguous device tensor of exactly this shape and type, or None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _dev(t, name, dtype)
+
+
+def _here(t, name) -> None:
+    """A kernel runs on the current device: its tensors must lie there."""
+    if t.is_cuda and _current_device is not None and t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
 
 
 def workspace_bytes(desc) -> int:
@@ -391,11 +414,12 @@ def combine_backward(desc, dout, dst_slot, weights, dy, workspace, expert_out=No
     shape = dy.shape
     if len(shape) != 2:
         raise ValueError("dy must be [capacity, H]")
+    _here(dy, "dy")
     cap, H = shape
     if dweights is not None and expert_out is None:
         raise ValueError("dweights needs expert_out")
     st = load_library().moe_combine_backward(
-        ctypes.byref(_desc(desc)), _like(dout, (N, H), "dout", torch.bfloat16), H,
+        _desc_ref(N, K, E, int(desc.num_ranks), int(desc.alignment)), _like(dout, (N, H), "dout", torch.bfloat16), H,
         _dev(dst_slot, "dst_slot", torch.int32, N * K), _dev(weights, "weights", torch.float32, N * K),
         _like(expert_out, shape, "expert_out", torch.bfloat16), _like(dy, shape, "dy", torch.bfloat16), cap,
         _dev(dweights, "dweights", torch.float32, N * K, allow_none=True),
@@ -654,15 +678,6 @@ def _norm_types(stream, weight, cols):
     return stream is torch.float32, weight.dtype is torch.float32
 
 
-def _like(t, shape, name, dtype):
-    """Pointer of a contiguous device tensor of exactly this shape and type, or None."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return _dev(t, name, dtype)
 
 
 def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, residual_out=None, rstd=None, eps=1e-6, total_rows=None,
@@ -676,6 +691,7 @@ def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, residual_out=Non
     shape = x.shape
     if len(shape) != 2:
         raise ValueError("x must be [rows, cols]")
+    _here(x, "x")
     rows, cols = shape
     if (residual is None) != (residual_out is None):
         raise ValueError("residual and residual_out go together")
@@ -716,6 +732,7 @@ def rms_norm_backward(dy, z, rstd, weight, dz, dresidual=None, dx=None, dweight=
     shape, kind = dy.shape, z.dtype
     if len(shape) != 2:
         raise ValueError("dy must be [rows, cols]")
+    _here(dy, "dy")
     rows, cols = shape
     fp32, weight_fp32 = _norm_types(kind, weight, cols)
     if dweight is not None and workspace is None:

@@ -1,6 +1,6 @@
-"""A mixture-of-experts layer in 8-bit floating point on the library's calls.
+"""A mixture-of-experts layer in 8-bit floating point on the library's calls, and a block around it.
 
-    python examples/moe_layer.py            # one serving pass and one training step on cuda:0
+    python examples/moe_layer.py            # one serving pass and one training step of each on cuda:0
 
 Serving (``MoELayer.serve``): gate -> 8-bit rows -> layout and dispatch -> gate/up
 product -> SwiGLU -> down product -> combine.  Rows travel through the dispatch in
@@ -8,9 +8,13 @@ product -> SwiGLU -> down product -> combine.  Rows travel through the dispatch 
 
 Training (``MoELayer.step``): the same with bf16 rows dispatched (the weight
 gradients quantise them down the columns too), then every gradient: expert
-weights, router, and the input's share through the experts.  The weighted sum's
-own gradient (a product of rows and a dot product) and the activation's bf16 rows
-for the second weight gradient are plain torch here.
+weights, router, and the input's share through the experts.  The activation's
+bf16 rows for the second weight gradient are plain torch here.
+
+``MoEBlock`` puts the residual stream in front: its addition and norm in one call,
+whose bf16 rows the router reads and whose 8-bit rows the dispatch moves, and
+routing by sigmoid + correction bias within a token's best groups of experts.  The
+bias follows the load: experts with more than their share become less attractive.
 """
 from __future__ import annotations
 
@@ -43,7 +47,7 @@ def transpose_weights(q: torch.Tensor, sf: torch.Tensor):
 
 class MoELayer:
     def __init__(self, hidden, width, num_experts, topk, num_ranks=1, alignment=128, balance_coef=0.01, seed=0,
-                 device="cuda"):
+                 device="cuda", cfg=None):
         g = torch.Generator(device=device).manual_seed(seed)
         rand = lambda *s, scale: torch.randn(s, generator=g, device=device) * scale
         self.hidden, self.width, self.E, self.K = hidden, width, num_experts, topk
@@ -51,7 +55,8 @@ class MoELayer:
         self.router = rand(num_experts, hidden, scale=hidden ** -0.5)
         self.gate_up, self.gate_up_sf = quantize_weights(rand(num_experts, 2 * width, hidden, scale=hidden ** -0.5))
         self.down, self.down_sf = quantize_weights(rand(num_experts, hidden, width, scale=width ** -0.5))
-        self.cfg = binding.GateConfig(score="softmax", normalize=True, scale=1.0, balance_coef=balance_coef)
+        self.cfg = cfg or binding.GateConfig(score="softmax", normalize=True, scale=1.0, balance_coef=balance_coef)
+        self.bias = None                # [experts], for the choice of experts
 
     def _plan(self, N):
         """Buffers of one batch size."""
@@ -64,12 +69,19 @@ class MoELayer:
         return torch.empty(shape, dtype=dtype, device=self.device)
 
     def serve(self, x):
-        N, H, I = x.shape[0], self.hidden, self.width
-        desc, cap, gate, lay = self._plan(N)
-        gate.forward(x.float() @ self.router.t())
-        lay.build(gate.topk_idx)
-        q, sf = self._empty(N, H, dtype=E4M3), self._empty(N, -(-H // BLOCK), dtype=torch.float32)
+        q, sf = self.rows_8bit(x.shape[0])
         binding.quantize_rows(x, q, sf)
+        return self.serve_rows(x, q, sf)
+
+    def rows_8bit(self, N):
+        return self._empty(N, self.hidden, dtype=E4M3), self._empty(N, -(-self.hidden // BLOCK), dtype=torch.float32)
+
+    def serve_rows(self, x, q, sf):
+        """``x`` [N, H] for the router, ``q`` and ``sf`` its 8-bit rows for the dispatch."""
+        N, H = x.shape[0], self.hidden
+        desc, cap, gate, lay = self._plan(N)
+        gate.forward(x.float() @ self.router.t(), bias=self.bias)
+        lay.build(gate.topk_idx)
         recv, recv_sf = self._empty(cap, H, dtype=E4M3), binding.new_sf_col_major(sf.shape[1], cap, device=self.device)
         lay.permute(q, recv)
         lay.permute_sf_col_major(sf, recv_sf)
@@ -105,7 +117,7 @@ class MoELayer:
         N, H, I, E, K = x.shape[0], self.hidden, self.width, self.E, self.K
         desc, cap, gate, lay = self._plan(N)
         logits = x.float() @ self.router.t()
-        gate.forward(logits)
+        gate.forward(logits, bias=self.bias)
         lay.build(gate.topk_idx)
         recv = self._empty(cap, H)
         lay.permute(x, recv)
@@ -115,13 +127,8 @@ class MoELayer:
         lay.combine(y, gate.weights, out)
 
         # the weighted sum: y_row's gradient is its weight times the token's, a weight's the rows' dot product
-        slot = lay.dst_slot[: N * K].long()
-        routed = slot >= 0
-        at = slot.clamp(min=0)
-        token = torch.arange(N * K, device=self.device) // K
-        dy = torch.zeros((cap, H), dtype=torch.bfloat16, device=self.device)
-        dy[at[routed]] = (gate.weights.view(-1, 1) * dout.float()[token])[routed].to(torch.bfloat16)
-        dweights = torch.where(routed, (y.float()[at] * dout.float()[token]).sum(1), 0.0).view(N, K)
+        dy, dweights = self._empty(cap, H), self._empty(N, K, dtype=torch.float32)
+        lay.combine_backward(dout, gate.weights, dy, y, dweights)
 
         down_t, gate_up_t = transpose_weights(self.down, self.down_sf), transpose_weights(self.gate_up, self.gate_up_sf)
         dh = self._empty(cap, I)
@@ -154,6 +161,39 @@ class MoELayer:
                 raise RuntimeError(f"{name}: {binding.ERROR_NAMES.get(code, code)}")
 
 
+class MoEBlock:
+    """residual += x, norm, routing by groups, experts: a block's second half."""
+
+    def __init__(self, hidden, width, num_experts, topk, num_groups, topk_groups, eps=1e-6, bias_rate=1e-3, seed=0,
+                 device="cuda", **kw):
+        cfg = binding.GateConfig(score="sigmoid", normalize=True, scale=2.5, balance_coef=1e-3, bias_on="score",
+                                 num_groups=num_groups, topk_groups=topk_groups, group_sum=2)
+        self.layer = MoELayer(hidden, width, num_experts, topk, seed=seed, device=device, cfg=cfg, **kw)
+        self.layer.bias = torch.zeros(num_experts, device=device)
+        self.weight = torch.ones(hidden, dtype=torch.bfloat16, device=device)
+        self.eps, self.bias_rate, self.device = eps, bias_rate, device
+
+    def serve(self, x, residual):
+        """The layer's output; ``residual`` is updated in place."""
+        y = torch.empty_like(x)
+        q, sf = self.layer.rows_8bit(x.shape[0])
+        binding.rms_norm(x, self.weight, y=y, q=q, sf=sf, residual=residual, residual_out=residual, eps=self.eps)
+        return self.layer.serve_rows(y, q, sf)
+
+    def step(self, x, residual, dout, dresidual):
+        """Outputs of ``serve`` with the new residual, and the gradients of out . dout + residual . dresidual + loss."""
+        N, H = x.shape
+        y, z, rstd = torch.empty_like(x), torch.empty_like(residual), torch.empty(N, device=self.device)
+        binding.rms_norm(x, self.weight, y=y, residual=residual, residual_out=z, rstd=rstd, eps=self.eps)
+        r = self.layer.step(y, dout)
+        dz, dweight = torch.empty_like(z), torch.empty(H, device=self.device)
+        binding.rms_norm_backward(r["dx"], z, rstd, self.weight, dz, dresidual=dresidual, dweight=dweight,
+                                  workspace=binding.new_norm_workspace(H, self.device))
+        count = r["expert_count"].float()
+        self.layer.bias += self.bias_rate * torch.sign(count.mean() - count)      # takes part in the next choice only
+        return dict(r, residual=z, dx=dz, weight=dweight)
+
+
 if __name__ == "__main__":
     layer = MoELayer(hidden=1024, width=512, num_experts=16, topk=4)
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -165,3 +205,9 @@ if __name__ == "__main__":
           float((served.float() - got["out"].float()).norm() / served.float().norm()))
     print("balance loss", float(got["loss"]), " tokens an expert", got["expert_count"].tolist())
     print("gradient norms", {k: round(float(got[k].float().norm()), 4) for k in ("dx", "router", "gate_up", "down")})
+    block = MoEBlock(hidden=1024, width=512, num_experts=32, topk=4, num_groups=8, topk_groups=4)
+    residual = torch.randn((2000, 1024), generator=g, device="cuda").to(torch.bfloat16)
+    got = block.step(x, residual, dout, dout)
+    served = block.serve(x, residual)
+    print("block: residuals equal", torch.equal(residual, got["residual"]), " tokens an expert", got["expert_count"].tolist())
+    print("gradient norms", {k: round(float(got[k].float().norm()), 4) for k in ("dx", "weight", "router", "gate_up", "down")})

@@ -143,3 +143,38 @@ def test_norm_formula_against_differences():
                 sides.append(float((y(z, w) * dy).sum()))
             arg.view(-1)[i] = keep
             assert abs((sides[0] - sides[1]) / 2e-5 - float(grad.reshape(-1)[i])) < 1e-7
+
+
+def test_python_refusals():
+    """What the binding refuses by itself, before a pointer is taken: shapes, types, what belongs together."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    x, w = bf(4, 256), bf(256)
+    for kw in (dict(residual=x), dict(q=x), dict(sf=x), dict(residual=bf(4, 256).half(), residual_out=x)):
+        with pytest.raises(ValueError):
+            binding.rms_norm(x, w, y=x, **kw)
+    with pytest.raises(ValueError):
+        binding.rms_norm(bf(256), w, y=x)
+    with pytest.raises(ValueError):
+        binding.rms_norm(x, bf(128), y=x)
+    with pytest.raises(ValueError):
+        binding.rms_norm(x, w.half(), y=x)
+    with pytest.raises(ValueError):
+        binding.rms_norm_backward(x, x, torch.zeros(4), w, x, dweight=torch.zeros(256))
+    desc = binding.LayoutDesc(4, 2, 8, 1, 1)
+    with pytest.raises(ValueError):
+        binding.combine_backward(desc, x, torch.zeros(8, dtype=torch.int32), torch.zeros(4, 2), bf(8, 256), x, dweights=torch.zeros(4, 2))
+    with pytest.raises(ValueError):
+        binding.combine_backward(desc, x, torch.zeros(8, dtype=torch.int32), torch.zeros(4, 2), bf(8, 128), x)
+
+
+def test_a_tensor_elsewhere_is_refused(monkeypatch):
+    """Tensors of another device than the current one."""
+    class Elsewhere:
+        is_cuda, device = True, "cuda:1"
+        get_device = staticmethod(lambda: 1)
+
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    with pytest.raises(ValueError):
+        binding._here(Elsewhere(), "x")
+    monkeypatch.setattr(binding, "_current_device", lambda: 1)
+    binding._here(Elsewhere(), "x")
