@@ -9,14 +9,24 @@
 //
 // Keys are numbers, not their approximations in 32 bits: two of them may lie closer than
 // those err (their order then hangs on how a sigmoid was computed).  So a warp compares in
-// 32 bits with the errors' bound in hand, and where a decision lies within it, that token's
-// is done again with keys of two floats (exact_picks), after the loop over the tokens: calls
-// within it cost all tokens registers (131072 x 384 in 16 groups 194 us, 168 without them).
-// Equal logits with equal biases tie exactly, and where no bias differs from another the
-// order of the logits is that of the keys; neither is left open.
+// 32 bits with the errors' bound in hand, and a token with a decision within it (a few in ten
+// thousand) is done again with keys of two floats after the loop over the tokens: one that
+// has its candidates listed from those (exact_rank, about 1 us), others from all experts
+// (exact_picks, about 8).  Calls within the loop cost all tokens registers (131072 x 384 in 16
+// groups 194 us, 168 without them).  Equal logits with equal biases tie exactly, and where
+// no bias differs from another the order of the logits is that of the keys; neither is left open.
 //
-// One warp a token, as in the gate (gate_kernels.cu, whose list of candidates this is).
-// The groups' two largest keys: 32 / G lanes a group walk its keys in shared memory.
+// One warp a token, as in the gate (gate_kernels.cu).  A lane has V columns side by side where
+// they are of one group and rows lie on vectors' boundaries: the groups' two largest keys then
+// come from registers and shuffles (else 32 / G lanes a group walk its keys in shared
+// memory).  Candidates are the keys from a bound on: what the token before had as its K-th
+// key, a little lower; or, if fewer than K or more than 32 reach that, the K-th largest of the
+// lanes' two largest.  The bound changes the work, not the result.
+//
+// 131072 x 384, sigmoid with bias, top-8: 135 us, in 16 groups of which 4 stay 172 (256 experts
+// in 8 groups 156); the logits once are 201 MB, 30 us.  It is bound by its instructions, 850 to
+// 1100 a token, of which 500 do not depend on the number of experts (ncu: issue slots 56 % busy,
+// ALU 58 %, DRAM 16 %).  64 x 256 in 8 groups: 8.8 us a call, the launch and one token's chain.
 #include <cfloat>
 
 #include "gate_common.cuh"
@@ -425,7 +435,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
       const auto near = [&](float x, float y) {
         return biased && fabsf(x - y) <= 2.0f * err + 0x1p-23f * fmaxf(fabsf(x), fabsf(y));
       };
-      bool exact = false;                  // the choice is left open
+      bool exact = false;                // the choice is left open
       float hi = -INFINITY, lo = -INFINITY;   // the lane's largest keys
       if (limited && !by_logit) {
 #pragma unroll
@@ -443,7 +453,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
           hi = fmaxf(hi, key[i]);
         }
       }
-      float own_hi = hi, own_lo = lo;      // of the lane's keys, for the choice
+      float own_hi = hi, own_lo = lo;    // of the lane's keys, for the choice
       bool held = true;                  // the lane's experts (BLOCKED) are of a kept group
       unsigned kept = kFull;
       if (limited) {
@@ -488,16 +498,17 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
           const bool there = score > -INFINITY;
           const unsigned reach = __reduce_max_sync(kFull, there && !held ? sortable(score + off) : 0u);
           const unsigned least = __reduce_min_sync(kFull, held ? sortable(score - off) : kFull);
-          exact = reach >= least;
+          exact = route && reach >= least;
         }
-        if (!BLOCKED)
+        if (!BLOCKED) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const unsigned g = static_cast<unsigned>(route_column<V, BLOCKED>(lane, i)) * inverse >> 22;
             if (!(kept >> (g & 31) & 1)) key[i] = -INFINITY;
           }
-        else if (!held)
+        } else if (!held) {
           own_hi = own_lo = -INFINITY;
+        }
       }
       // Few lanes have keys left, or many picks are wanted: a lane's second counts too.
       if ((limited && !(BLOCKED && biased && !by_logit)) || (!limited && K > 8)) {
@@ -608,6 +619,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
             slot = before;
           }
         } else {
+          // More than a list holds: one pick after the other, and one more to look behind the last.
           float last_key = INFINITY, last_l = 0.0f, last_b = 0.0f;
           float h;
           for (int k = 0; k <= K && top > kKeyNegInf; ++k) {
@@ -668,7 +680,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
   __syncwarp();
   if (late.found > 0 || any_open)
     settle_open<T, SIGMOID>(a, bias_s, biased, key64, cnt_s, late, any_open,
-                               static_cast<int64_t>(blockIdx.x) * kGateWarps + warp, stride);
+                            static_cast<int64_t>(blockIdx.x) * kGateWarps + warp, stride);
   if (lane == 0 && routed > 0) atomicAdd(&cnt_s[E], routed);
   add_columns<V>(acc, E, sum_s, [](int l, int i) { return route_column<V, BLOCKED>(l, i); });
   finish_sums(a, sum_s, cnt_s, red_s, last_s);

@@ -188,6 +188,11 @@ def test_rows_that_cannot_be_routed():
     check(gate, r)
     gate = route(l[:1], torch.where(torch.arange(32) == 7, float("nan"), b), 4, "sigmoid", 4, 2, 2)
     assert gate.error() == 1 and torch.all(gate.topk_idx == -1) and int(gate.routed_tokens) == 0
+    # the same where every group ties, so that the groups alone would leave the choice open
+    for value in (float("nan"), float("inf")):
+        gate = route(torch.zeros((40, 32)), torch.where(torch.arange(32) == 7, value, torch.arange(32) % 8 * 0.1), 4, "sigmoid", 4, 2, 2)
+        assert gate.error() == 1 and torch.all(gate.topk_idx == -1) and torch.all(gate.weights == 0)
+        assert int(gate.routed_tokens) == 0 and int(gate.expert_count.sum()) == 0
 
 
 def test_experts_closed_by_their_bias():
