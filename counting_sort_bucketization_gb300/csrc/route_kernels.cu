@@ -35,12 +35,15 @@ namespace moe {
 namespace {
 
 // Bounds of what a 32-bit score errs by, of the row's largest score (a sigmoid counts as 1/8
-// at most).  e^x as 2^(x log2 e) errs by 1.5 * 2^-24 |x| + 2^-22 of itself.  Sigmoid: |x| <= 21
-// unless all are tiny (then they are e^(x - max)), and two roundings and a reciprocal's 2^-23:
-// 2^-18.7 of a small one; near 1 what e^-x errs by counts s (1 - s), 2^-21.9 in all.  Softmax: a
-// sum of up to 37 additions one after the other, and a quotient: 2^-18.6.
+// at most), u = 2^-24.
+// Sigmoid: e^-x as 2^(-x log2 e) errs by (1.5 |x| + 4) u of itself, 1 + e^-x and the reciprocal by
+// 3 u more; |x| <= 28 unless the scores' sum is tiny (then they are e^(x - max)).  48 u of a small
+// score; of one near 1 e^-x's error counts s (1 - s): 4.4 u.
 constexpr float kErrSigmoid = 0x1p-18f;
-constexpr float kErrSoftmax = 0x1p-18f;
+// Softmax: e^x errs by (2.5 |x| + 4) u of itself, 5 u of the largest; the sum by as much in the
+// mean, where |x| is at most log E, and by V + 5 additions; the quotient by 5 u.
+template <int V>
+constexpr float kErrSoftmax = (V + 48) * 0x1p-24f;
 
 // Numbers as sums of two floats, good to about 2^-46: hi is the sum rounded, lo the rest.
 // (The 64-bit unit does 2 multiply-adds a cycle and SM; a token redone with it took 40 us.)
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
       // (a sigmoid is below e^m)
       float most = factor;
       if (SIGMOID) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(most) : "f"(m * 1.4426950408889634f));
-      const float err = (SIGMOID ? 1.01f * kErrSigmoid * fminf(most, 0.125f) : kErrSoftmax * most) + 0x1p-120f;
+      const float err = (SIGMOID ? 1.01f * kErrSigmoid * fminf(most, 0.125f) : kErrSoftmax<V> * most) + 0x1p-120f;
       const auto near = [&](float x, float y) {
         return biased && fabsf(x - y) <= 2.0f * err + 0x1p-23f * fmaxf(fabsf(x), fabsf(y));
       };
