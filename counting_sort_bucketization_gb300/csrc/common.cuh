@@ -85,7 +85,7 @@ inline WorkspaceLayout make_workspace_layout(const moe_layout_desc& d, const Til
 // everything before its immediate predecessor on the stream has completed,
 // and it may read before its wait whatever no kernel of the library that
 // triggers writes: the routing ids (topk_idx) and the token rows and scale rows
-// (x, sf).  The gate and the quantisers write those and never trigger: their
+// (x, sf).  The gate, the norm and the quantisers write those and never trigger: their
 // dependents start after they have ended.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,

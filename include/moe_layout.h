@@ -442,8 +442,8 @@ typedef struct moe_gate_groups {
  *   the K largest keys of those groups, in descending order, equal keys by ascending id;
  *   ids, weights (of s, without the bias), counts and balance loss as in moe_gate_forward.
  * Keys are compared as numbers, not as what 32 bits make of them: what fp32 leaves open is
- * settled in 64 bits.  Where all biases are equal the order of the keys is that of the
- * logits.
+ * settled to about 2^-46 (scores below 2^-124 may count as zeros there).  Where all biases
+ * are equal the order of the keys is that of the logits.
  * Tokens with a NaN or +inf among their logits or keys are not routed and record
  * MOE_ERR_INVALID_ARG.
  */
