@@ -252,3 +252,36 @@ def test_other_stream_and_graph():
     want, off, want_w, off_w = grad(y, z, rstd, w, None, 300)
     assert torch.all((dz.double() - want).abs() <= off + HALF[BF16] * want.abs())
     assert torch.all((dw.double() - want_w).abs() <= off_w)
+
+
+def test_on_a_named_stream():
+    """The ``stream`` argument of the norm, its gradient, the routing and the combine's gradient: work that is behind a
+    long wait on that stream is not done before it, and is done after."""
+    x, res, w = draw(64, 1040, 11)
+    s = torch.cuda.Stream()
+    y, z, dz = (torch.zeros_like(x) for _ in range(3))
+    rstd, dw, ws = torch.zeros(64, device=DEV), torch.zeros(1040, device=DEV), binding.new_norm_workspace(1040)
+    desc = binding.LayoutDesc(64, 2, 8, 1, 1)
+    gate = binding.Gate(desc, binding.GateConfig("sigmoid", bias_on="score", num_groups=4, topk_groups=2, group_sum=2))
+    l = torch.randn((64, 8), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    lay = binding.Layout(desc, 128)
+    dy, dwk = torch.zeros((128, 1040), dtype=BF16, device=DEV), torch.zeros((64, 2), device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)          # about a tenth of a second
+    binding.rms_norm(x, w, y=y, residual=res, residual_out=z, rstd=rstd, eps=EPS, stream=s)
+    binding.rms_norm_backward(y, z, rstd, w, dz, dweight=dw, workspace=ws, stream=s)
+    gate.forward(l, stream=s)
+    lay.build(gate.topk_idx, stream=s)
+    lay.combine_backward(y, gate.weights, dy, dy, dwk, stream=s)
+    early = y.clone()                           # on the current stream, which does not wait
+    torch.cuda.current_stream().synchronize()
+    assert not early.any()
+    s.synchronize()
+    check(dict(z=z, y=y, rstd=rstd), x, w, res)
+    want, off, want_w, off_w = grad(y, z, rstd, w, None, 64)
+    assert torch.all((dz.double() - want).abs() <= off + HALF[BF16] * want.abs())
+    assert torch.all((dw.double() - want_w).abs() <= off_w)
+    slot = lay.dst_slot[:128].long()
+    assert torch.equal(dy[slot], (gate.weights.view(-1, 1) * y.float().repeat_interleave(2, 0)).to(BF16))
+    assert gate.error() == 0 and lay.error() == 0
