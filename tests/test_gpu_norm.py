@@ -266,15 +266,24 @@ def test_on_a_named_stream():
     l = torch.randn((64, 8), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
     lay = binding.Layout(desc, 128)
     dy, dwk = torch.zeros((128, 1040), dtype=BF16, device=DEV), torch.zeros((64, 2), device=DEV)
+
+    def run():
+        binding.rms_norm(x, w, y=y, residual=res, residual_out=z, rstd=rstd, eps=EPS, stream=s)
+        binding.rms_norm_backward(y, z, rstd, w, dz, dweight=dw, workspace=ws, stream=s)
+        gate.forward(l, stream=s)
+        lay.build(gate.topk_idx, stream=s)
+        lay.combine_backward(y, gate.weights, dy, dy, dwk, stream=s)
+        return y.clone()                        # on the current stream, which does not wait
+
+    torch.cuda.synchronize()
+    run()                                       # a kernel's first launch loads it, which may wait for the device
+    torch.cuda.synchronize()
+    for t in (y, z, dz, rstd, dw, dy, dwk):
+        t.zero_()
     torch.cuda.synchronize()
     with torch.cuda.stream(s):
         torch.cuda._sleep(200_000_000)          # about a tenth of a second
-    binding.rms_norm(x, w, y=y, residual=res, residual_out=z, rstd=rstd, eps=EPS, stream=s)
-    binding.rms_norm_backward(y, z, rstd, w, dz, dweight=dw, workspace=ws, stream=s)
-    gate.forward(l, stream=s)
-    lay.build(gate.topk_idx, stream=s)
-    lay.combine_backward(y, gate.weights, dy, dy, dwk, stream=s)
-    early = y.clone()                           # on the current stream, which does not wait
+    early = run()
     torch.cuda.current_stream().synchronize()
     assert not early.any()
     s.synchronize()
