@@ -24,9 +24,10 @@
 // lanes' two largest.  The bound changes the work, not the result.
 //
 // 131072 x 384, sigmoid with bias, top-8: 135 us, in 16 groups of which 4 stay 172 (256 experts
-// in 8 groups 156); the logits once are 201 MB, 30 us.  It is bound by its instructions, 850 to
-// 1100 a token, of which 500 do not depend on the number of experts (ncu: issue slots 56 % busy,
-// ALU 58 %, DRAM 16 %).  64 x 256 in 8 groups: 8.8 us a call, the launch and one token's chain.
+// in 8 groups 156); the logits once are 201 MB, 30 us.  It is bound by its instructions, 780 a
+// token (in 16 groups 960; 128 experts 620, so most do not depend on their number; 440 are the
+// choice and the weights), and their chain (ncu: issue slots 56 % busy, ALU 58 %, DRAM 16 %).
+// 64 x 256 in 8 groups: 8.8 us a call, the launch and one token's chain.
 #include <cfloat>
 
 #include "gate_common.cuh"
