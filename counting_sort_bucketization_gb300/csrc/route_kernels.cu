@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
           for (int i = 0; i < V; ++i) add_best(own_hi, own_lo, key[i]);
       }
       if (route && !exact) {
+        // Keys from `least` on, which is above -inf: that is the key of closed experts and past E.
         const auto mark = [&](float least) {
           unsigned bits = 0;
           if (!BLOCKED || held)
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
           float least = -FLT_MAX;
           if (floor > kKeyNegInf) {
             least = unsortable(floor);
-            if (biased) least -= 2.0f * err + 0x1p-22f * fabsf(least);
+            if (biased) least = fmaxf(least - (2.0f * err + 0x1p-22f * fabsf(least)), -FLT_MAX);
           }
           bits = mark(least);
           count(bits);
@@ -612,10 +613,10 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
           }
           if (found >= K) {
             const float last = list_k[K - 1];
-            if (few) slack = fmaxf(2.0f * slack, 0x1p-4f * (list_k[0] - last) + 0x1p-8f * fabsf(last));
+            if (few) slack = fminf(fmaxf(2.0f * slack, 0x1p-4f * (list_k[0] - last) + 0x1p-8f * fabsf(last)), FLT_MAX);
             else if (many) slack *= 0.5f;
             else if (found > 20) slack *= 0.75f;
-            guess = last - slack;
+            guess = fmaxf(last - slack, -FLT_MAX);   // a key may be the type's lowest value
           }
           candidate = id;
           if (lane < found) {
