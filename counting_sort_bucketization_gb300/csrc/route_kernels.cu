@@ -111,6 +111,7 @@ __device__ __forceinline__ uint64_t ordered(Two k) {
 __device__ __forceinline__ Two number(uint64_t u) {
   return {unsortable(static_cast<unsigned>(u >> 32)), unsortable(static_cast<unsigned>(u))};
 }
+__device__ __forceinline__ Two half(Two k) { return {0.5f * k.hi, 0.5f * k.lo}; }
 __device__ __forceinline__ Two plus_bias(Two s, float b) {
   const Two k = exact_sum(s.hi, b);
   return quick_sum(k.hi, __fadd_rn(k.lo, s.lo));
@@ -174,7 +175,9 @@ __device__ __noinline__ int exact_picks(const GateArgs& a, const T* row, float m
         lo = max(lo, min(hi, k));
         hi = max(hi, k);
       }
-      score = a.group_sum == 2 && lo > 0 ? ordered(add(number(hi), number(lo))) : hi;
+      // Halves, which add without an overflow; a group's only key is halved too.
+      if (a.group_sum == 1 || hi == 0) score = hi;
+      else score = ordered(lo > 0 ? add(half(number(hi)), half(number(lo))) : half(number(hi)));
     }
     unsigned kept = 0;
     for (int j = 0; j < a.topk_groups; ++j) {
@@ -485,8 +488,11 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
             merge_best(hi, lo, __shfl_xor_sync(kFull, hi, o), __shfl_xor_sync(kFull, lo, o));
           __syncwarp();                  // the keys are read
         }
-        const float score = group < G ? (a.group_sum == 2 && lo > -INFINITY ? hi + lo : hi) : -INFINITY;
-        const float off = by_logit ? 0.0f : 2.0f * err + 0x1p-23f * (fabsf(hi) + (lo > -INFINITY ? fabsf(lo) : 0.0f));
+        // Half the sum of two (two keys of the lowest value would add to -inf, a closed group's score), and
+        // what it may err by: half of two keys' errors, their roundings and the sum's.
+        const float second = lo > -INFINITY ? 0.5f * lo : 0.0f;
+        const float score = group >= G ? -INFINITY : a.group_sum == 2 ? 0.5f * hi + second : hi;
+        const float off = by_logit ? 0.0f : err + 0x1p-23f * (0.5f * fabsf(hi) + fabsf(second));
         unsigned rest = sortable(score + 0.0f);
         kept = 0;
         held = false;

@@ -30,7 +30,7 @@ def plain(l, b, K, score, G, kept, group_sum):
     """Ids, normalised weights and the means of the scores' shares (of their logarithms: they may be below 64 bits)."""
     N, E = l.shape
     x = l.double()
-    shift = torch.zeros(E, dtype=torch.float64, device=DEV) if b is None else torch.where(b == LOWEST, -64.0, b.double())
+    shift = torch.zeros(E, dtype=torch.float64, device=DEV) if b is None else torch.where(b.abs() == -LOWEST, 64.0 * b.sign(), b).double()
     open_ = (x > float("-inf")) & (shift > float("-inf"))
     s = torch.sigmoid(x) if score == "sigmoid" else torch.nan_to_num(torch.softmax(x, 1))
     key = torch.where(open_, s + shift, float("-inf"))
@@ -108,3 +108,24 @@ def test_biases_of_the_lowest_value(E, K, G, kept, score):
         masked = torch.where(torch.arange(E, device=DEV) < open_, b, LOWEST)
         masked[E // 3] = float("-inf")
         check(l, masked, K, score, G, kept)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("value", [LOWEST, -LOWEST])
+@pytest.mark.parametrize("E,G,kept,K", [(24, 3, 1, 4), (24, 3, 2, 6), (64, 8, 4, 6), (64, 32, 5, 6), (96, 12, 7, 12), (256, 8, 3, 8), (60, 12, 4, 8)])
+def test_groups_of_extreme_biases(E, G, kept, K, value, score):
+    """Two such keys add to the group's score without an overflow: a masked group is the last that stays, above closed
+    ones, and never before another; one of the largest value is the first.  Also where every choice of groups is left
+    open (all biases and scores equal but for the masked groups')."""
+    per = E // G
+    l, b, some = draw(6000, E, 5 * E + G)
+    l = torch.round(l * 16) / 16 + 2.0 ** -6          # no two whose sigmoids add to one
+    b = b if score == "sigmoid" else b * 0.1
+    g = torch.arange(E, device=DEV) // per
+    for some_groups in ([1], [0, 2], list(range(1, G)), list(range(G))):
+        b2 = torch.where(torch.isin(g, torch.tensor(some_groups, device=DEV)), value, b)
+        check(l, b2, K, score, G, kept, 2)
+        b2[0] = b2[E // 2] = float("-inf")
+        check(l, b2, K, score, G, kept, 2)
+        b2 = torch.where(torch.isin(g, torch.tensor(some_groups, device=DEV)), value, 0.25 * (torch.arange(E, device=DEV) % per % 2))
+        check(torch.zeros_like(l), b2, K, score, G, kept, 2)
