@@ -573,6 +573,13 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
           count(bits);
           edge = -FLT_MAX;               // further below
         }
+        // The next token's guess, from this one's first and K-th key.  (A key may be the type's lowest value.)
+        const auto expect = [&](float first, float last) {
+          if (few) slack = fminf(fmaxf(2.0f * slack, 0x1p-4f * (first - last) + 0x1p-8f * fabsf(last)), FLT_MAX);
+          else if (many) slack *= 0.5f;
+          else if (found > 20) slack *= 0.75f;
+          guess = fmaxf(last - slack, -FLT_MAX);
+        };
         float picked = 0.0f, score = 0.0f;   // the pick's logit and score
         int candidate = 0;
         bool beyond = false;             // what is not listed may belong to the picks
@@ -617,13 +624,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
               exact |= load_logit(row + other) != l || bias_s[other] != bias;
             }
           }
-          if (found >= K) {
-            const float last = list_k[K - 1];
-            if (few) slack = fminf(fmaxf(2.0f * slack, 0x1p-4f * (list_k[0] - last) + 0x1p-8f * fabsf(last)), FLT_MAX);
-            else if (many) slack *= 0.5f;
-            else if (found > 20) slack *= 0.75f;
-            guess = fmaxf(last - slack, -FLT_MAX);   // a key may be the type's lowest value
-          }
+          if (found >= K) expect(list_k[0], list_k[K - 1]);
           candidate = id;
           if (lane < found) {
             if (before < K) mine = id, picked = l;
@@ -631,7 +632,8 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
           }
         } else {
           // More than a list holds: one pick after the other, and one more to look behind the last.
-          float last_key = INFINITY, last_l = 0.0f, last_b = 0.0f;
+          const float first = unsortable(top);
+          float last_key = first, last_l = 0.0f, last_b = 0.0f;
           float h;
           for (int k = 0; k <= K && top > kKeyNegInf; ++k) {
             const float want = unsortable(top);
@@ -642,8 +644,9 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
                 if (key[i] == want) lowest = static_cast<unsigned>(route_column<V, BLOCKED>(lane, i));
             const unsigned id = __reduce_min_sync(kFull, lowest);
             const float lk = load_logit(row + id), bk = bias_s[id];
-            if (near(last_key, want) && (lk != last_l || bk != last_b)) exact = true;
+            if (k > 0 && near(last_key, want) && (lk != last_l || bk != last_b)) exact = true;
             last_key = want, last_l = lk, last_b = bk;
+            if (k == K - 1) expect(first, want);
             if (lane == k && k < K) mine = id, picked = lk, score = SIGMOID ? sigmoid(lk) : exp_neg(lk - m) * inv;
             h = -INFINITY;
             if (!BLOCKED || held)
