@@ -573,13 +573,6 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
           count(bits);
           edge = -FLT_MAX;               // further below
         }
-        // The next token's guess, from this one's first and K-th key.  (A key may be the type's lowest value.)
-        const auto expect = [&](float first, float last) {
-          if (few) slack = fminf(fmaxf(2.0f * slack, 0x1p-4f * (first - last) + 0x1p-8f * fabsf(last)), FLT_MAX);
-          else if (many) slack *= 0.5f;
-          else if (found > 20) slack *= 0.75f;
-          guess = fmaxf(last - slack, -FLT_MAX);
-        };
         float picked = 0.0f, score = 0.0f;   // the pick's logit and score
         int candidate = 0;
         bool beyond = false;             // what is not listed may belong to the picks
@@ -624,7 +617,14 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
               exact |= load_logit(row + other) != l || bias_s[other] != bias;
             }
           }
-          if (found >= K) expect(list_k[0], list_k[K - 1]);
+          // The next token's guess.  A key may be the type's lowest value.  What a row whose K-th key is a mask leaves
+          // as slack is gone after one ordinary row: only halved, -1e9 took 25 and the lowest value over 100.
+          if (found >= K) {
+            const float last = list_k[K - 1];
+            if (few) slack = fminf(fmaxf(2.0f * slack, 0x1p-4f * (list_k[0] - last) + 0x1p-8f * fabsf(last)), FLT_MAX);
+            else if (many || found > 20) slack = fminf((many ? 0.5f : 0.75f) * slack, list_k[0] - last + 0x1p-4f * fabsf(last));
+            guess = fmaxf(last - slack, -FLT_MAX);
+          }
           candidate = id;
           if (lane < found) {
             if (before < K) mine = id, picked = l;
@@ -646,7 +646,10 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
             const float lk = load_logit(row + id), bk = bias_s[id];
             if (k > 0 && near(last_key, want) && (lk != last_l || bk != last_b)) exact = true;
             last_key = want, last_l = lk, last_b = bk;
-            if (k == K - 1) expect(first, want);
+            if (k == K - 1 && want < first) {      // (a padding row's equal keys say nothing)
+              slack = fminf(fmaxf(few ? 2.0f * slack : 0.0f, 0x1p-4f * (first - want) + 0x1p-8f * fabsf(want)), FLT_MAX);
+              guess = fmaxf(want - slack, -FLT_MAX);
+            }
             if (lane == k && k < K) mine = id, picked = lk, score = SIGMOID ? sigmoid(lk) : exp_neg(lk - m) * inv;
             h = -INFINITY;
             if (!BLOCKED || held)
