@@ -13,8 +13,9 @@
 // thousand) is done again with keys of two floats after the loop over the tokens: one that
 // has its candidates listed from those (exact_rank, about 1 us), others from all experts
 // (exact_picks, about 8).  Calls within the loop cost all tokens registers (131072 x 384 in 16
-// groups 194 us, 168 without them).  Equal logits with equal biases tie exactly, and where
-// no bias differs from another the order of the logits is that of the keys; neither is left open.
+// groups 194 us, 168 without them).  Equal logits with equal biases tie exactly, experts and
+// groups whose largest keys are such, and where no bias differs from another the order of the
+// logits is that of the keys; none of these is left open.
 //
 // One warp a token, as in the gate (gate_kernels.cu).  A lane has V columns side by side where
 // they are of one group and rows lie on vectors' boundaries: the groups' two largest keys then
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
       }
       const float inv = __fdividef(1.0f, sum);
       float b[V];
-      if (biased || limited) {
+      if (biased) {
         if constexpr (BLOCKED && V % 4 == 0) {
 #pragma unroll
           for (int i = 0; i < V; i += 4) load4(bias_s + lane * V + i, b + i);
@@ -447,10 +448,9 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
       if (limited && !by_logit) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float k = key[i] > -INFINITY ? fmaf(s[i], factor, b[i]) : -INFINITY;
-          if (BLOCKED) add_best(hi, lo, k);
-          else key_s[route_column<V, BLOCKED>(lane, i)] = k;
-          if (biased) key[i] = k;
+          if (biased) key[i] = key[i] > -INFINITY ? fmaf(s[i], factor, b[i]) : -INFINITY;
+          if (BLOCKED) add_best(hi, lo, key[i]);
+          else key_s[route_column<V, BLOCKED>(lane, i)] = key[i];
         }
       } else {
 #pragma unroll
@@ -488,11 +488,16 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
             merge_best(hi, lo, __shfl_xor_sync(kFull, hi, o), __shfl_xor_sync(kFull, lo, o));
           __syncwarp();                  // the keys are read
         }
+        // Without a bias hi and lo are logits: the keys are their scores and the bias that all have.
+        const auto key_of = [&](float l) {
+          return l > -INFINITY ? (SIGMOID ? sigmoid(l) : exp_neg(fminf(l - m, 0.0f)) * inv) + bias_s[0] : -INFINITY;
+        };
+        const float k1 = biased || by_logit ? hi : key_of(hi), k2 = biased || by_logit ? lo : key_of(lo);
         // Half the sum of two (two keys of the lowest value would add to -inf, a closed group's score), and
         // what it may err by: half of two keys' errors, their roundings and the sum's.
-        const float second = lo > -INFINITY ? 0.5f * lo : 0.0f;
-        const float score = group >= G ? -INFINITY : a.group_sum == 2 ? 0.5f * hi + second : hi;
-        const float off = by_logit ? 0.0f : err + 0x1p-23f * (0.5f * fabsf(hi) + fabsf(second));
+        const float second = k2 > -INFINITY ? 0.5f * k2 : 0.0f;
+        const float score = group >= G ? -INFINITY : a.group_sum == 2 ? 0.5f * k1 + second : k1;
+        const float off = by_logit ? 0.0f : err + 0x1p-23f * (0.5f * fabsf(k1) + fabsf(second));
         unsigned rest = sortable(score + 0.0f);
         kept = 0;
         held = false;
@@ -506,9 +511,44 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
         if (!by_logit) {
           // What a group left may reach, and the least that a kept one may be.
           const bool there = score > -INFINITY;
-          const unsigned reach = __reduce_max_sync(kFull, there && !held ? sortable(score + off) : 0u);
-          const unsigned least = __reduce_min_sync(kFull, held ? sortable(score - off) : kFull);
-          exact = route && reach >= least;
+          const unsigned high = sortable(score + off), low = sortable(score - off);
+          const unsigned reach = __reduce_max_sync(kFull, there && !held ? high : 0u);
+          const unsigned least = __reduce_min_sync(kFull, held ? low : kFull);
+          if (route && reach >= least) {
+            // Groups that may be on either side are left open unless they tie exactly: equal logits as their two
+            // largest (keys: and nothing near one of them that is not the same logit and bias).
+            const bool between = held ? low <= reach : there && high >= least;
+            const unsigned own1 = sortable(hi + 0.0f), own2 = a.group_sum == 2 ? sortable(lo + 0.0f) : 0u;
+            const unsigned h1 = __reduce_max_sync(kFull, between ? own1 : 0u), h2 = __reduce_max_sync(kFull, between ? own2 : 0u);
+            exact = __any_sync(kFull, between && (own1 != h1 || own2 != h2));
+            if (biased && !exact) {
+              const unsigned groups = __reduce_or_sync(kFull, between ? 1u << group : 0u);
+              const float top1 = unsortable(h1), top2 = h2 > kKeyNegInf ? unsortable(h2) : top1;
+              const auto in_groups = [&](int i) {
+                return (groups >> (BLOCKED ? group : static_cast<unsigned>(route_column<V, BLOCKED>(lane, i)) * inverse >> 22 & 31) & 1) != 0;
+              };
+              unsigned at1 = E - 1, at2 = E - 1;
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                const unsigned col = route_column<V, BLOCKED>(lane, i);
+                if (key[i] == top1 && in_groups(i)) at1 = min(at1, col);
+                if (key[i] == top2 && in_groups(i)) at2 = min(at2, col);
+              }
+              at1 = __reduce_min_sync(kFull, at1);
+              at2 = __reduce_min_sync(kFull, at2);
+              const float l1 = load_logit(row + at1), b1 = bias_s[at1], l2 = load_logit(row + at2), b2 = bias_s[at2];
+              exact = top1 != top2 && near(top1, top2);
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                if (!(key[i] > -INFINITY) || !in_groups(i)) continue;
+                const bool first = near(key[i], top1);
+                if (!first && !near(key[i], top2)) continue;
+                const int col = route_column<V, BLOCKED>(lane, i);
+                exact |= load_logit(row + col) != (first ? l1 : l2) || bias_s[col] != (first ? b1 : b2);
+              }
+              exact = __any_sync(kFull, exact);
+            }
+          }
         }
         if (!BLOCKED) {
 #pragma unroll
