@@ -26,8 +26,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGapCtas = 4;              // that share an expert's gap rows
 
-// Alignment-gap rows to zero, by the first CTAs of the grid.
+// Alignment-gap rows to zero, by the first CTAs of the grid.  A layout of more rows than there
+// are has no slots, and its gaps are not touched either, as by the permutes.
 __device__ __forceinline__ void zero_gaps(const CombineBackwardArgs& a) {
+  if (a.expert_offset[a.num_experts] > a.capacity) return;
   const int e = static_cast<int>(blockIdx.x) / kGapCtas;
   const int64_t end = min64(a.expert_offset[e + 1], a.capacity);
   int64_t r = max64(0, static_cast<int64_t>(a.expert_offset[e]) + a.expert_count[e]) + blockIdx.x % kGapCtas;

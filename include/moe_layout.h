@@ -460,7 +460,8 @@ MOE_API int moe_gate_forward_grouped(const moe_layout_desc* desc, const moe_gate
  * in fp32, in an order that does not change from run to run; dweights of a masked
  * slot is 0.  dweights may be NULL, and expert_out with it.  With zero_pad != 0 the
  * alignment-gap rows of dy are set to zero (expert_offset and expert_count as written by
- * the layout; NULL allowed otherwise); rows past the last segment are not written.
+ * the layout; NULL allowed otherwise) unless expert_offset[E] > capacity_rows, a layout
+ * that did not fit; rows past the last segment are not written.
  *   dout bf16 [N, hidden], expert_out and dy bf16 [capacity_rows, hidden]; hidden a
  *   positive multiple of 8; 16-byte aligned.  dy may be expert_out itself (written in
  *   place); other overlaps are refused.  Slots >= capacity_rows are skipped (their
