@@ -71,8 +71,10 @@ bool touch(const void* x, int64_t x_bytes, const void* y, int64_t y_bytes, bool 
   return a < b + static_cast<uintptr_t>(y_bytes) && b < a + static_cast<uintptr_t>(x_bytes);
 }
 
+// eps: squares that vanish in fp32 (below 2^-149) are nothing beside 2^-126, and 2^88 is nothing
+// beside a mean of squares whose sum overflows.
 int check_norm(const moe_norm_desc* d) {
-  if (d == nullptr || !(d->eps > 0.0f) || !(d->eps <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (d == nullptr || !(d->eps >= 0x1p-126f) || !(d->eps <= 0x1p88f)) return MOE_ERR_INVALID_ARG;
   if (int st = check_rows(d->rows, d->cols, 16)) return st;
   return d->cols > MOE_MAX_NORM_COLS ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? kShortThreads : MAXT, NV <= 4 ? 4
   }
   sum = row_sum<CTA_ROW>(sum, part);
   float r = 1.0f / sqrtf(sum / static_cast<float>(cols) + a.eps);
-  if (!(sum < INFINITY)) {               // squares beyond fp32: eps is nothing beside them
+  if (!(sum < INFINITY)) {               // squares beyond fp32: eps, at most 2^88, is nothing beside a mean from 2^113 on
     sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {

@@ -477,7 +477,7 @@ MOE_API int moe_combine_backward(const moe_layout_desc* desc, const void* dout, 
 typedef struct moe_norm_desc {
   int64_t rows;          /* rows >= 0                                                      */
   int64_t cols;          /* a positive multiple of 16, at most MOE_MAX_NORM_COLS           */
-  float eps;             /* > 0                                                            */
+  float eps;             /* 2^-126 .. 2^88: beside others what fp32 loses of squares counts */
   int32_t stream_fp32;   /* residual stream (residual, residual_out, z, dz): 0 bf16, 1 fp32 */
   int32_t weight_fp32;   /* weight: 0 bf16, 1 fp32                                         */
 } moe_norm_desc;
