@@ -204,13 +204,15 @@ def _nbytes(t: torch.Tensor) -> int:
     return t.numel() * t.element_size()
 
 
-def _dev(t: torch.Tensor | None, name: str, dtype=None, numel=None, allow_none=False, nbytes=None):
+def _dev(t: torch.Tensor | None, name: str, dtype=None, numel=None, allow_none=False, nbytes=None, device=None):
     if t is None:
         if allow_none:
             return None
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -222,21 +224,25 @@ def _dev(t: torch.Tensor | None, name: str, dtype=None, numel=None, allow_none=F
     return t.data_ptr()
 
 
-def _like(t, shape, name, dtype):
-    """Pointer of a contiguous device tensor of exactly this shape and type, or None."""
+def _like(t, shape, name, dtype, device):
+    """Pointer of a contiguous tensor of exactly this shape and type on the device, or None."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
         return t.data_ptr()
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return _dev(t, name, dtype)
+    return _dev(t, name, dtype, device=device)
 
 
-def _here(t, name) -> None:
-    """A kernel runs on the current device: its tensors must lie there."""
-    if t.is_cuda and _current_device is not None and t.get_device() != _current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+def _here(t, name) -> int:
+    """The current device, on which a kernel runs: ``t`` must lie there, and all the call's other tensors."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    current = torch.cuda.current_device() if _current_device is None else _current_device()
+    if t.get_device() != current:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{current}")
+    return current
 
 
 def workspace_bytes(desc) -> int:
@@ -414,18 +420,18 @@ def combine_backward(desc, dout, dst_slot, weights, dy, workspace, expert_out=No
     shape = dy.shape
     if len(shape) != 2:
         raise ValueError("dy must be [capacity, H]")
-    _here(dy, "dy")
     cap, H = shape
     if dweights is not None and expert_out is None:
         raise ValueError("dweights needs expert_out")
+    here = _here(dy, "dy")
     st = load_library().moe_combine_backward(
-        _desc_ref(N, K, E, int(desc.num_ranks), int(desc.alignment)), _like(dout, (N, H), "dout", torch.bfloat16), H,
-        _dev(dst_slot, "dst_slot", torch.int32, N * K), _dev(weights, "weights", torch.float32, N * K),
-        _like(expert_out, shape, "expert_out", torch.bfloat16), _like(dy, shape, "dy", torch.bfloat16), cap,
-        _dev(dweights, "dweights", torch.float32, N * K, allow_none=True),
-        _dev(expert_offset, "expert_offset", torch.int32, E + 1, allow_none=not zero_pad),
-        _dev(expert_count, "expert_count", torch.int32, E, allow_none=not zero_pad), 1 if zero_pad else 0,
-        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+        _desc_ref(N, K, E, int(desc.num_ranks), int(desc.alignment)), _like(dout, (N, H), "dout", torch.bfloat16, here), H,
+        _dev(dst_slot, "dst_slot", torch.int32, N * K, device=here), _dev(weights, "weights", torch.float32, N * K, device=here),
+        _like(expert_out, shape, "expert_out", torch.bfloat16, here), _like(dy, shape, "dy", torch.bfloat16, here), cap,
+        _dev(dweights, "dweights", torch.float32, N * K, allow_none=True, device=here),
+        _dev(expert_offset, "expert_offset", torch.int32, E + 1, allow_none=not zero_pad, device=here),
+        _dev(expert_count, "expert_count", torch.int32, E, allow_none=not zero_pad, device=here), 1 if zero_pad else 0,
+        _dev(workspace, "workspace", torch.uint8, device=here), workspace.numel(), _stream(stream))
     _check(st, "moe_combine_backward")
 
 
@@ -678,8 +684,6 @@ def _norm_types(stream, weight, cols):
     return stream is torch.float32, weight.dtype is torch.float32
 
 
-
-
 def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, residual_out=None, rstd=None, eps=1e-6, total_rows=None,
              col_major=False, stream=None) -> None:
     """z = x + residual (kept in ``residual_out``, which may be ``residual``), normed by its root mean square and
@@ -691,12 +695,12 @@ def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, residual_out=Non
     shape = x.shape
     if len(shape) != 2:
         raise ValueError("x must be [rows, cols]")
-    _here(x, "x")
     rows, cols = shape
     if (residual is None) != (residual_out is None):
         raise ValueError("residual and residual_out go together")
     if (q is None) != (sf is None):
         raise ValueError("q and sf go together")
+    here = _here(x, "x")
     kind = torch.bfloat16 if residual is None else residual.dtype
     fp32, weight_fp32 = _norm_types(kind, weight, cols)
     ld, scales = 0, None
@@ -706,12 +710,12 @@ def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, residual_out=Non
             ld = _sf_ld(sf, rows, scales[1])
             scales = (scales[1], ld)
     st = load_library().moe_rms_norm(
-        _norm_desc(rows, cols, eps, fp32, weight_fp32), _like(x, shape, "x", torch.bfloat16),
-        _like(residual, shape, "residual", kind), _like(weight, weight.shape, "weight", weight.dtype),
-        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True),
-        _like(residual_out, shape, "residual_out", kind), _like(y, shape, "y", torch.bfloat16),
-        _like(q, shape, "q", torch.float8_e4m3fn), _like(sf, scales, "sf", torch.float32), ld,
-        _like(rstd, (rows,), "rstd", torch.float32), _stream(stream))
+        _norm_desc(rows, cols, eps, fp32, weight_fp32), _like(x, shape, "x", torch.bfloat16, here),
+        _like(residual, shape, "residual", kind, here), _like(weight, weight.shape, "weight", weight.dtype, here),
+        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True, device=here),
+        _like(residual_out, shape, "residual_out", kind, here), _like(y, shape, "y", torch.bfloat16, here),
+        _like(q, shape, "q", torch.float8_e4m3fn, here), _like(sf, scales, "sf", torch.float32, here), ld,
+        _like(rstd, (rows,), "rstd", torch.float32, here), _stream(stream))
     if st:
         _check(st, "moe_rms_norm")
 
@@ -732,18 +736,18 @@ def rms_norm_backward(dy, z, rstd, weight, dz, dresidual=None, dx=None, dweight=
     shape, kind = dy.shape, z.dtype
     if len(shape) != 2:
         raise ValueError("dy must be [rows, cols]")
-    _here(dy, "dy")
     rows, cols = shape
     fp32, weight_fp32 = _norm_types(kind, weight, cols)
     if dweight is not None and workspace is None:
         raise ValueError("dweight needs a workspace")
+    here = _here(dy, "dy")
     st = load_library().moe_rms_norm_backward(
-        _norm_desc(rows, cols, 1.0, fp32, weight_fp32), _like(dy, shape, "dy", torch.bfloat16), _like(z, shape, "z", kind),
-        _like(rstd, (rows,), "rstd", torch.float32), _like(weight, weight.shape, "weight", weight.dtype),
-        _like(dresidual, shape, "dresidual", kind),
-        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True), _like(dz, shape, "dz", kind),
-        _like(dx, shape, "dx", torch.bfloat16), _like(dweight, (cols,), "dweight", torch.float32), int(bool(accumulate)),
-        _dev(workspace, "workspace", torch.uint8, allow_none=True), 0 if workspace is None else workspace.numel(),
+        _norm_desc(rows, cols, 1.0, fp32, weight_fp32), _like(dy, shape, "dy", torch.bfloat16, here), _like(z, shape, "z", kind, here),
+        _like(rstd, (rows,), "rstd", torch.float32, here), _like(weight, weight.shape, "weight", weight.dtype, here),
+        _like(dresidual, shape, "dresidual", kind, here),
+        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True, device=here), _like(dz, shape, "dz", kind, here),
+        _like(dx, shape, "dx", torch.bfloat16, here), _like(dweight, (cols,), "dweight", torch.float32, here), int(bool(accumulate)),
+        _dev(workspace, "workspace", torch.uint8, allow_none=True, device=here), 0 if workspace is None else workspace.numel(),
         _stream(stream))
     _check(st, "moe_rms_norm_backward")
 
