@@ -332,7 +332,7 @@ Shape shape_of(int64_t cols, bool backward) {
   return {nv, threads <= 256 ? 256 : 512, threads};
 }
 
-template <typename F>
+template <bool BACKWARD, typename F>
 cudaError_t with_shape(const Shape& s, bool fp32, F run) {
 #define MOE_NORM_CASE(NV, MAXT) \
   if (s.nv == NV && s.max_threads == MAXT) return fp32 ? run.template operator()<NV, MAXT, true>() : run.template operator()<NV, MAXT, false>();
@@ -341,8 +341,11 @@ cudaError_t with_shape(const Shape& s, bool fp32, F run) {
   MOE_NORM_CASE(4, 32)
   MOE_NORM_CASE(2, 256)
   MOE_NORM_CASE(4, 256)
-  MOE_NORM_CASE(4, 512)
-  MOE_NORM_CASE(8, 256)
+  if constexpr (BACKWARD) {
+    MOE_NORM_CASE(4, 512)
+  } else {
+    MOE_NORM_CASE(8, 256)
+  }
   MOE_NORM_CASE(8, 512)
 #undef MOE_NORM_CASE
   return cudaErrorInvalidValue;
@@ -388,7 +391,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
   const Shape s = shape_of(a.cols, false);
   count_launch();
-  return with_shape(s, a.stream_fp32, Forward{a, s, stream});
+  return with_shape<false>(s, a.stream_fp32, Forward{a, s, stream});
 }
 
 int64_t norm_parts(int64_t cols) { return 160 * max64(1, 1024 / shape_of(cols, true).threads); }
@@ -397,7 +400,7 @@ int64_t norm_parts(int64_t cols) { return 160 * max64(1, 1024 / shape_of(cols, t
 cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream) {
   if (a.rows == 0 && a.dweight == nullptr) return cudaSuccess;
   const Shape s = shape_of(a.cols, true);
-  return with_shape(s, a.stream_fp32, Backward{a, s, stream});
+  return with_shape<true>(s, a.stream_fp32, Backward{a, s, stream});
 }
 
 }  // namespace moe
