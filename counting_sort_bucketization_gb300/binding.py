@@ -235,6 +235,13 @@ def _like(t, shape, name, dtype, device):
     return _dev(t, name, dtype, device=device)
 
 
+def _flat(t, name, dtype, numel, device, allow_none=False):
+    """``_dev`` of a tensor on the device, where nothing is amiss in as few looks as without it."""
+    if t is not None and t.dtype is dtype and t.numel() >= numel and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, dtype, numel, allow_none, device=device)
+
+
 def _here(t, name) -> int:
     """The current device, on which a kernel runs: ``t`` must lie there, and all the call's other tensors."""
     if not t.is_cuda:
@@ -426,12 +433,12 @@ def combine_backward(desc, dout, dst_slot, weights, dy, workspace, expert_out=No
     here = _here(dy, "dy")
     st = load_library().moe_combine_backward(
         _desc_ref(N, K, E, int(desc.num_ranks), int(desc.alignment)), _like(dout, (N, H), "dout", torch.bfloat16, here), H,
-        _dev(dst_slot, "dst_slot", torch.int32, N * K, device=here), _dev(weights, "weights", torch.float32, N * K, device=here),
+        _flat(dst_slot, "dst_slot", torch.int32, N * K, here), _flat(weights, "weights", torch.float32, N * K, here),
         _like(expert_out, shape, "expert_out", torch.bfloat16, here), _like(dy, shape, "dy", torch.bfloat16, here), cap,
-        _dev(dweights, "dweights", torch.float32, N * K, allow_none=True, device=here),
-        _dev(expert_offset, "expert_offset", torch.int32, E + 1, allow_none=not zero_pad, device=here),
-        _dev(expert_count, "expert_count", torch.int32, E, allow_none=not zero_pad, device=here), 1 if zero_pad else 0,
-        _dev(workspace, "workspace", torch.uint8, device=here), workspace.numel(), _stream(stream))
+        _flat(dweights, "dweights", torch.float32, N * K, here, True),
+        _flat(expert_offset, "expert_offset", torch.int32, E + 1, here, not zero_pad),
+        _flat(expert_count, "expert_count", torch.int32, E, here, not zero_pad), 1 if zero_pad else 0,
+        _flat(workspace, "workspace", torch.uint8, 0, here), workspace.numel(), _stream(stream))
     _check(st, "moe_combine_backward")
 
 
@@ -712,7 +719,7 @@ def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, residual_out=Non
     st = load_library().moe_rms_norm(
         _norm_desc(rows, cols, eps, fp32, weight_fp32), _like(x, shape, "x", torch.bfloat16, here),
         _like(residual, shape, "residual", kind, here), _like(weight, weight.shape, "weight", weight.dtype, here),
-        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True, device=here),
+        _flat(total_rows, "total_rows", torch.int32, 1, here, True),
         _like(residual_out, shape, "residual_out", kind, here), _like(y, shape, "y", torch.bfloat16, here),
         _like(q, shape, "q", torch.float8_e4m3fn, here), _like(sf, scales, "sf", torch.float32, here), ld,
         _like(rstd, (rows,), "rstd", torch.float32, here), _stream(stream))
@@ -745,9 +752,9 @@ def rms_norm_backward(dy, z, rstd, weight, dz, dresidual=None, dx=None, dweight=
         _norm_desc(rows, cols, 1.0, fp32, weight_fp32), _like(dy, shape, "dy", torch.bfloat16, here), _like(z, shape, "z", kind, here),
         _like(rstd, (rows,), "rstd", torch.float32, here), _like(weight, weight.shape, "weight", weight.dtype, here),
         _like(dresidual, shape, "dresidual", kind, here),
-        _dev(total_rows, "total_rows", torch.int32, 1, allow_none=True, device=here), _like(dz, shape, "dz", kind, here),
+        _flat(total_rows, "total_rows", torch.int32, 1, here, True), _like(dz, shape, "dz", kind, here),
         _like(dx, shape, "dx", torch.bfloat16, here), _like(dweight, (cols,), "dweight", torch.float32, here), int(bool(accumulate)),
-        _dev(workspace, "workspace", torch.uint8, allow_none=True, device=here), 0 if workspace is None else workspace.numel(),
+        _flat(workspace, "workspace", torch.uint8, 0, here, True), 0 if workspace is None else workspace.numel(),
         _stream(stream))
     _check(st, "moe_rms_norm_backward")
 
