@@ -443,7 +443,10 @@ typedef struct moe_gate_groups {
  *   ids, weights (of s, without the bias), counts and balance loss as in moe_gate_forward.
  * Keys are compared as numbers, not as what 32 bits make of them: what fp32 leaves open is
  * settled to about 2^-46 (scores below 2^-124 may count as zeros there).  Where all biases
- * are equal the order of the keys is that of the logits.
+ * are equal the order of experts, and of groups with group_sum 1, is that of the logits;
+ * sums of two are compared as sums of such keys: two that lie closer together than
+ * that, saturated sigmoids for instance, may count as equal, and equal ones of different
+ * scores (s(x) + s(-x) is 1 for every x) as different.
  * Tokens with a NaN or +inf among their logits or keys are not routed and record
  * MOE_ERR_INVALID_ARG.
  */
