@@ -180,7 +180,8 @@ int moe_combine_backward(const moe_layout_desc* desc, const void* dout, int64_t 
   if (desc->num_tokens > 0 && (dout == nullptr || dst_slot == nullptr || weights == nullptr ||
                                (dweights != nullptr && expert_out == nullptr && capacity_rows > 0)))
     return MOE_ERR_INVALID_ARG;
-  if (!aligned(dout, 16) || !aligned(expert_out, 16) || !aligned(dy, 16) || !aligned(weights, 4) || !aligned(dweights, 4))
+  if (!aligned(dout, 16) || !aligned(expert_out, 16) || !aligned(dy, 16) || !aligned(weights, 4) || !aligned(dweights, 4) ||
+      !aligned(dst_slot, 4) || !aligned(expert_offset, 4) || !aligned(expert_count, 4))
     return MOE_ERR_INVALID_ARG;
   const int64_t dense = 2 * hidden * desc->num_tokens, rows = 2 * hidden * capacity_rows;
   const int64_t pairs = 4 * desc->num_tokens * desc->topk;
@@ -188,6 +189,11 @@ int moe_combine_backward(const moe_layout_desc* desc, const void* dout, int64_t 
       touch(dy, rows, dst_slot, pairs, false) || touch(dweights, pairs, dout, dense, false) ||
       touch(dweights, pairs, expert_out, rows, false) || touch(dweights, pairs, dy, rows, false) ||
       touch(dweights, pairs, weights, pairs, false) || touch(dweights, pairs, dst_slot, pairs, false))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t E = desc->num_experts;
+  if (zero_pad != 0 && (touch(dy, rows, expert_offset, 4 * (E + 1), false) || touch(dy, rows, expert_count, 4 * E, false) ||
+                        touch(dweights, pairs, expert_offset, 4 * (E + 1), false) ||
+                        touch(dweights, pairs, expert_count, 4 * E, false)))
     return MOE_ERR_INVALID_ARG;
   CombineBackwardArgs a{};
   a.dout = static_cast<const uint16_t*>(dout);
