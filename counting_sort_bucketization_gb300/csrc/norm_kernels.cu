@@ -14,11 +14,17 @@
 // CTA a longer one.  Statistics are fp32 sums in a fixed order; each rounding to 16 or 8 bits is
 // the one that the output's type asks for.
 //
-// HBM bound: 9 bytes a value (bf16 stream, both outputs), the gradient 8.  32768 x 7168 in 307
-// us, 6.9 TB/s of the 6.8 that a copy reaches; 32768 x 4096 182, fp32 stream 254 (6.9); 16384 x
-// 16384 379 (6.4).  The gradient with the weight's, 32768 x 4096 176 us (6.1), x 7168 338 (5.6),
-// 16384 x 16384 387 (5.5): the weight's sums take the registers of the warps that would
-// fill its phases.  64 x 7168: 8 us a call, of which the host takes 7.
+// HBM bound: 9 bytes a value (bf16 stream, both outputs), the gradient 8.  One call after another:
+//   32768 x 4096   178 us, 6.8 TB/s (a copy's rate); stream in fp32 250, 7.0
+//   32768 x 7168   305, 7.0;  508, 6.0          16384 x 16384  367, 6.6;  766, 4.6
+//   8192 x 32768   394, 6.2;  770, 4.5
+// the gradient with the weight's
+//   32768 x 4096   176, 6.1;  284, 6.6          32768 x 7168   331, 5.7;  603, 5.5
+//   16384 x 16384  375, 5.7;  730, 5.2          8192 x 32768   592, 3.6; 1410, 2.7
+// The weight's sums take the registers of the warps that would fill the gradient's phases.  Past
+// 8192 columns (the gradient: 16384) a thread has eight vectors, which in fp32 leave one CTA
+// an SM; past 16384 they no longer fit its registers in fp32 (176 bytes of spills a thread), nor
+// in the gradient (488, fp32 740).  64 x 7168: 8 us a call, of which the host takes 7.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -107,9 +113,9 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 }
 
 // MAXT: threads of a row at most; 32: each warp of a CTA has a row.  A CTA a row (or eight):
-// a wave of CTAs that walk the rows, with the next row's copies under way, took 183 us in
-// place of 182 on 32768 x 4096, 330 in place of 254 with the stream in fp32: SMs are not
-// equally fast, and the block scheduler evens that out.
+// a wave of CTAs that walk the rows, with the next row's copies under way, took 200 us in
+// place of 182 on 32768 x 4096, 330 in place of 254 with the stream in fp32 (L2 flushed): SMs are
+// not equally fast, and the block scheduler evens that out.
 template <int NV, int MAXT, bool FP32>
 __global__ void __launch_bounds__(MAXT == 32 ? kShortThreads : MAXT, NV <= 4 ? 4 : 1) norm_kernel(NormArgs a) {
   constexpr bool CTA_ROW = MAXT > 32;
@@ -200,11 +206,11 @@ __global__ void __launch_bounds__(MAXT == 32 ? kShortThreads : MAXT, NV <= 4 ? 4
 
 // A CTA walks a share of the rows; a thread keeps its columns' part of the weight's gradient
 // over them, and the CTAs' parts are added by the kernel below.  Shares are fixed, so the
-// sums are.  (32768 x 4096: 184 us; two shares for each CTA that fits, so that SMs that are
-// ahead take more, 191, four 203: their parts cost more than they even out.)
+// sums are.  (32768 x 4096, L2 flushed: 184 us; two shares for each CTA that fits, so that SMs
+// that are ahead take more, 191, four 203: their parts cost more than they even out.)
 //
-// CTAs an SM: what is in flight counts, so many with few registers: 32768 x 4096 with four
-// 184 us, three 190, two 221; the stream in fp32 spills with four (383, 342 with three).
+// CTAs an SM: what is in flight counts, so many with few registers: the same with four 184 us,
+// three 190, two 221; the stream in fp32 spills with four (383, 342 with three).
 template <int NV, int MAXT, bool FP32>
 __global__ void __launch_bounds__(MAXT == 32 ? kShortThreads : MAXT,
                                   NV == 1 ? 4 : NV == 2 ? (MAXT == 256 && !FP32 ? 4 : 3) : MAXT <= 256 ? 2 : 1)
@@ -318,7 +324,7 @@ __global__ void __launch_bounds__(kSumThreads) norm_weight_kernel(const float* p
 
 // Vectors of a thread and threads of a row.  A warp has up to 1024 columns, a CTA two
 // vectors a thread up to 4096, four up to 8192, then eight; the gradient, which holds more,
-// four and twice the threads up to 16384 (385 us in place of 559 on 16384 x 16384).
+// four and twice the threads up to 16384 (375 us; eight vectors took 559 on 16384 x 16384).
 struct Shape {
   int nv;
   int max_threads;

@@ -13,7 +13,7 @@
 // thousand) is done again with keys of two floats after the loop over the tokens: one that
 // has its candidates listed from those (exact_rank, about 1 us), others from all experts
 // (exact_picks, about 8).  Calls within the loop cost all tokens registers (131072 x 384 in 16
-// groups 194 us, 168 without them).  Equal logits with equal biases tie exactly, experts and
+// groups 194 us, 168 without them, when both were tried).  Equal logits with equal biases tie exactly, experts and
 // groups whose largest keys are such, and where no bias differs from another the order of the
 // logits is that of the keys; none of these is left open.
 //
@@ -22,13 +22,19 @@
 // come from registers and shuffles (else 32 / G lanes a group walk its keys in shared
 // memory).  Candidates are the keys from a bound on: what the token before had as its K-th
 // key, a little lower; or, if fewer than K or more than 32 reach that, the K-th largest of the
-// lanes' two largest.  The bound changes the work, not the result.
+// lanes' two largest.  The bound changes the work, not the result.  It stays above -inf, the
+// key of closed experts and of columns past E, which are never listed.  Where more than 32 keys
+// reach it still (equal ones, K near 32, groups that few lanes hold) they are picked one after
+// the other: 131072 x 128, top-32, 606 us, and 131072 x 1024, one group of 16, top-8, 515.
 //
-// 131072 x 384, sigmoid with bias, top-8: 135 us, in 16 groups of which 4 stay 172 (256 experts
-// in 8 groups 156); the logits once are 201 MB, 30 us.  It is bound by its instructions, 780 a
-// token (in 16 groups 960; 128 experts 620, so most do not depend on their number; 440 are the
-// choice and the weights), and their chain (ncu: issue slots 56 % busy, ALU 58 %, DRAM 16 %).
-// 64 x 256 in 8 groups: 8.8 us a call, the launch and one token's chain.
+// 131072 x 384, sigmoid with bias, top-8, the L2 flushed: 137 us, in 16 groups of which 4 stay
+// 174 (256 experts in 8 groups 156); the logits once are 201 MB, 30 us.  A token takes 780
+// instructions (in 16 groups 970; 128 experts 640, so most do not depend on their number; 440
+// are the choice and the weights), which is 100 us of issue slots; the rest is their chain, a
+// warp at a time, with 24 warps an SM (ncu: issue slots 56 % busy, ALU 58 %, DRAM 16 %).  Half a
+// warp a token has two chains a warp and took 158 in place of 188 when it was tried, with 4 us
+// more for 64 tokens and twice the code.  64 x 256 in 8 groups: 8.9 us a call, the launch and one
+// token's chain.  Rows of zeros (padding): 369 us for 131072 x 384 in 16 groups.
 #include <cfloat>
 
 #include "gate_common.cuh"
@@ -49,7 +55,9 @@ constexpr float kErrSoftmax = (V + 48) * 0x1p-24f;
 
 // Numbers as sums of two floats, good to about 2^-46: hi is the sum rounded, lo the rest.
 // (The 64-bit unit does 2 multiply-adds a cycle and SM; a token redone with it took 40 us.)
-// Intrinsics, so that no addition is fused with a product.
+// Knuth's sum of two numbers with its error, Dekker's where the first is the larger, and his
+// product with the error by one fused multiply-add.  Intrinsics, so that no addition is fused
+// with a product.
 struct Two {
   float hi, lo;
 };
@@ -76,7 +84,8 @@ __device__ __forceinline__ Two reciprocal(Two d) {
   return quick_sum(q, __fmul_rn(rest, q));
 }
 // e^x, x <= 0: x = n ln 2 + r, the Taylor series of e^r (its terms from r^7 on need one float),
-// times 2^n.  ln 2 comes in three parts, of which n times the first two is exact.  Below
+// times 2^n.  ln 2 comes in three parts, of which n times the first two is exact (Cody and
+// Waite's reduction).  Below
 // 2^-125 zero.
 __device__ __forceinline__ Two two_exp(Two x) {
   if (!(x.hi > -86.0f)) return {0.0f, 0.0f};
