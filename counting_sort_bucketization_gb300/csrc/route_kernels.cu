@@ -659,11 +659,15 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
           __syncwarp();
           if (lane < found) list_k[before] = k, list_id[before] = id;
           __syncwarp();
-          if (biased && lane < found && before < K) {
-            if (before == K - 1) exact = beyond = near(k, edge);
-            if (before + 1 < found && near(k, list_k[before + 1])) {
-              const int other = list_id[before + 1];
-              exact |= load_logit(row + other) != l || bias_s[other] != bias;
+          // A pick is compared with the next one, and every key behind the picks with the last of them: where
+          // neither is near, or is the same logit and bias, the order is that of the numbers.
+          if (biased && lane < found) {
+            const int mate = before < K - 1 ? before + 1 : K - 1;
+            if (before == K - 1) {
+              exact = beyond = near(k, edge);
+            } else if (mate < found && near(k, list_k[mate])) {
+              const int other = list_id[mate];
+              exact = load_logit(row + other) != l || bias_s[other] != bias;
             }
           }
           // The next token's guess.  A key may be the type's lowest value.  What a row whose K-th key is a mask leaves
@@ -680,11 +684,11 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
             slot = before;
           }
         } else {
-          // More than a list holds: one pick after the other, and one more to look behind the last.
+          // More than a list holds: one pick after the other, each near no other number, nor what is left the last.
           const float first = unsortable(top);
           float last_key = first, last_l = 0.0f, last_b = 0.0f;
           float h;
-          for (int k = 0; k <= K && top > kKeyNegInf; ++k) {
+          for (int k = 0; k < K && top > kKeyNegInf; ++k) {
             const float want = unsortable(top);
             unsigned lowest = kFull;
             if (!BLOCKED || held)
@@ -699,7 +703,7 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
               slack = fminf(fmaxf(few ? 2.0f * slack : 0.0f, 0x1p-4f * (first - want) + 0x1p-8f * fabsf(want)), FLT_MAX);
               guess = fmaxf(want - slack, -FLT_MAX);
             }
-            if (lane == k && k < K) mine = id, picked = lk, score = SIGMOID ? sigmoid(lk) : exp_neg(lk - m) * inv;
+            if (lane == k) mine = id, picked = lk, score = SIGMOID ? sigmoid(lk) : exp_neg(lk - m) * inv;
             h = -INFINITY;
             if (!BLOCKED || held)
 #pragma unroll
@@ -709,6 +713,13 @@ __global__ void __launch_bounds__(kGateThreads, V <= 4 ? 4 : V <= 12 ? 3 : 2) ro
               }
             top = __reduce_max_sync(kFull, sortable(h + 0.0f));
           }
+          if (biased && top > kKeyNegInf && (!BLOCKED || held))
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (key[i] > -INFINITY && near(key[i], last_key)) {
+                const int col = route_column<V, BLOCKED>(lane, i);
+                exact |= load_logit(row + col) != last_l || bias_s[col] != last_b;
+              }
         }
         __syncwarp();                    // the list is read
         exact = __any_sync(kFull, exact);
