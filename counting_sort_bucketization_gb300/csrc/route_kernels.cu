@@ -25,16 +25,16 @@
 // lanes' two largest.  The bound changes the work, not the result.  It stays above -inf, the
 // key of closed experts and of columns past E, which are never listed.  Where more than 32 keys
 // reach it still (equal ones, K near 32, groups that few lanes hold) they are picked one after
-// the other: 131072 x 128, top-32, 606 us, and 131072 x 1024, one group of 16, top-8, 515.
+// the other: 131072 x 128, top-32, 645 us, and 131072 x 1024, one group of 16, top-8, 564.
 //
 // 131072 x 384, sigmoid with bias, top-8, the L2 flushed: 137 us, in 16 groups of which 4 stay
-// 174 (256 experts in 8 groups 156); the logits once are 201 MB, 30 us.  A token takes 780
-// instructions (in 16 groups 970; 128 experts 640, so most do not depend on their number; 440
-// are the choice and the weights), which is 100 us of issue slots; the rest is their chain, a
-// warp at a time, with 24 warps an SM (ncu: issue slots 56 % busy, ALU 58 %, DRAM 16 %).  Half a
+// 175 (256 experts in 8 groups 158); the logits once are 201 MB, 30 us.  A token takes 780
+// instructions (128 experts 645, so most do not depend on their number; 440 are the choice and
+// the weights), in 16 groups 960, which is 100 us of issue slots; the rest is their chain, with
+// 24 warps an SM (ncu: issue slots 56 % busy, ALU 58 %, DRAM 16 %).  Half a
 // warp a token has two chains a warp and took 158 in place of 188 when it was tried, with 4 us
 // more for 64 tokens and twice the code.  64 x 256 in 8 groups: 8.9 us a call, the launch and one
-// token's chain.  Rows of zeros (padding): 369 us for 131072 x 384 in 16 groups.
+// token's chain.  Rows of zeros (padding): 351 us for 131072 x 384 in 16 groups.
 #include <cfloat>
 
 #include "gate_common.cuh"
